@@ -1,0 +1,798 @@
+// linear_ce.cu -- output layer and softmax cross entropy without keeping the
+// logits, and its gradients.
+//
+//   z = x W^T      lse_t = log sum_v exp z_tv      loss_t = lse_t - z_t,label
+//   dz = dloss_t (exp(z - lse_t) - [v = label])    dx = dz W      dW = dz^T x
+//
+// Four matrix products on the tensor cores, all of them the one kernel below:
+//   scores   x W^T, whose epilogue leaves one (max, sum) pair per row and
+//            256 vocabulary entries; a small kernel joins the pairs
+//   dz       x W^T again for a piece of the vocabulary, whose epilogue writes
+//            dz of the piece in bf16 (for fp32 gradients as the sum of two
+//            bf16 numbers, so that both products keep fp32's accuracy)
+//   dx       dz W, added up over the pieces
+//   dW       dz^T x, the piece's rows
+// Sums are fp32 in tensor memory, softmax statistics fp32.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "lm_common.cuh"
+#include "lm_internal.h"
+
+namespace rcc {
+namespace lm {
+namespace {
+
+// ---- PTX ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// the same shared-memory address in block `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_addr(uint32_t at, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+// `bar` is an address of any block of the cluster.  Relaxed: the arrival
+// publishes nothing of this thread's, only the bytes the copies will bring.
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                   bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Waits for a phase, at most about two seconds; false when that ran out.
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
+    if (bar_try(bar, parity)) return true;
+  } while (clock64() - t0 < kWaitCycles);
+  return false;
+}
+
+// One box of a two-dimensional tensor map into this block's shared memory;
+// the bytes count on `bar`, which with CG = 2 is the pair's first block's.
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    bool accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+}
+// Arrives on `bar` (in every block of the pair) once all products issued so
+// far are done.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar), "h"((uint16_t)3) : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     bar) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 32 columns of this thread's row
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  __syncwarp();  // the whole warp loads
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---- the product -------------------------------------------------------------------
+
+constexpr int kBM = 128;   // rows of C of one block
+constexpr int kBN = 256;   // columns of C of one block (of a pair: the same)
+constexpr int kBK = 64;    // of the sum per stage: 128 bytes, one swizzle row
+constexpr int kRowBytes = kBK * 2;
+constexpr int kEpiWarps = 4;
+constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
+constexpr int kTmemCols = 512;  // two accumulators of kBN columns
+
+enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
+
+struct GemmArgs {
+  CUtensorMap a[2], b;   // a[1]: the second bf16 number of A's values
+  int m, n;              // of C
+  int m_tiles, n_tiles;  // of kBM * CG rows, of kBN columns
+  int k_blocks, splits;  // of kBK; pieces of the sum, each with a C of its own
+  int group;             // tiles of rows that share a run over the columns
+  int b_row0;            // first row of B (vocabulary entry) of this piece
+  int a_x0, b_y0;        // offsets of the maps' coordinates
+  // stats
+  float2* part;          // [n_tiles][m]
+  float* zlab;           // [m]
+  const void* labels;
+  int labels64;
+  int vocab;
+  // dz
+  const float* lse;
+  const float* dloss;
+  __nv_bfloat16* dz[2];  // [m][ld_dz], the second one NULL for bf16 gradients
+  size_t ld_dz;
+  // out
+  void* c;
+  size_t ld_c, split_stride;  // elements
+  int c_type;
+  int add;               // C += instead of C =
+};
+
+// Shared-memory descriptor of a tile in rows of 128 bytes, swizzled by 128.
+// Along the sum (K major): a row holds 64 of the sum, eight rows are 1,024
+// bytes.  Across it (MN major): a row holds 64 rows of the matrix, eight of
+// the sum are 1,024 bytes, and 64 rows of the matrix a block of 8,192.
+template <bool MN>
+__device__ __forceinline__ uint64_t smem_desc(uint32_t at) {
+  uint64_t d = (uint64_t)((at >> 4) & 0x3FFF);
+  d |= (uint64_t)(MN ? (kBK * 128) >> 4 : 1) << 16;  // between blocks of 64 rows
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+template <int CG, int PARTS>
+struct Stage {
+  static constexpr int kBRows = kBN / CG;  // columns of C whose B this block holds
+  static constexpr int kABytes = kBM * kRowBytes;
+  static constexpr int kBBytes = kBRows * kRowBytes;
+  static constexpr int kBytes = PARTS * kABytes + kBBytes;
+  static constexpr int kCount = (200 * 1024) / kBytes;
+  static constexpr int kShared = kCount * kBytes + 1024 + 256;
+};
+
+struct Tile {
+  int m, n, k0, k1, split;
+};
+__device__ __forceinline__ Tile tile_of(const GemmArgs& g, int t) {
+  Tile r;
+  const int plane = g.m_tiles * g.n_tiles;
+  r.split = t / plane;
+  t -= r.split * plane;
+  const int band = g.group * g.n_tiles;
+  const int m0 = t / band * g.group;
+  t -= m0 * g.n_tiles;
+  const int rows = min(g.group, g.m_tiles - m0);
+  r.m = m0 + t % rows;
+  r.n = t / rows;
+  r.k0 = (int)((long long)g.k_blocks * r.split / g.splits);
+  r.k1 = (int)((long long)g.k_blocks * (r.split + 1) / g.splits);
+  return r;
+}
+
+constexpr float kLog2e = 1.44269504f;
+
+// A row's 256 scores: the running (max, sum of exp) of the columns that exist.
+__device__ __forceinline__ void epilogue_stats(const GemmArgs& g, uint32_t acc, int row, int col0,
+                                               bool failed) {
+  const bool live = row < g.m;
+  const int64_t label = live ? load_id(g.labels, g.labels64, row, g.vocab) : -1;
+  const float nan = __uint_as_float(0x7FC00000u);
+  float top = -INFINITY, sum = 0.f;
+  for (int c = 0; c < kBN; c += 32) {
+    const int left = g.n - (col0 + c);
+    if (left <= 0) break;
+    float v[32];
+    tmem_load32(acc + c, v);
+    if (left < 32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i >= left) v[i] = -INFINITY;
+    }
+    const int64_t at = label - (col0 + c);
+    if (at >= 0 && at < 32) {
+      float z = v[0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) z = i == at ? v[i] : z;
+      g.zlab[row] = failed ? nan : z;
+    }
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
+    m = fmaxf(top, m);
+    const float ml = m * kLog2e;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += exp2f(fmaf(v[i], kLog2e, -ml));
+    // nothing before the first columns: top is -inf there and sum 0
+    sum = c == 0 ? s : fmaf(sum, exp2f(fmaf(top, kLog2e, -ml)), s);
+    top = m;
+  }
+  if (live)
+    g.part[(size_t)(col0 / kBN) * g.m + row] = failed ? make_float2(nan, nan) : make_float2(top, sum);
+}
+
+// dz of a row's 256 columns; columns past the piece are not written.
+__device__ __forceinline__ void epilogue_dz(const GemmArgs& g, uint32_t acc, int row, int col0,
+                                            bool failed) {
+  const bool live = row < g.m;
+  const int64_t label = live ? load_id(g.labels, g.labels64, row, g.vocab) : -1;
+  const float lse = live ? g.lse[row] : 0.f;
+  const float f = label >= 0 ? g.dloss[row] : 0.f;
+  const float ll = lse * kLog2e;
+  for (int c = 0; c < kBN; c += 32) {
+    const int left = g.n - (col0 + c);
+    if (left <= 0) break;
+    float v[32];
+    tmem_load32(acc + c, v);
+    const int64_t at = label - (g.b_row0 + col0 + c);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float p = exp2f(fmaf(v[i], kLog2e, -ll));
+      v[i] = label < 0 ? 0.f : f * (i == at ? p - 1.f : p);
+      if (failed) v[i] = __uint_as_float(0x7FC00000u);
+    }
+    if (!live) continue;
+    // ld_dz is a multiple of 64, so that whole vectors stay inside the row
+    for (int part = 0; part < 2; ++part) {
+      if (!g.dz[part]) break;
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+      uint4* out = reinterpret_cast<uint4*>(g.dz[part] + (size_t)row * g.ld_dz + col0 + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (8 * i < left) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        widen2(w[i], lo, hi);
+        v[2 * i] -= lo;
+        v[2 * i + 1] -= hi;
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void epilogue_out(const GemmArgs& g, uint32_t acc, int row, int col0,
+                                             int split, bool failed) {
+  T* c0 = static_cast<T*>(g.c) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
+  for (int c = 0; c < kBN; c += 32) {
+    const int left = g.n - (col0 + c);
+    if (left <= 0) break;
+    float v[32];
+    tmem_load32(acc + c, v);
+    if (row >= g.m) continue;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      if (i >= left) break;  // n is a multiple of 8
+      float o[8];
+      if (g.add) {
+        load8(c0 + c + i, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o[e] += v[i + e];
+        if (failed) o[e] = __uint_as_float(0x7FC00000u);
+      }
+      store8(c0 + c + i, o);
+    }
+  }
+}
+
+// C = A B^T tile by tile, one block (CG = 1) or a pair of blocks on two SMs
+// (CG = 2) per tile, every block or pair taking tiles in turn.  Warp 0 fills
+// the stages by TMA, warp 1 issues the products, the last warps take the
+// finished accumulator out of tensor memory while the next one is summed.
+template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+  using S = Stage<CG, PARTS>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t bars = base + S::kCount * S::kBytes;
+  const uint32_t full = bars, empty = bars + 8 * S::kCount;
+  const uint32_t acc_full = empty + 8 * S::kCount, acc_empty = acc_full + 16;
+  const uint32_t tmem_slot = acc_empty + 16;
+  static_assert(16 * S::kCount + 36 <= 256, "barriers");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cta_rank() : 0;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int tiles = g.m_tiles * g.n_tiles * g.splits;
+
+  if (tid == 0) {
+    for (int s = 0; s < S::kCount; ++s) {
+      bar_init(full + 8 * s, CG);
+      bar_init(empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(acc_full + 8 * s, 1);
+      bar_init(acc_empty + 8 * s, CG * kEpiWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) tmem_alloc<CG>(tmem_slot, kTmemCols);
+  tmem_fence_before();
+  if constexpr (CG == 2) cluster_sync();
+  __syncthreads();
+  tmem_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+  pdl_wait_then_release();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // what earlier kernels wrote by ordinary stores, before copies by TMA
+      asm volatile("fence.proxy.async;" ::: "memory");
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const Tile tile = tile_of(g, t);
+        const int m0 = (tile.m * CG + (int)rank) * kBM;
+        const int n0 = tile.n * kBN + (int)rank * S::kBRows;
+        for (int k = tile.k0; k < tile.k1; ++k) {
+          if (!(ok = bar_wait(empty + 8 * s, phase ^ 1))) break;
+          const uint32_t at = base + s * S::kBytes;
+          const uint32_t bar = CG == 2 ? peer_addr(full + 8 * s, 0) : full + 8 * s;
+          bar_expect(bar, S::kBytes);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            const uint32_t to = at + p * S::kABytes;
+            if constexpr (A_MN) {
+#pragma unroll
+              for (int j = 0; j < kBM / 64; ++j)
+                tma_load<CG>(to + j * kBK * 128, &g.a[p], m0 + 64 * j, k * kBK, bar);
+            } else {
+              tma_load<CG>(to, &g.a[p], k * kBK, m0, bar);
+            }
+          }
+          const uint32_t to = at + PARTS * S::kABytes;
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int j = 0; j < S::kBRows / 64; ++j)
+              tma_load<CG>(to + j * kBK * 128, &g.b, n0 + 64 * j, g.b_row0 + k * kBK, bar);
+          } else {
+            tma_load<CG>(to, &g.b, k * kBK, g.b_row0 + n0, bar);
+          }
+          if (++s == S::kCount) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // Until the products have read them, the copies may still be in flight:
+      // the last use of every stage is waited for, so no copy outlives the block.
+      for (int i = 0; i < S::kCount; ++i) {
+        bar_wait(empty + 8 * s, phase ^ 1);
+        if (++s == S::kCount) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
+                             ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(kBN / 8) << 17) |
+                             ((uint32_t)(kBM * CG / 16) << 24);
+      int s = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const Tile tile = tile_of(g, t);
+        if (!(ok = bar_wait(acc_empty + 8 * buf, acc_phase ^ 1))) break;
+        tmem_fence_after();
+        const uint32_t d = tmem + buf * kBN;
+        bool more = false;
+        for (int k = tile.k0; k < tile.k1; ++k) {
+          if (!(ok = bar_wait(full + 8 * s, phase))) break;
+          tmem_fence_after();
+          const uint32_t at = base + s * S::kBytes;
+          const uint64_t b = smem_desc<B_MN>(at + PARTS * S::kABytes);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            const uint64_t a = smem_desc<A_MN>(at + p * S::kABytes);
+#pragma unroll
+            for (int i = 0; i < kBK / 16; ++i) {
+              // 16 of the sum: 32 bytes along a row, or 16 rows of 128 bytes
+              mma<CG>(d, a + i * ((A_MN ? 2048 : 32) >> 4), b + i * ((B_MN ? 2048 : 32) >> 4),
+                      idesc, more);
+              more = true;
+            }
+          }
+          mma_commit<CG>(empty + 8 * s);
+          if (++s == S::kCount) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) mma_commit<CG>(acc_full + 8 * buf);
+        if ((buf ^= 1) == 0) acc_phase ^= 1;
+      }
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;  // the 32 rows of tensor memory this warp may read
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = first; t < tiles; t += stride) {
+      const Tile tile = tile_of(g, t);
+      // A wait that ran out leaves NaN in everything this block still owes.
+      ok = ok && bar_wait(acc_full + 8 * buf, acc_phase);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tmem_fence_after();
+      const uint32_t acc = tmem + buf * kBN + ((uint32_t)(quarter * 32) << 16);
+      const int row = (tile.m * CG + (int)rank) * kBM + quarter * 32 + lane;
+      if constexpr (EPI == kEpiStats) {
+        epilogue_stats(g, acc, row, tile.n * kBN, !ok);
+      } else if constexpr (EPI == kEpiDz) {
+        epilogue_dz(g, acc, row, tile.n * kBN, !ok);
+      } else {
+        if (g.c_type == RCC_F32)
+          epilogue_out<float>(g, acc, row, tile.n * kBN, tile.split, !ok);
+        else
+          epilogue_out<__nv_bfloat16>(g, acc, row, tile.n * kBN, tile.split, !ok);
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar = acc_empty + 8 * buf;
+        bar_arrive(CG == 2 ? peer_addr(bar, 0) : bar);
+      }
+      if ((buf ^= 1) == 0) acc_phase ^= 1;
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tmem_fence_after();
+  if (warp == 2) tmem_free<CG>(tmem, kTmemCols);
+}
+
+// ---- joins ---------------------------------------------------------------------------
+
+constexpr int kJoinRows = 32, kJoinParts = 32;
+
+// lse and loss of a row from its (max, sum) pairs.
+__global__ void __launch_bounds__(kJoinRows* kJoinParts)
+    join_stats_kernel(const float2* part, int parts, const float* zlab, const void* labels,
+                      int labels64, size_t tokens, size_t vocab, float* loss, float* lse) {
+  __shared__ float2 red[kJoinParts][kJoinRows + 1];
+  pdl_wait_then_release();
+  const int x = threadIdx.x % kJoinRows, y = threadIdx.x / kJoinRows;
+  const size_t row = (size_t)blockIdx.x * kJoinRows + x;
+  float top = -INFINITY, sum = 0.f;
+  auto add = [&](float2 p) {
+    if (p.x == -INFINITY) return;  // nothing in it
+    const float m = fmaxf(top, p.x);
+    sum = sum * exp2f((top - m) * kLog2e) + p.y * exp2f((p.x - m) * kLog2e);
+    top = m;
+  };
+  if (row < tokens)
+    for (int j = y; j < parts; j += kJoinParts) add(part[(size_t)j * tokens + row]);
+  red[y][x] = make_float2(top, sum);
+  __syncthreads();
+  if (y == 0 && row < tokens) {
+    for (int j = 1; j < kJoinParts; ++j) add(red[j][x]);
+    const float l = top + logf(sum);
+    lse[row] = l;
+    loss[row] = load_id(labels, labels64, row, vocab) >= 0 ? l - zlab[row] : 0.f;
+  }
+}
+
+// out = the sum of the slices, eight elements a thread
+template <typename T>
+__global__ void __launch_bounds__(256)
+    join_slices_kernel(const float* part, int slices, size_t n, T* out) {
+  pdl_wait_then_release();
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float s[8];
+  load8(part + i, s);
+  for (int k = 1; k < slices; ++k) {
+    float v[8];
+    load8(part + (size_t)k * n + i, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += v[e];
+  }
+  store8(out + i, s);
+}
+
+// ---- host ------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &got) != cudaSuccess ||
+        got != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = reinterpret_cast<EncodeFn>(p);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+// A bf16 matrix of `rows` rows of `cols`, read in boxes of 64 columns (128
+// bytes, swizzled) and `box_rows` rows; what lies outside reads as zero.
+bool make_map(CUtensorMap* map, const void* p, size_t cols, size_t rows, size_t ld, int box_rows) {
+  const EncodeFn encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
+                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t ceil_div(size_t a, size_t b) { return (a + b - 1) / b; }
+
+template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
+cudaError_t launch_gemm_of(GemmArgs& g, cudaStream_t stream) {
+  using S = Stage<CG, PARTS>;
+  auto kernel = gemm_kernel<CG, PARTS, A_MN, B_MN, EPI>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       S::kShared);
+  if (e != cudaSuccess) return e;
+  const int tiles = g.m_tiles * g.n_tiles * g.splits;
+  const int units = std::min(tiles, sm_count() / CG);
+  return launch_cluster(kernel, dim3(units * CG), dim3(kGemmThreads), S::kShared, CG, stream, g);
+}
+
+// Rows of C, columns, and the extent of the sum; the maps are the caller's.
+template <int PARTS, bool A_MN, bool B_MN, int EPI>
+cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, int splits,
+                        int group, cudaStream_t stream) {
+  g.m = (int)m;
+  g.n = (int)n;
+  g.m_tiles = (int)ceil_div(m, kBM * (pair ? 2 : 1));
+  g.n_tiles = (int)ceil_div(n, kBN);
+  g.k_blocks = (int)ceil_div(k, kBK);
+  g.splits = splits;
+  g.group = group;
+  return pair ? launch_gemm_of<2, PARTS, A_MN, B_MN, EPI>(g, stream)
+              : launch_gemm_of<1, PARTS, A_MN, B_MN, EPI>(g, stream);
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Two SMs share a tile of 256 rows unless 128 rows are all there are.
+bool paired(size_t rows) { return rows > (size_t)kBM; }
+
+constexpr int kScoreGroup = 32, kGradGroup = 8;
+
+// The backward pass's pieces of the vocabulary and what it keeps of each.
+struct Pieces {
+  size_t width;      // vocabulary entries of a piece, a multiple of kBN
+  size_t count;
+  int parts;         // bf16 numbers that make one dz
+  int splits;        // of the sum of dx
+  size_t dz_bytes;   // of one part
+  size_t dx_bytes;   // of the fp32 slices of dx, 0: summed in dx itself
+};
+constexpr size_t kDzBytes = (size_t)512 << 20;
+
+Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
+  Pieces p;
+  p.parts = grad_type == RCC_F32 ? 2 : 1;
+  const size_t most = std::max<size_t>(kBN, kDzBytes / (tokens * 2 * p.parts) / kBN * kBN);
+  p.count = ceil_div(vocab, most);
+  p.width = ceil_div(ceil_div(vocab, p.count), kBN) * kBN;
+  p.count = ceil_div(vocab, p.width);
+  p.dz_bytes = up256(tokens * p.width * 2);
+  const int cg = paired(tokens) ? 2 : 1;
+  const size_t tiles = ceil_div(tokens, kBM * cg) * ceil_div(dim, kBN);
+  const size_t units = sm_count() / cg, k_blocks = p.width / kBK;
+  // few tiles and a long sum: split the sum until every SM has some
+  p.splits = (int)std::max<size_t>(1, std::min(units / tiles, k_blocks / 8));
+  const bool direct = p.splits == 1 && (p.count == 1 || grad_type == RCC_F32);
+  p.dx_bytes = direct ? 0 : up256(p.splits * tokens * dim * 4);
+  return p;
+}
+
+}  // namespace
+
+size_t linear_ce_workspace(size_t tokens, size_t vocab, size_t dim, bool backward, int grad_type) {
+  if (!backward) return up256(ceil_div(vocab, kBN) * tokens * sizeof(float2)) + up256(tokens * 4);
+  const Pieces p = pieces_of(tokens, vocab, dim, grad_type);
+  return p.parts * p.dz_bytes + p.dx_bytes;
+}
+
+cudaError_t launch_linear_ce_forward(const CeArgs& a, cudaStream_t stream, uint64_t* launches) {
+  const bool pair = paired(a.tokens);
+  const int parts = (int)ceil_div(a.vocab, kBN);
+  GemmArgs g = {};
+  g.part = static_cast<float2*>(a.workspace);
+  g.zlab = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
+                                    up256((size_t)parts * a.tokens * sizeof(float2)));
+  g.labels = a.labels;
+  g.labels64 = a.labels64;
+  g.vocab = (int)a.vocab;
+  if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, kBM) ||
+      !make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBN / (pair ? 2 : 1)))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_gemm<1, false, false, kEpiStats>(g, pair, a.tokens, a.vocab, a.dim, 1,
+                                                          kScoreGroup, stream);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(join_stats_kernel, dim3((unsigned)ceil_div(a.tokens, kJoinRows)),
+                    dim3(kJoinRows * kJoinParts), 0, stream, (const float2*)g.part, parts,
+                    (const float*)g.zlab, a.labels, a.labels64, a.tokens, a.vocab, a.loss, a.lse);
+  if (e == cudaSuccess) *launches = 2;
+  return e;
+}
+
+cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint64_t* launches) {
+  const Pieces p = pieces_of(a.tokens, a.vocab, a.dim, a.grad_type);
+  char* ws = static_cast<char*>(a.workspace);
+  __nv_bfloat16* dz[2] = {reinterpret_cast<__nv_bfloat16*>(ws),
+                          p.parts == 2 ? reinterpret_cast<__nv_bfloat16*>(ws + p.dz_bytes)
+                                       : nullptr};
+  float* slices = p.dx_bytes ? reinterpret_cast<float*>(ws + p.parts * p.dz_bytes) : nullptr;
+  const size_t grad_size = a.grad_type == RCC_F32 ? 4 : 2;
+  const bool pair = paired(a.tokens);
+  cudaError_t e;
+  for (size_t i = 0; i < p.count; ++i) {
+    const size_t v0 = i * p.width, width = std::min(p.width, a.vocab - v0);
+    {  // dz of the piece
+      GemmArgs g = {};
+      g.b_row0 = (int)v0;
+      g.labels = a.labels;
+      g.labels64 = a.labels64;
+      g.vocab = (int)a.vocab;
+      g.lse = a.lse;
+      g.dloss = a.dloss;
+      g.dz[0] = dz[0];
+      g.dz[1] = dz[1];
+      g.ld_dz = p.width;
+      if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, kBM) ||
+          !make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBN / (pair ? 2 : 1)))
+        return cudaErrorInvalidValue;
+      e = launch_gemm<1, false, false, kEpiDz>(g, pair, a.tokens, width, a.dim, 1, kScoreGroup,
+                                               stream);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+    if (a.dx) {  // dx (+)= dz W
+      GemmArgs g = {};
+      g.b_row0 = (int)v0;
+      g.c = slices ? slices : a.dx;
+      g.c_type = slices ? RCC_F32 : a.grad_type;
+      g.ld_c = a.dim;
+      g.split_stride = a.tokens * a.dim;
+      g.add = i > 0;
+      for (int k = 0; k < p.parts; ++k)
+        if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBM)) return cudaErrorInvalidValue;
+      if (!make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBK)) return cudaErrorInvalidValue;
+      const int splits = (int)std::min<size_t>(p.splits, ceil_div(width, kBK));
+      e = p.parts == 2 ? launch_gemm<2, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
+                                                              splits, kGradGroup, stream)
+                       : launch_gemm<1, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
+                                                              splits, kGradGroup, stream);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+    if (a.dw) {  // the piece's rows of dW (+)= dz^T x
+      GemmArgs g = {};
+      g.c = static_cast<char*>(a.dw) + v0 * a.dim * grad_size;
+      g.c_type = a.grad_type;
+      g.ld_c = a.dim;
+      g.add = a.accumulate;
+      for (int k = 0; k < p.parts; ++k)
+        if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBK)) return cudaErrorInvalidValue;
+      if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, kBK)) return cudaErrorInvalidValue;
+      const bool wide = paired(width);
+      e = p.parts == 2 ? launch_gemm<2, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, 1,
+                                                             kGradGroup, stream)
+                       : launch_gemm<1, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, 1,
+                                                             kGradGroup, stream);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+  }
+  if (a.dx && slices) {
+    const size_t n = a.tokens * a.dim;
+    const dim3 grid((unsigned)ceil_div(n, 256 * 8));
+    e = a.grad_type == RCC_F32
+            ? launch_kernel(join_slices_kernel<float>, grid, dim3(256), 0, stream,
+                            (const float*)slices, p.splits, n, static_cast<float*>(a.dx))
+            : launch_kernel(join_slices_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
+                            (const float*)slices, p.splits, n, static_cast<__nv_bfloat16*>(a.dx));
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace lm
+}  // namespace rcc

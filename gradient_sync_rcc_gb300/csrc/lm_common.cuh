@@ -1,0 +1,122 @@
+// lm_common.cuh -- element access and reductions shared by the kernels of the
+// language-model operators.  Arithmetic is fp32 throughout; a bf16 value is
+// widened exactly on load and rounded once, to nearest even, on store.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "launch.cuh"
+
+namespace rcc {
+namespace lm {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+
+// Eight consecutive elements.  The vector forms want a 16-byte boundary.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0];
+  const float4 b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void widen2(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  widen2(a.x, v[0], v[1]);
+  widen2(a.y, v[2], v[3]);
+  widen2(a.z, v[4], v[5]);
+  widen2(a.w, v[6], v[7]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
+                                            pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+// The same for any alignment and a row that ends inside the eight: `left`
+// elements are there, the others read as zero and are not written.
+template <typename T>
+__device__ __forceinline__ void load_upto8(const T* p, size_t left, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < left ? to_f32(p[e]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void store_upto8(T* p, size_t left, const float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < left) from_f32(v[e], p[e]);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_row8(const T* row, size_t col, size_t dim, float (&v)[8]) {
+  if constexpr (VEC) {
+    load8(row + col, v);
+  } else {
+    load_upto8(row + col, dim - col, v);
+  }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_row8(T* row, size_t col, size_t dim, const float (&v)[8]) {
+  if constexpr (VEC) {
+    store8(row + col, v);
+  } else {
+    store_upto8(row + col, dim - col, v);
+  }
+}
+
+// A token id or label; one outside [0, vocab) comes back as -1 (padding).
+__device__ __forceinline__ int64_t load_id(const void* ids, int ids64, size_t t, size_t vocab) {
+  const int64_t id = ids64 ? static_cast<const int64_t*>(ids)[t]
+                           : static_cast<const int32_t*>(ids)[t];
+  return id >= 0 && id < static_cast<int64_t>(vocab) ? id : -1;
+}
+
+// launch_kernel for a grid of clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                           int cluster, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// SMs of the current device (152 on GB300).
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 152;
+  }
+  return n;
+}
+
+}  // namespace lm
+}  // namespace rcc

@@ -404,6 +404,104 @@ rcc_status rcc_grad_stats_noalloc(const float* const* grads, int num_ranks,
                                   float* mean_grad, uint32_t* report,
                                   rcc_stream_t stream);
 
+/* ---- language-model operators ----------------------------------------------
+ *
+ * The ends of a language model, whose gradients are the largest that the
+ * gradient sync sees, and the norm between them: the token embedding and its
+ * gradient, an RMS norm that keeps its input in 8 bits for the backward pass,
+ * and the output layer with softmax cross entropy, which never keeps the
+ * logits.  The pages have no counterpart to these calls.
+ *
+ * Shared by all of them:
+ *   - Asynchronous on `stream`; no session, no allocation, no
+ *     synchronisation, so they can be captured into a CUDA graph.  Scratch is
+ *     the caller's: at least rcc_*_workspace bytes, 256-byte aligned, not used
+ *     by anything else until the call's work is done, its contents arbitrary.
+ *   - Matrices are row major.  Inputs may have rows `ld_*` elements apart
+ *     (ld >= the row's length, at most 2^30); outputs are contiguous.
+ *     Outputs and scratch must not overlap each other or an input.
+ *   - Ids and labels are RCC_I32 or RCC_I64.  One outside [0, vocab) is
+ *     padding: it embeds as zeros, has a loss of 0 and adds to no gradient.
+ *   - Sums and softmax statistics are fp32; a bf16 output is rounded once, to
+ *     nearest even.  No sum depends on an order that changes: the same call
+ *     gives the same bits.  A NaN or infinity in an input reaches the outputs
+ *     that depend on it, so that a gradient sync skips the step.
+ *   - tokens = 0 is a valid no-op, except that a gradient that is not
+ *     accumulated is set to zero.
+ *   - Gradients with `accumulate` are added to what the buffer holds (a tied
+ *     weight, further micro-batches); otherwise the buffer is overwritten.
+ *   - Sizes, types and alignments that an operator does not have:
+ *     RCC_ERR_INVALID_ARGUMENT; a stride or workspace that is too small:
+ *     RCC_ERR_SHAPE_MISMATCH.
+ */
+typedef enum { RCC_I32 = 0, RCC_I64 = 1 } rcc_index;
+
+/* out[t] = scale * table[ids[t]]: tokens rows of dim elements (any dim up to
+ * 2^20), rounded once to out_type. */
+rcc_status rcc_embedding_forward(const void* table, rcc_dtype table_type, size_t ld_table,
+                                 const void* ids, rcc_index index, size_t tokens, size_t vocab,
+                                 size_t dim, float scale, void* out, rcc_dtype out_type,
+                                 rcc_stream_t stream);
+
+/* dtable[v] (+)= scale * sum of dout[t] over the tokens with ids[t] = v, added
+ * in fp32 in an order that the ids alone decide.  Without `accumulate` rows of
+ * absent tokens become zero; with it they are not touched. */
+size_t rcc_embedding_backward_workspace(size_t tokens, size_t vocab, size_t dim);
+rcc_status rcc_embedding_backward(const void* dout, rcc_dtype dout_type, size_t ld_dout,
+                                  const void* ids, rcc_index index, size_t tokens, size_t vocab,
+                                  size_t dim, float scale, void* dtable, rcc_dtype dtable_type,
+                                  int accumulate, void* workspace, size_t workspace_bytes,
+                                  rcc_stream_t stream);
+
+/* y = x r weight with r = 1 / sqrt(mean(x^2) + eps), for tokens rows of dim
+ * elements (dim up to 32,768); x and y of `type`, weight fp32.
+ * `kept` and `scales`, when not NULL, receive x in 8 bits for the backward
+ * pass: for each group of 128 columns with largest magnitude a,
+ *   kept = rint(x * (127 * (1 / a))),  scales = a * (1 / 127),
+ * every operation rounded to fp32;
+ * kept [tokens][128 G] (16-byte aligned; zeros past dim) and scales
+ * [tokens][G] with G = ceil(dim / 128).  A group with a < 2^-120 is kept as
+ * zeros; the scale of a group with a NaN or infinity is NaN. */
+rcc_status rcc_rmsnorm_forward(const void* x, rcc_dtype type, size_t ld_x, const float* weight,
+                               float eps, size_t tokens, size_t dim, void* y, int8_t* kept,
+                               float* scales, rcc_stream_t stream);
+
+/* The gradient of the norm at x' = kept * scales, for dy and dx of `type`:
+ *   n = x' r', r' = 1 / sqrt(mean(x'^2) + eps)
+ *   dx = r' (dy weight - n mean(dy weight n)),  dweight (+)= sum_t dy n. */
+size_t rcc_rmsnorm_backward_workspace(size_t tokens, size_t dim);
+rcc_status rcc_rmsnorm_backward(const void* dy, rcc_dtype type, size_t ld_dy, const int8_t* kept,
+                                const float* scales, const float* weight, float eps,
+                                size_t tokens, size_t dim, void* dx, float* dweight,
+                                int accumulate, void* workspace, size_t workspace_bytes,
+                                rcc_stream_t stream);
+
+/* With logits z = x w^T (x [tokens][dim] and w [vocab][dim] bf16, dim a
+ * multiple of 8, buffers 16-byte aligned, row strides multiples of 8):
+ *   lse[t] = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][labels[t]].
+ * The logits are formed in pieces on the tensor cores, summed in fp32 and
+ * never stored. */
+size_t rcc_linear_ce_workspace(size_t tokens, size_t vocab, size_t dim, int backward,
+                               rcc_dtype grad_type);
+rcc_status rcc_linear_ce_forward(const void* x, size_t ld_x, const void* w, size_t ld_w,
+                                 const void* labels, rcc_index index, size_t tokens, size_t vocab,
+                                 size_t dim, float* loss, float* lse, void* workspace,
+                                 size_t workspace_bytes, rcc_stream_t stream);
+
+/* Gradients of sum_t dloss[t] loss[t], with the forward pass's lse:
+ *   dz = dloss (exp(z - lse) - onehot(label)),  dx = dz w,  dw (+)= dz^T x.
+ * dx and dw are of grad_type and 16-byte aligned; either may be NULL (not
+ * wanted).  For RCC_BF16 gradients dz is rounded to bf16 for the tensor
+ * cores; for RCC_F32 it is carried as the sum of two bf16 numbers, which
+ * costs twice the products and keeps fp32's accuracy.  The logits are formed
+ * again, a piece of the vocabulary at a time; the workspace holds one
+ * piece's dz (512 MiB at most, and a piece is at least 256 entries). */
+rcc_status rcc_linear_ce_backward(const void* x, size_t ld_x, const void* w, size_t ld_w,
+                                  const void* labels, rcc_index index, const float* lse,
+                                  const float* dloss, size_t tokens, size_t vocab, size_t dim,
+                                  void* dx, void* dw, rcc_dtype grad_type, int accumulate,
+                                  void* workspace, size_t workspace_bytes, rcc_stream_t stream);
+
 /* ---- diagnostics ---------------------------------------------------------- */
 
 /* Message describing the calling thread's most recent error ("" if none). */
