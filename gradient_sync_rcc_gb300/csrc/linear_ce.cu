@@ -147,23 +147,19 @@ __device__ __forceinline__ void tmem_fence_before() {
 __device__ __forceinline__ void tmem_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// 32 columns of this thread's row
-__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
-  uint32_t r[32];
-  __syncwarp();  // the whole warp loads
+// v += 16 columns of this thread's row; the whole warp calls it
+__device__ __forceinline__ void tmem_add16(uint32_t at, float* v) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(at));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
 
 // ---- the product -------------------------------------------------------------------
@@ -172,9 +168,16 @@ constexpr int kBM = 128;   // rows of C of one block
 constexpr int kBN = 256;   // columns of C of one block (of a pair: the same)
 constexpr int kBK = 64;    // of the sum per stage: 128 bytes, one swizzle row
 constexpr int kRowBytes = kBK * 2;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;  // two for each 32 rows, half of the columns each
+constexpr int kHalf = kBN / 2;
 constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
 constexpr int kTmemCols = 512;  // two accumulators of kBN columns
+// Additions on the tensor cores drop what does not fit the accumulator instead
+// of rounding it, a loss that grows with their number (3.7e-5 of dx after
+// 4,000 of them).  So an accumulator of an fp32 result takes 64 instructions of
+// 16 products at most, and the epilogue adds it up in registers, rounding to
+// nearest; a result that is rounded to bf16 is taken whole.
+constexpr int kChunkMmas = 64;
 
 enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
 
@@ -183,11 +186,12 @@ struct GemmArgs {
   int m, n;              // of C
   int m_tiles, n_tiles;  // of kBM * CG rows, of kBN columns
   int k_blocks, splits;  // of kBK; pieces of the sum, each with a C of its own
+  int chunk;             // k_blocks that one accumulator takes
   int group;             // tiles of rows that share a run over the columns
   int b_row0;            // first row of B (vocabulary entry) of this piece
   int a_x0, b_y0;        // offsets of the maps' coordinates
   // stats
-  float2* part;          // [n_tiles][m]
+  float2* part;          // [2 n_tiles][m]
   float* zlab;           // [m]
   const void* labels;
   int labels64;
@@ -249,115 +253,103 @@ __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int t) {
 
 constexpr float kLog2e = 1.44269504f;
 
-// A row's 256 scores: the running (max, sum of exp) of the columns that exist.
-__device__ __forceinline__ void epilogue_stats(const GemmArgs& g, uint32_t acc, int row, int col0,
-                                               bool failed) {
-  const bool live = row < g.m;
-  const int64_t label = live ? load_id(g.labels, g.labels64, row, g.vocab) : -1;
-  const float nan = __uint_as_float(0x7FC00000u);
-  float top = -INFINITY, sum = 0.f;
-  for (int c = 0; c < kBN; c += 32) {
-    const int left = g.n - (col0 + c);
-    if (left <= 0) break;
-    float v[32];
-    tmem_load32(acc + c, v);
-    if (left < 32) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i >= left) v[i] = -INFINITY;
-    }
-    const int64_t at = label - (col0 + c);
-    if (at >= 0 && at < 32) {
-      float z = v[0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) z = i == at ? v[i] : z;
-      g.zlab[row] = failed ? nan : z;
-    }
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
-    m = fmaxf(top, m);
-    const float ml = m * kLog2e;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s += exp2f(fmaf(v[i], kLog2e, -ml));
-    // nothing before the first columns: top is -inf there and sum 0
-    sum = c == 0 ? s : fmaf(sum, exp2f(fmaf(top, kLog2e, -ml)), s);
-    top = m;
-  }
-  if (live)
-    g.part[(size_t)(col0 / kBN) * g.m + row] = failed ? make_float2(nan, nan) : make_float2(top, sum);
+// exp2, denormal results as zero
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// dz of a row's 256 columns; columns past the piece are not written.
-__device__ __forceinline__ void epilogue_dz(const GemmArgs& g, uint32_t acc, int row, int col0,
-                                            bool failed) {
-  const bool live = row < g.m;
-  const int64_t label = live ? load_id(g.labels, g.labels64, row, g.vocab) : -1;
-  const float lse = live ? g.lse[row] : 0.f;
+// Half a row of scores: (max, sum of exp) of the columns that exist.
+__device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHalf], int row,
+                                               int col0, bool failed) {
+  const int left = g.n - col0;
+  if (row >= g.m || left <= 0) {
+    if (row < g.m) g.part[(size_t)(col0 / kHalf) * g.m + row] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const float nan = __uint_as_float(0x7FC00000u);
+  const int64_t at = load_id(g.labels, g.labels64, row, g.vocab) - col0;
+  if (at >= 0 && at < kHalf) {
+    float z = v[0];
+#pragma unroll
+    for (int i = 1; i < kHalf; ++i) z = i == at ? v[i] : z;
+    g.zlab[row] = failed ? nan : z;
+  }
+  if (left < kHalf) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i)
+      if (i >= left) v[i] = -INFINITY;
+  }
+  float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int i = 4; i < kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  const float ml = m * kLog2e;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i) sum[i & 3] += exp2_fast(fmaf(v[i], kLog2e, -ml));
+  g.part[(size_t)(col0 / kHalf) * g.m + row] =
+      failed ? make_float2(nan, nan) : make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+}
+
+// dz of half a row; columns past the piece are not written.
+__device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf], int row,
+                                            int col0, bool failed) {
+  const int left = g.n - col0;
+  if (row >= g.m || left <= 0) return;
+  const int64_t label = load_id(g.labels, g.labels64, row, g.vocab);
+  const int64_t at = label - (g.b_row0 + col0);
   const float f = label >= 0 ? g.dloss[row] : 0.f;
-  const float ll = lse * kLog2e;
-  for (int c = 0; c < kBN; c += 32) {
-    const int left = g.n - (col0 + c);
-    if (left <= 0) break;
-    float v[32];
-    tmem_load32(acc + c, v);
-    const int64_t at = label - (g.b_row0 + col0 + c);
+  const float ll = g.lse[row] * kLog2e;
+  __nv_bfloat16* out = g.dz[0] + (size_t)row * g.ld_dz + col0;
+  __nv_bfloat16* rest = g.dz[1] ? g.dz[1] + (size_t)row * g.ld_dz + col0 : nullptr;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float p = exp2f(fmaf(v[i], kLog2e, -ll));
-      v[i] = label < 0 ? 0.f : f * (i == at ? p - 1.f : p);
-      if (failed) v[i] = __uint_as_float(0x7FC00000u);
+  for (int c = 0; c < kHalf; c += 8) {
+    // ld_dz is a multiple of 256, so whole vectors stay inside the row
+    if (c >= left) break;
+    uint32_t w[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = exp2_fast(fmaf(v[c + i], kLog2e, -ll));
+      float d = label < 0 ? 0.f : f * (c + i == at ? p - 1.f : p);
+      if (failed) d = __uint_as_float(0x7FC00000u);
+      v[c + i] = d;
     }
-    if (!live) continue;
-    // ld_dz is a multiple of 64, so that whole vectors stay inside the row
-    for (int part = 0; part < 2; ++part) {
-      if (!g.dz[part]) break;
-      uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
-      uint4* out = reinterpret_cast<uint4*>(g.dz[part] + (size_t)row * g.ld_dz + col0 + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (8 * i < left) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float lo, hi;
-        widen2(w[i], lo, hi);
-        v[2 * i] -= lo;
-        v[2 * i + 1] -= hi;
-      }
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
+      float lo, hi;
+      widen2(w[i], lo, hi);
+      u[i] = pack2(v[c + 2 * i] - lo, v[c + 2 * i + 1] - hi);
     }
+    *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (rest) *reinterpret_cast<uint4*>(rest + c) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void epilogue_out(const GemmArgs& g, uint32_t acc, int row, int col0,
-                                             int split, bool failed) {
-  T* c0 = static_cast<T*>(g.c) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
-  for (int c = 0; c < kBN; c += 32) {
-    const int left = g.n - (col0 + c);
-    if (left <= 0) break;
-    float v[32];
-    tmem_load32(acc + c, v);
-    if (row >= g.m) continue;
+__device__ __forceinline__ void epilogue_out(const GemmArgs& g, const float (&v)[kHalf], int row,
+                                             int col0, int split, bool failed) {
+  const int left = g.n - col0;  // n is a multiple of 8
+  if (row >= g.m) return;
+  T* out = static_cast<T*>(g.c) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      if (i >= left) break;  // n is a multiple of 8
-      float o[8];
-      if (g.add) {
-        load8(c0 + c + i, o);
-      } else {
+  for (int c = 0; c < kHalf; c += 8) {
+    if (c >= left) break;
+    float o[8];
+    if (g.add) {
+      load8(out + c, o);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o[e] += v[i + e];
-        if (failed) o[e] = __uint_as_float(0x7FC00000u);
-      }
-      store8(c0 + c + i, o);
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      o[e] += v[c + e];
+      if (failed) o[e] = __uint_as_float(0x7FC00000u);
+    }
+    store8(out + c, o);
   }
 }
 
@@ -399,7 +391,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
   pdl_wait_then_release();
-
   if (warp == 0) {
     if (lane == 0) {
       // what earlier kernels wrote by ordinary stores, before copies by TMA
@@ -461,66 +452,76 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
         const Tile tile = tile_of(g, t);
-        if (!(ok = bar_wait(acc_empty + 8 * buf, acc_phase ^ 1))) break;
-        tmem_fence_after();
-        const uint32_t d = tmem + buf * kBN;
-        bool more = false;
-        for (int k = tile.k0; k < tile.k1; ++k) {
-          if (!(ok = bar_wait(full + 8 * s, phase))) break;
+        for (int k0 = tile.k0; k0 < tile.k1 && ok; k0 += g.chunk) {
+          const int k1 = min(k0 + g.chunk, tile.k1);
+          if (!(ok = bar_wait(acc_empty + 8 * buf, acc_phase ^ 1))) break;
           tmem_fence_after();
-          const uint32_t at = base + s * S::kBytes;
-          const uint64_t b = smem_desc<B_MN>(at + PARTS * S::kABytes);
+          const uint32_t d = tmem + buf * kBN;
+          for (int k = k0; k < k1; ++k) {
+            if (!(ok = bar_wait(full + 8 * s, phase))) break;
+            tmem_fence_after();
+            const uint32_t at = base + s * S::kBytes;
+            const uint64_t b = smem_desc<B_MN>(at + PARTS * S::kABytes);
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            const uint64_t a = smem_desc<A_MN>(at + p * S::kABytes);
+            for (int p = 0; p < PARTS; ++p) {
+              const uint64_t a = smem_desc<A_MN>(at + p * S::kABytes);
 #pragma unroll
-            for (int i = 0; i < kBK / 16; ++i) {
-              // 16 of the sum: 32 bytes along a row, or 16 rows of 128 bytes
-              mma<CG>(d, a + i * ((A_MN ? 2048 : 32) >> 4), b + i * ((B_MN ? 2048 : 32) >> 4),
-                      idesc, more);
-              more = true;
+              for (int i = 0; i < kBK / 16; ++i)
+                // 16 of the sum: 32 bytes along a row, or 16 rows of 128 bytes
+                mma<CG>(d, a + i * ((A_MN ? 2048 : 32) >> 4), b + i * ((B_MN ? 2048 : 32) >> 4),
+                        idesc, k > k0 || p > 0 || i > 0);
+            }
+            mma_commit<CG>(empty + 8 * s);
+            if (++s == S::kCount) {
+              s = 0;
+              phase ^= 1;
             }
           }
-          mma_commit<CG>(empty + 8 * s);
-          if (++s == S::kCount) {
-            s = 0;
-            phase ^= 1;
-          }
+          if (ok) mma_commit<CG>(acc_full + 8 * buf);
+          if ((buf ^= 1) == 0) acc_phase ^= 1;
         }
-        if (ok) mma_commit<CG>(acc_full + 8 * buf);
-        if ((buf ^= 1) == 0) acc_phase ^= 1;
       }
     }
   } else if (warp >= 4) {
     const int quarter = warp & 3;  // the 32 rows of tensor memory this warp may read
+    const int half = (warp - 4) >> 2;
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int t = first; t < tiles; t += stride) {
       const Tile tile = tile_of(g, t);
-      // A wait that ran out leaves NaN in everything this block still owes.
-      ok = ok && bar_wait(acc_full + 8 * buf, acc_phase);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tmem_fence_after();
-      const uint32_t acc = tmem + buf * kBN + ((uint32_t)(quarter * 32) << 16);
+      float v[kHalf];
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) v[i] = 0.f;
+      for (int k0 = tile.k0; k0 < tile.k1; k0 += g.chunk) {
+        // A wait that ran out leaves NaN in everything this block still owes.
+        ok = ok && bar_wait(acc_full + 8 * buf, acc_phase);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tmem_fence_after();
+        const uint32_t acc = tmem + buf * kBN + half * kHalf + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 16) tmem_add16(acc + c, v + c);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = acc_empty + 8 * buf;
+          bar_arrive(CG == 2 ? peer_addr(bar, 0) : bar);
+        }
+        if ((buf ^= 1) == 0) acc_phase ^= 1;
+      }
       const int row = (tile.m * CG + (int)rank) * kBM + quarter * 32 + lane;
+      const int col0 = tile.n * kBN + half * kHalf;
       if constexpr (EPI == kEpiStats) {
-        epilogue_stats(g, acc, row, tile.n * kBN, !ok);
+        epilogue_stats(g, v, row, col0, !ok);
       } else if constexpr (EPI == kEpiDz) {
-        epilogue_dz(g, acc, row, tile.n * kBN, !ok);
+        epilogue_dz(g, v, row, col0, !ok);
       } else {
         if (g.c_type == RCC_F32)
-          epilogue_out<float>(g, acc, row, tile.n * kBN, tile.split, !ok);
+          epilogue_out<float>(g, v, row, col0, tile.split, !ok);
         else
-          epilogue_out<__nv_bfloat16>(g, acc, row, tile.n * kBN, tile.split, !ok);
+          epilogue_out<__nv_bfloat16>(g, v, row, col0, tile.split, !ok);
       }
-      tmem_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        const uint32_t bar = acc_empty + 8 * buf;
-        bar_arrive(CG == 2 ? peer_addr(bar, 0) : bar);
-      }
-      if ((buf ^= 1) == 0) acc_phase ^= 1;
     }
   }
   __syncwarp();
@@ -641,6 +642,7 @@ cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, in
   g.k_blocks = (int)ceil_div(k, kBK);
   g.splits = splits;
   g.group = group;
+  g.chunk = EPI == kEpiOut && g.c_type == RCC_BF16 ? g.k_blocks : kChunkMmas / (PARTS * (kBK / 16));
   return pair ? launch_gemm_of<2, PARTS, A_MN, B_MN, EPI>(g, stream)
               : launch_gemm_of<1, PARTS, A_MN, B_MN, EPI>(g, stream);
 }
@@ -684,14 +686,14 @@ Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
 }  // namespace
 
 size_t linear_ce_workspace(size_t tokens, size_t vocab, size_t dim, bool backward, int grad_type) {
-  if (!backward) return up256(ceil_div(vocab, kBN) * tokens * sizeof(float2)) + up256(tokens * 4);
+  if (!backward) return up256(2 * ceil_div(vocab, kBN) * tokens * sizeof(float2)) + up256(tokens * 4);
   const Pieces p = pieces_of(tokens, vocab, dim, grad_type);
   return p.parts * p.dz_bytes + p.dx_bytes;
 }
 
 cudaError_t launch_linear_ce_forward(const CeArgs& a, cudaStream_t stream, uint64_t* launches) {
   const bool pair = paired(a.tokens);
-  const int parts = (int)ceil_div(a.vocab, kBN);
+  const int parts = 2 * (int)ceil_div(a.vocab, kBN);  // one for each half of a tile's columns
   GemmArgs g = {};
   g.part = static_cast<float2*>(a.workspace);
   g.zlab = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
