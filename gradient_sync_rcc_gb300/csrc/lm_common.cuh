@@ -19,6 +19,31 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
+// Two fp32 operations in one instruction, each rounded as usual.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Eight consecutive elements.  The vector forms want a 16-byte boundary.
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0];
@@ -62,6 +87,14 @@ __device__ __forceinline__ void store_upto8(T* p, size_t left, const float (&v)[
   for (int e = 0; e < 8; ++e)
     if (e < left) from_f32(v[e], p[e]);
 }
+// The same as four pairs
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float2 (&v)[4]) {
+  float f[8];
+  load8(p, f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
 template <bool VEC, typename T>
 __device__ __forceinline__ void load_row8(const T* row, size_t col, size_t dim, float (&v)[8]) {
   if constexpr (VEC) {
@@ -77,6 +110,24 @@ __device__ __forceinline__ void store_row8(T* row, size_t col, size_t dim, const
   } else {
     store_upto8(row + col, dim - col, v);
   }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_row8(const T* row, size_t col, size_t dim, float2 (&v)[4]) {
+  float f[8];
+  load_row8<VEC>(row, col, dim, f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_row8(T* row, size_t col, size_t dim, const float2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = v[e].x;
+    f[2 * e + 1] = v[e].y;
+  }
+  store_row8<VEC>(row, col, dim, f);
 }
 
 // A token id or label; one outside [0, vocab) comes back as -1 (padding).

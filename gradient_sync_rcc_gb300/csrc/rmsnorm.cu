@@ -10,6 +10,8 @@
 // The backward pass is the exact gradient of the norm at the kept input x', so
 // nothing but q and s (1.03 bytes an element) has to survive from the forward
 // pass.
+#include <algorithm>
+
 #include "lm_common.cuh"
 #include "lm_internal.h"
 
@@ -22,7 +24,8 @@ namespace {
 constexpr float kTiny = 7.52316385e-37f;  // 2^-120
 
 // Sums over the G threads (a power of two) that share a row; G > 32 goes
-// through shared memory.  Every thread of the block calls it.
+// through `red`, which the caller alternates from row to row, so that one
+// barrier a row is enough.  Every thread of the block calls it.
 template <int G, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N], int tid) {
 #pragma unroll
@@ -30,7 +33,6 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N], int tid)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
   if constexpr (G > 32) {
-    __syncthreads();  // the previous row's sums have been read
     if ((tid & 31) == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) red[tid >> 5][i] = v[i];
@@ -38,156 +40,469 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N], int tid)
     const int w0 = (tid / G) * (G / 32);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
     for (int w = 0; w < G / 32; ++w)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += red[w0 + w][i];
   }
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN wins
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 1.5 2^23: adding it leaves a value below 2^22 rounded to a whole number,
+// ties to even, in the low bits of the sum.
+constexpr float kWhole = 12582912.f;
+
+// rint(x inv) of two values, in the low bytes.  Two roundings, the product's
+// and the whole number's: never one fused operation.
+__device__ __forceinline__ uint32_t quantize2(float2 a, float inv) {
+  a = mul2(a, both(inv));
+  return __byte_perm(__float_as_uint(__fadd_rn(a.x, kWhole)),
+                     __float_as_uint(__fadd_rn(a.y, kWhole)), 0x0040);
+}
+// and back: four signed bytes as floats (2^23 + 128 + q has q + 128 in its low bits)
+__device__ __forceinline__ void widen4(uint32_t q, float2& a, float2& b) {
+  q ^= 0x80808080u;
+  constexpr uint32_t k = 0x4B000000u;
+  constexpr float c = -8388736.f;
+  a = add2(make_float2(__uint_as_float(__byte_perm(q, k, 0x7540)),
+                       __uint_as_float(__byte_perm(q, k, 0x7541))), both(c));
+  b = add2(make_float2(__uint_as_float(__byte_perm(q, k, 0x7542)),
+                       __uint_as_float(__byte_perm(q, k, 0x7543))), both(c));
+}
+
 // threads of a block whose rows take G threads each
 template <int G>
 constexpr int kBlock = G > 256 ? G : 256;
 
-// One row for each group of G threads; a thread holds NV vectors of eight
-// columns, vector k at (k G + t) 8, so 16 neighbouring threads hold one group
-// of 128 columns.
-template <typename T, int G, int NV, bool VEC>
-__global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs a) {
-  constexpr int kRows = kBlock<G> / G;
-  __shared__ float red[kBlock<G> / 32][1];
-  pdl_wait_then_release();
-  const int tid = threadIdx.x, t = tid % G;
-  const size_t row = (size_t)blockIdx.x * kRows + tid / G;
-  const bool live = row < a.tokens;
-  const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.ld_x;
-  float v[NV][8];
-  float sum[1] = {0.f};
+// A thread holds parts of 16 bytes: kE consecutive elements, as they lie in
+// memory or as kE / 2 fp32 pairs.  Part p of thread t of the G that share a row
+// begins at column (p G + t) kE, so neighbouring threads read neighbouring
+// parts, and 128 / kE threads hold a group of 128 columns.
+template <typename T>
+struct Part {
+  static constexpr int kE = 16 / (int)sizeof(T);
+  static constexpr int kPairs = kE / 2;
+  static constexpr int kBytes8 = kE / 4;  // words of the 8-bit form
+};
+__device__ __forceinline__ void widen(const uint4& r, float2 (&v)[4], __nv_bfloat16) {
+  widen2(r.x, v[0].x, v[0].y);
+  widen2(r.y, v[1].x, v[1].y);
+  widen2(r.z, v[2].x, v[2].y);
+  widen2(r.w, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void widen(const uint4& r, float2 (&v)[2], float) {
+  v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+  v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ uint4 narrow(const float2 (&v)[4], __nv_bfloat16) {
+  return make_uint4(pack2(v[0].x, v[0].y), pack2(v[1].x, v[1].y), pack2(v[2].x, v[2].y),
+                    pack2(v[3].x, v[3].y));
+}
+__device__ __forceinline__ uint4 narrow(const float2 (&v)[2], float) {
+  return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                    __float_as_uint(v[1].y));
+}
+// A part at p: whole and aligned (VEC), or of any alignment with `left`
+// elements there, what lies past them as zeros and not written
+template <bool VEC, typename T>
+__device__ __forceinline__ uint4 load_part(const T* p, int left) {
+  if constexpr (VEC) {
+    return *reinterpret_cast<const uint4*>(p);
+  } else {
+    float2 v[Part<T>::kPairs];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const size_t col = (size_t)(k * G + t) * 8;
-    if (live && col < a.dim) {
-      load_row8<VEC>(x, col, a.dim, v[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = 0.f;
+    for (int e = 0; e < Part<T>::kPairs; ++e) {
+      v[e].x = 2 * e < left ? to_f32(p[2 * e]) : 0.f;
+      v[e].y = 2 * e + 1 < left ? to_f32(p[2 * e + 1]) : 0.f;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
+    return narrow(v, T());
   }
-  row_sum<G>(sum, red, tid);
-  const float r = __frsqrt_rn(sum[0] / (float)a.dim + a.eps);
-  const size_t groups = (a.dim + kKeepGroup - 1) / kKeepGroup;
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_part(T* p, int left, const float2 (&v)[Part<T>::kPairs]) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uint4*>(p) = narrow(v, T());
+  } else {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const size_t col = (size_t)(k * G + t) * 8;
-    if (a.kept) {
-      // |x| as its bits: ordered like the values, infinity and NaN above them
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[k][e]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      if (live && col < groups * kKeepGroup) {
-        const float amax = __uint_as_float(top);
-        const bool bad = top >= 0x7F800000u, small = amax < kTiny;
-        const float inv = bad || small ? 0.f : 127.f * __frcp_rn(amax);
-        uint32_t w[2] = {0u, 0u};
-        if (!bad) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int q = __float2int_rn(v[k][e] * inv);
-            w[e >> 2] |= (uint32_t)(q & 0xFF) << (8 * (e & 3));
-          }
-        }
-        *reinterpret_cast<uint2*>(a.kept + row * groups * kKeepGroup + col) =
-            make_uint2(w[0], w[1]);
-        if ((t & 15) == 0)
-          a.scales[row * groups + col / kKeepGroup] =
-              bad ? __uint_as_float(0x7FC00000u) : small ? 0.f : amax * (1.f / 127.f);
-      }
-    }
-    if (live && col < a.dim) {
-      float w8[8];
-      load_row8<VEC>(a.weight, col, a.dim, w8);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * r * w8[e];
-      store_row8<VEC>(static_cast<T*>(a.y) + row * a.ld_y, col, a.dim, v[k]);
+    for (int e = 0; e < Part<T>::kPairs; ++e) {
+      if (2 * e < left) from_f32(v[e].x, p[2 * e]);
+      if (2 * e + 1 < left) from_f32(v[e].y, p[2 * e + 1]);
     }
   }
 }
+// The weight of a part's columns
+template <bool VEC, int PAIRS>
+__device__ __forceinline__ void load_weight(const float* w, int left, float2 (&v)[PAIRS]) {
+#pragma unroll
+  for (int e = 0; e < PAIRS; e += 2) {
+    const uint4 f = load_part<VEC>(w + 2 * e, left - 2 * e);
+    v[e] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+    v[e + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+  }
+}
+
+// `n` (4, 8 or 16) bytes of global memory into shared memory, asynchronously
+template <int N>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(N)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the newest N groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Measured at 16,384 rows of 4,096 bf16 (fp32) columns, where 6.78 TB/s would
+// take 50 (89) us each way:
+//   forward   rows copied ahead, twice the blocks that fit    54.6 (97.6) us
+//             three rows ahead, as many blocks as fit         63.3 (106)
+//             nothing copied ahead, a block a row             66.6 (91.6)
+//   backward  768 threads an SM, 3 rows held                  67.4 (125)
+//             2 rows held                                     66.4 (136)
+//             1,024 threads, 2 rows held                      77.6 (139)
+//             512 threads, 3 rows held                        96 (125)
+//             nothing copied ahead, 1,024 threads             131 (169)
+constexpr int kForeThreads = 2048, kForeStages = 2;
+constexpr int kBackThreads = 768, kBackStages = 3;
+constexpr int kSharedMost = 220 * 1024;   // of all blocks of one SM
+
+// blocks of `threads` that one SM takes, of `shared` bytes each, for `all` threads
+constexpr int blocks_per_sm(int all, int threads, int shared) {
+  return shared && kSharedMost / shared < all / threads ? (kSharedMost / shared > 0 ? kSharedMost / shared : 1)
+                                                        : (all / threads > 0 ? all / threads : 1);
+}
+
+// Rows copied ahead into shared memory (aligned rows, VEC).  A thread writes
+// and reads its own parts alone, so the copies need no barrier.
+template <typename T, int G, int NV, bool VEC>
+struct NormFore {
+  static constexpr int kThreads = kBlock<G>;
+  static constexpr int kParts = NV * 8 / Part<T>::kE;
+  static constexpr int kStage = kThreads * kParts * 16;
+  static constexpr int kFit = kSharedMost / kStage;
+  static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kForeStages ? kFit : kForeStages) : 0;
+  static constexpr int kShared = kStages * kStage;
+  static constexpr int kPerSm = blocks_per_sm(kForeThreads, kThreads, kShared);
+};
+
+// One row for each group of G threads at a time; a thread keeps its part of
+// the weight over all its rows.
+template <typename T, int G, int NV, bool VEC>
+__global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs a) {
+  using F = NormFore<T, G, NV, VEC>;
+  using P = Part<T>;
+  constexpr int kThreads = F::kThreads, kRows = kThreads / G, kStages = F::kStages;
+  constexpr int kParts = F::kParts;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[2][kThreads / 32][1];
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, t = tid % G;
+  constexpr int kSpan = G * P::kE;  // columns from a thread's part to its next
+  const int dim = (int)a.dim, left = dim - t * P::kE;
+  const int groups = (dim + (int)kKeepGroup - 1) / (int)kKeepGroup;
+  const int kept_left = groups * (int)kKeepGroup - t * P::kE;
+  const float inv_dim = 1.f / (float)dim;
+  // this thread's first part of its row, here and in the row that is copied ahead
+  size_t row = (size_t)blockIdx.x * kRows + tid / G;
+  const size_t step = (size_t)gridDim.x * kRows;
+  const T* ahead = static_cast<const T*>(a.x) + row * a.ld_x + t * P::kE;
+  T* y = static_cast<T*>(a.y) + row * a.ld_y + t * P::kE;
+  int8_t* kept = a.kept + row * groups * kKeepGroup + t * P::kE;
+  float* scales = a.scales + row * groups + t * P::kE / (int)kKeepGroup;
+  size_t ahead_row = row;
+  auto x_at = [&](int s, int p) {
+    return reinterpret_cast<uint4*>(smem + s * F::kStage) + p * kThreads + tid;
+  };
+  auto copy_row = [&](int s) {
+    if (ahead_row < a.tokens) {
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+        if (left > p * kSpan) copy_async<16>(x_at(s, p), ahead + p * kSpan);
+    }
+    copies_commit();  // one group a row, also when there is none
+    ahead += step * a.ld_x;
+    ahead_row += step;
+  };
+  for (int s = 0; s < kStages - 1; ++s) copy_row(s);
+  float2 w[kParts][P::kPairs];
+#pragma unroll
+  for (int p = 0; p < kParts; ++p)
+    if (left > p * kSpan)
+      load_weight<VEC>(a.weight + t * P::kE + p * kSpan, left - p * kSpan, w[p]);
+  int stage = 0, flip = 0;
+  for (size_t first = (size_t)blockIdx.x * kRows; first < a.tokens; first += step, row += step) {
+    const bool live = kRows == 1 || row < a.tokens;
+    if constexpr (kStages > 0) {
+      copy_row(stage == 0 ? kStages - 1 : stage - 1);
+      copies_wait<kStages - 1>();
+    }
+    float2 v[kParts][P::kPairs];
+    float2 sq = both(0.f);
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (live && left > p * kSpan) {
+        if constexpr (kStages > 0)
+          raw = *x_at(stage, p);
+        else
+          raw = load_part<VEC>(ahead + p * kSpan, left - p * kSpan);
+      }
+      widen(raw, v[p], T());
+#pragma unroll
+      for (int e = 0; e < P::kPairs; ++e) sq = fma2(v[p][e], v[p][e], sq);
+    }
+    float sum[1] = {sq.x + sq.y};
+    row_sum<G>(sum, red[flip], tid);
+    const float r = rsqrtf(fmaf(sum[0], inv_dim, a.eps));
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      if (a.kept) {
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < P::kPairs; ++e)
+          amax = max_nan(max_nan(amax, fabsf(v[p][e].x)), fabsf(v[p][e].y));
+#pragma unroll
+        for (int o = (int)kKeepGroup / P::kE / 2; o > 0; o >>= 1)
+          amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        if (live && kept_left > p * kSpan) {
+          // a NaN or infinity: zeros and a NaN scale; next to nothing: zeros
+          const bool fine = amax >= kTiny && amax < INFINITY;
+          const float inv = fine ? 127.f * __frcp_rn(amax) : 0.f;
+          uint32_t q[P::kBytes8];
+#pragma unroll
+          for (int i = 0; i < P::kBytes8; ++i)
+            q[i] = __byte_perm(quantize2(v[p][2 * i], inv), quantize2(v[p][2 * i + 1], inv),
+                               0x5410);
+          if (!fine) q[0] = q[P::kBytes8 - 1] = 0u;
+          if constexpr (P::kBytes8 == 2)
+            *reinterpret_cast<uint2*>(kept + p * kSpan) = make_uint2(q[0], q[P::kBytes8 - 1]);
+          else
+            *reinterpret_cast<uint32_t*>(kept + p * kSpan) = q[0];
+          if (t % ((int)kKeepGroup / P::kE) == 0)
+            scales[p * (kSpan / (int)kKeepGroup)] =
+                fine ? amax * (1.f / 127.f) : amax < kTiny ? 0.f : __uint_as_float(0x7FC00000u);
+        }
+      }
+      if (live && left > p * kSpan) {
+#pragma unroll
+        for (int e = 0; e < P::kPairs; ++e) v[p][e] = mul2(mul2(v[p][e], both(r)), w[p][e]);
+        store_part<VEC>(y + p * kSpan, left - p * kSpan, v[p]);
+      }
+    }
+    y += step * a.ld_y;
+    kept += step * groups * kKeepGroup;
+    scales += step * groups;
+    if constexpr (kStages == 0) ahead += step * a.ld_x;
+    stage = stage + 1 >= kStages ? 0 : stage + 1;
+    flip ^= 1;
+  }
+}
+
+// ---- backward ------------------------------------------------------------------
+
+// What a block of the backward pass holds in shared memory: the weight, and
+// rows of dy, the 8-bit input and its scales copied ahead.  Where not even two
+// rows fit (fp32 rows of more than 16,384) nothing is copied ahead.
+template <typename T, int G, int NV, bool VEC>
+struct NormBack {
+  static constexpr int kThreads = kBlock<G>;
+  static constexpr int kParts = NV * 8 / Part<T>::kE;
+  static constexpr int kStage = kThreads * kParts * (16 + Part<T>::kE + 4);
+  static constexpr bool kHoldWeight = kThreads * NV * 32 + 2 * kStage <= kSharedMost;
+  static constexpr int kWeight = kHoldWeight ? kThreads * NV * 32 : 0;
+  static constexpr int kFit = (kSharedMost - kWeight) / kStage;
+  static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kBackStages ? kFit : kBackStages) : 0;
+  static constexpr int kShared = kWeight + kStages * kStage;
+  static constexpr int kPerSm = blocks_per_sm(kBackThreads, kThreads, kShared);
+};
 
 // Rows are dealt to the blocks in turn; a thread keeps the weight gradient of
 // its columns in registers over all of its rows, and each block writes one
 // row of partial sums, which norm_dweight_kernel adds in a fixed order.
+// Bandwidth bound: rows are copied ahead into shared memory (aligned rows,
+// VEC) while the current one is reduced.
 template <typename T, int G, int NV, bool VEC>
 __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGradArgs a) {
-  constexpr int kRows = kBlock<G> / G;
-  __shared__ float red[kBlock<G> / 32][2];
+  using B = NormBack<T, G, NV, VEC>;
+  using P = Part<T>;
+  constexpr int kThreads = B::kThreads, kRows = kThreads / G, kStages = B::kStages;
+  constexpr int kParts = B::kParts;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[2][kThreads / 32][2];
   pdl_wait_then_release();
   const int tid = threadIdx.x, t = tid % G;
-  const size_t groups = (a.dim + kKeepGroup - 1) / kKeepGroup;
-  float acc[NV][8];
+  constexpr int kSpan = G * P::kE;  // columns from a thread's part to its next
+  const int dim = (int)a.dim, left = dim - t * P::kE;
+  const int groups = (dim + (int)kKeepGroup - 1) / (int)kKeepGroup;
+  const float inv_dim = 1.f / (float)dim;
+  size_t row = (size_t)blockIdx.x * kRows + tid / G;
+  const size_t step = (size_t)gridDim.x * kRows;
+  // this thread's first part of the row that is copied ahead, and of its output
+  const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + t * P::kE;
+  const int8_t* kept = a.kept + row * groups * kKeepGroup + t * P::kE;
+  const float* scales = a.scales + row * groups + t * P::kE / (int)kKeepGroup;
+  T* dx_out = static_cast<T*>(a.dx) + row * a.ld_dx + t * P::kE;
+  size_t ahead_row = row;
+  // what neighbouring threads hold of one kind lies side by side
+  auto weight_at = [&](int p, int h) {
+    return reinterpret_cast<float4*>(smem) + (p * P::kBytes8 + h) * kThreads + tid;
+  };
+  auto dy_at = [&](int s, int p) {
+    return reinterpret_cast<uint4*>(smem + B::kWeight + s * B::kStage) + p * kThreads + tid;
+  };
+  auto q_at = [&](int s, int p) {
+    return reinterpret_cast<uint32_t*>(smem + B::kWeight + s * B::kStage +
+                                       kThreads * kParts * 16) +
+           (p * kThreads + tid) * P::kBytes8;
+  };
+  auto scale_at = [&](int s, int p) {
+    return reinterpret_cast<float*>(smem + B::kWeight + s * B::kStage +
+                                    kThreads * kParts * (16 + P::kE)) + p * kThreads + tid;
+  };
+  auto weight = [&](int p, float2 (&w)[P::kPairs]) {
+    if constexpr (B::kHoldWeight) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
-  for (size_t first = (size_t)blockIdx.x * kRows; first < a.tokens;
-       first += (size_t)gridDim.x * kRows) {
-    const size_t row = first + tid / G;
-    const bool live = row < a.tokens;
-    const T* dy = static_cast<const T*>(a.dy) + (live ? row : 0) * a.ld_dy;
-    float x[NV][8], d[NV][8];
-    float sum[2] = {0.f, 0.f};  // of x'^2, of dy w x'
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const size_t col = (size_t)(k * G + t) * 8;
-      if (live && col < a.dim) {
-        load_row8<VEC>(dy, col, a.dim, d[k]);
-        const uint2 q = *reinterpret_cast<const uint2*>(
-            a.kept + row * groups * kKeepGroup + col);
-        const float s = a.scales[row * groups + col / kKeepGroup];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[k][e] = (float)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3))) * s;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = d[k][e] = 0.f;
+      for (int h = 0; h < P::kBytes8; ++h) {
+        const float4 f = *weight_at(p, h);
+        w[2 * h] = make_float2(f.x, f.y);
+        w[2 * h + 1] = make_float2(f.z, f.w);
       }
-      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (col < a.dim) load_row8<VEC>(a.weight, col, a.dim, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[0] = fmaf(x[k][e], x[k][e], sum[0]);
-        sum[1] = fmaf(d[k][e] * w[e], x[k][e], sum[1]);
-      }
+    } else {
+      load_weight<VEC>(a.weight + t * P::kE + p * kSpan, left - p * kSpan, w);
     }
-    row_sum<G>(sum, red, tid);
-    const float r = __frsqrt_rn(sum[0] / (float)a.dim + a.eps);
-    const float m = sum[1] * r / (float)a.dim;  // mean of dy w n
+  };
+  auto next_row = [&]() {
+    dy += step * a.ld_dy;
+    kept += step * groups * kKeepGroup;
+    scales += step * groups;
+    ahead_row += step;
+  };
+  auto copy_row = [&](int s) {
+    if (ahead_row < a.tokens) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const size_t col = (size_t)(k * G + t) * 8;
-      if (live && col < a.dim) {
-        float w[8];
-        load_row8<VEC>(a.weight, col, a.dim, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = x[k][e] * r;
-          acc[k][e] = fmaf(d[k][e], n, acc[k][e]);
-          d[k][e] = r * (d[k][e] * w[e] - n * m);
+      for (int p = 0; p < kParts; ++p) {
+        if (left > p * kSpan) {
+          copy_async<16>(dy_at(s, p), dy + p * kSpan);
+          copy_async<P::kE>(q_at(s, p), kept + p * kSpan);
+          copy_async<4>(scale_at(s, p), scales + p * (kSpan / (int)kKeepGroup));
         }
-        store_row8<VEC>(static_cast<T*>(a.dx) + row * a.ld_dx, col, a.dim, d[k]);
       }
     }
+    copies_commit();  // one group a row, also when there is none
+    next_row();
+  };
+
+  for (int s = 0; s < kStages - 1; ++s) copy_row(s);
+  float2 acc[kParts][P::kPairs];
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    if (B::kHoldWeight && left > p * kSpan) {
+      float2 w[P::kPairs];
+      load_weight<VEC>(a.weight + t * P::kE + p * kSpan, left - p * kSpan, w);
+#pragma unroll
+      for (int h = 0; h < P::kBytes8; ++h)
+        *weight_at(p, h) = make_float4(w[2 * h].x, w[2 * h].y, w[2 * h + 1].x, w[2 * h + 1].y);
+    }
+#pragma unroll
+    for (int e = 0; e < P::kPairs; ++e) acc[p][e] = both(0.f);
+  }
+  int stage = 0, flip = 0;
+  for (size_t first = (size_t)blockIdx.x * kRows; first < a.tokens; first += step, row += step) {
+    const bool live = kRows == 1 || row < a.tokens;
+    if constexpr (kStages > 0) {
+      copy_row(stage == 0 ? kStages - 1 : stage - 1);
+      copies_wait<kStages - 1>();
+    }
+    // kept over the reduction: dy w, and dy and the bytes as they came
+    uint4 raw[kParts];
+    uint32_t q[kParts][P::kBytes8];
+    float2 dw[kParts][P::kPairs];
+    float scale[kParts];
+    float2 xx = both(0.f), dx = both(0.f);  // sums of x'^2, of dy w x'
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      if (live && left > p * kSpan) {
+        const uint32_t* bytes;
+        if constexpr (kStages > 0) {
+          raw[p] = *dy_at(stage, p);
+          bytes = q_at(stage, p);
+          scale[p] = *scale_at(stage, p);
+        } else {
+          raw[p] = load_part<VEC>(dy + p * kSpan, left - p * kSpan);
+          bytes = reinterpret_cast<const uint32_t*>(kept + p * kSpan);
+          scale[p] = scales[p * (kSpan / (int)kKeepGroup)];
+        }
+        if constexpr (P::kBytes8 == 2) {
+          const uint2 two = *reinterpret_cast<const uint2*>(bytes);
+          q[p][0] = two.x;
+          q[p][P::kBytes8 - 1] = two.y;
+        } else {
+          q[p][0] = bytes[0];
+        }
+        float2 x[P::kPairs], d[P::kPairs], w[P::kPairs], qq = both(0.f), dq = both(0.f);
+        weight(p, w);
+        widen(raw[p], d, T());
+#pragma unroll
+        for (int i = 0; i < P::kBytes8; ++i) widen4(q[p][i], x[2 * i], x[2 * i + 1]);
+#pragma unroll
+        for (int e = 0; e < P::kPairs; ++e) {  // of whole numbers; the group's scale comes after
+          dw[p][e] = mul2(d[e], w[e]);
+          qq = fma2(x[e], x[e], qq);
+          dq = fma2(dw[p][e], x[e], dq);
+        }
+        xx = fma2(qq, both(scale[p] * scale[p]), xx);
+        dx = fma2(dq, both(scale[p]), dx);
+      }
+    }
+    float sum[2] = {xx.x + xx.y, dx.x + dx.y};
+    row_sum<G>(sum, red[flip], tid);
+    const float r = rsqrtf(fmaf(sum[0], inv_dim, a.eps));
+    const float m = sum[1] * r * inv_dim;  // mean of dy w n
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      if (live && left > p * kSpan) {
+        float2 x[P::kPairs], d[P::kPairs], out[P::kPairs];
+        widen(raw[p], d, T());
+#pragma unroll
+        for (int i = 0; i < P::kBytes8; ++i) widen4(q[p][i], x[2 * i], x[2 * i + 1]);
+        const float rs = r * scale[p];
+#pragma unroll
+        for (int e = 0; e < P::kPairs; ++e) {
+          const float2 n = mul2(x[e], both(rs));
+          acc[p][e] = fma2(d[e], n, acc[p][e]);
+          out[e] = mul2(fma2(n, both(-m), dw[p][e]), both(r));
+        }
+        store_part<VEC>(dx_out + p * kSpan, left - p * kSpan, out);
+      }
+    }
+    dx_out += step * a.ld_dx;
+    if constexpr (kStages == 0) next_row();
+    stage = stage + 1 >= kStages ? 0 : stage + 1;
+    flip ^= 1;
   }
   // one row of partial sums for each group of threads
+  const int ld = groups * (int)kKeepGroup;
   float* part = static_cast<float*>(a.workspace) +
-                ((size_t)blockIdx.x * kRows + tid / G) * groups * kKeepGroup;
+                ((size_t)blockIdx.x * kRows + tid / G) * ld + t * P::kE;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const size_t col = (size_t)(k * G + t) * 8;
-    if (col < groups * kKeepGroup) store8(part + col, acc[k]);
-  }
+  for (int p = 0; p < kParts; ++p)
+    if (ld - t * P::kE > p * kSpan)
+#pragma unroll
+      for (int e = 0; e < P::kPairs; e += 2)
+        *reinterpret_cast<float4*>(part + p * kSpan + 2 * e) =
+            make_float4(acc[p][e].x, acc[p][e].y, acc[p][e + 1].x, acc[p][e + 1].y);
 }
 
 constexpr int kSumCols = 32, kSumRows = 32;
@@ -201,75 +516,97 @@ __global__ void __launch_bounds__(kSumCols* kSumRows)
   const int c = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
   const size_t col = (size_t)blockIdx.x * kSumCols + c;
   float s = 0.f;
-  if (col < dim)
-    for (size_t r = y; r < rows; r += kSumRows) s += part[r * ld + col];
+  if (col < dim) {
+    const float* p = part + y * ld + col;
+    size_t r = y;
+    for (; r + 7 * kSumRows < rows; r += 8 * kSumRows) {  // eight loads under way
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[i * kSumRows * ld];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+      p += 8 * kSumRows * ld;
+    }
+    for (; r < rows; r += kSumRows, p += kSumRows * ld) s += *p;
+  }
   red[y][c] = s;
   __syncthreads();
   if (y == 0 && col < dim) {
+#pragma unroll
     for (int i = 1; i < kSumRows; ++i) s += red[i][c];
     dweight[col] = accumulate ? dweight[col] + s : s;
   }
 }
 
-// Threads that share a row, and vectors of eight columns for each
+// Threads that share a row, and how often eight columns each of them holds
 struct NormShape {
   int g, nv;
 };
 NormShape norm_shape(size_t dim) {
   const size_t vecs = (dim + 7) / 8;
-  if (vecs <= 32) return {32, 1};
-  if (vecs <= 64) return {32, 2};
-  if (vecs <= 128) return {64, 2};
-  if (vecs <= 256) return {128, 2};
-  if (vecs <= 512) return {256, 2};
-  if (vecs <= 1024) return {256, 4};
-  if (vecs <= 2048) return {512, 4};
-  return {1024, 4};
+  int g = 32;
+  while (g < 1024 && (size_t)g * 2 < vecs) g *= 2;
+  return {g, (size_t)g >= vecs ? 1 : (size_t)g * 2 >= vecs ? 2 : 4};
 }
 
 int norm_threads(const NormShape& s) { return s.g > 256 ? s.g : 256; }
 int norm_rows_per_block(const NormShape& s) { return norm_threads(s) / s.g; }
 
-// blocks of the backward pass: every SM filled once with 1,024 threads
-size_t norm_backward_blocks(size_t tokens, const NormShape& s) {
+// blocks that the rows need, at most what fills every SM once
+size_t norm_blocks(size_t tokens, const NormShape& s, int per_sm) {
   const size_t rows = norm_rows_per_block(s);
-  const size_t need = (tokens + rows - 1) / rows;
-  const size_t fill = (size_t)sm_count() * (1024 / norm_threads(s));
+  const size_t need = (tokens + rows - 1) / rows, fill = (size_t)sm_count() * per_sm;
   return need < fill ? need : fill;
 }
 
 template <typename F>
 cudaError_t with_shape(const NormShape& s, F f) {
-  if (s.g == 32 && s.nv == 1) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-  if (s.g == 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-  if (s.g == 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-  if (s.g == 128) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
-  if (s.g == 256 && s.nv == 2) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-  if (s.g == 256) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
-  if (s.g == 512) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+  using Two = std::integral_constant<int, 2>;
+  switch (s.g) {
+    case 32:
+      if (s.nv == 1)
+        return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+      return f(std::integral_constant<int, 32>(), Two());
+    case 64: return f(std::integral_constant<int, 64>(), Two());
+    case 128: return f(std::integral_constant<int, 128>(), Two());
+    case 256: return f(std::integral_constant<int, 256>(), Two());
+    case 512: return f(std::integral_constant<int, 512>(), Two());
+  }
+  if (s.nv == 2) return f(std::integral_constant<int, 1024>(), Two());
   return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
 }
 
 template <typename T, bool VEC>
 cudaError_t forward_of(const NormArgs& a, cudaStream_t stream) {
   const NormShape s = norm_shape(a.dim);
-  const size_t rows = norm_rows_per_block(s);
   return with_shape(s, [&](auto g, auto nv) {
-    constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
-    return launch_kernel(norm_forward_kernel<T, G, NV, VEC>,
-                         dim3((unsigned)((a.tokens + rows - 1) / rows)), dim3(kBlock<G>), 0,
-                         stream, a);
+    using F = NormFore<T, decltype(g)::value, decltype(nv)::value, VEC>;
+    auto kernel = norm_forward_kernel<T, decltype(g)::value, decltype(nv)::value, VEC>;
+    if (F::kShared > 40 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kShared);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(kernel, dim3((unsigned)norm_blocks(a.tokens, s, F::kPerSm)),
+                         dim3(F::kThreads), F::kShared, stream, a);
   });
 }
 
+// *blocks: blocks launched, each of which leaves its rows of partial sums
 template <typename T, bool VEC>
-cudaError_t backward_of(const NormGradArgs& a, cudaStream_t stream) {
+cudaError_t backward_of(const NormGradArgs& a, cudaStream_t stream, size_t* blocks) {
   const NormShape s = norm_shape(a.dim);
   return with_shape(s, [&](auto g, auto nv) {
-    constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
-    return launch_kernel(norm_backward_kernel<T, G, NV, VEC>,
-                         dim3((unsigned)norm_backward_blocks(a.tokens, s)), dim3(kBlock<G>), 0,
-                         stream, a);
+    constexpr int G = decltype(g)::value;
+    using B = NormBack<T, G, decltype(nv)::value, VEC>;
+    auto kernel = norm_backward_kernel<T, G, decltype(nv)::value, VEC>;
+    if (B::kShared > 40 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, B::kShared);
+      if (e != cudaSuccess) return e;
+    }
+    *blocks = norm_blocks(a.tokens, s, B::kPerSm);
+    return launch_kernel(kernel, dim3((unsigned)*blocks), dim3(B::kThreads), B::kShared, stream, a);
   });
 }
 
@@ -284,24 +621,27 @@ cudaError_t launch_rmsnorm_forward(const NormArgs& a, cudaStream_t stream) {
 size_t rmsnorm_backward_workspace(size_t tokens, size_t dim) {
   const NormShape s = norm_shape(dim);
   const size_t ld = (dim + kKeepGroup - 1) / kKeepGroup * kKeepGroup;
-  return norm_backward_blocks(tokens, s) * norm_rows_per_block(s) * ld * sizeof(float);
+  const int most = std::max(1, kBackThreads / norm_threads(s));
+  return norm_blocks(tokens, s, most) * norm_rows_per_block(s) * ld * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_backward(const NormGradArgs& a, cudaStream_t stream,
                                     uint64_t* launches) {
   cudaError_t e;
+  size_t blocks = 0;
   if (a.type == RCC_F32)
-    e = a.vec ? backward_of<float, true>(a, stream) : backward_of<float, false>(a, stream);
+    e = a.vec ? backward_of<float, true>(a, stream, &blocks)
+              : backward_of<float, false>(a, stream, &blocks);
   else
-    e = a.vec ? backward_of<__nv_bfloat16, true>(a, stream)
-              : backward_of<__nv_bfloat16, false>(a, stream);
+    e = a.vec ? backward_of<__nv_bfloat16, true>(a, stream, &blocks)
+              : backward_of<__nv_bfloat16, false>(a, stream, &blocks);
   if (e != cudaSuccess) return e;
   const NormShape s = norm_shape(a.dim);
   const size_t ld = (a.dim + kKeepGroup - 1) / kKeepGroup * kKeepGroup;
   e = launch_kernel(norm_dweight_kernel, dim3((unsigned)((a.dim + kSumCols - 1) / kSumCols)),
                     dim3(kSumCols * kSumRows), 0, stream,
                     static_cast<const float*>(a.workspace),
-                    norm_backward_blocks(a.tokens, s) * (size_t)norm_rows_per_block(s), ld,
+                    blocks * norm_rows_per_block(s), ld,
                     a.dweight, a.dim, a.accumulate);
   if (e == cudaSuccess) *launches = 2;
   return e;

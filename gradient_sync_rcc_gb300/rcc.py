@@ -418,253 +418,20 @@ def grad_stats_noalloc(grads, loss_scale, report, mean_grad=None, stream=None):
 
 # ------------------------------------------------------------- language-model operators
 
-# The C calls receive bare pointers, sizes and strides; what they cannot see
-# (a type, a device, a shape that does not fit) is checked here.  An output or
-# a workspace that is not passed is allocated on the inputs' device, to be used
-# on `stream`.
-
-def _type(t, what):
-    import torch
-    if t == torch.bfloat16:
-        return BF16
-    if t == torch.float32:
-        return F32
-    raise ValueError("%s must be float32 or bfloat16, not %s" % (what, t))
+# embedding_forward, rmsnorm_forward, linear_ce_forward and the rest live in
+# lm.py, which needs torch at import; the first use of a name brings it here.
+_LM_NAMES = ("embedding_forward", "embedding_backward", "embedding_backward_workspace",
+             "KEEP_GROUP", "Kept", "rmsnorm_forward", "rmsnorm_backward",
+             "rmsnorm_backward_workspace", "linear_ce_forward", "linear_ce_backward",
+             "linear_ce_workspace")
 
 
-def _index(t, what):
-    import torch
-    if t.dtype == torch.int64:
-        return I64
-    if t.dtype == torch.int32:
-        return I32
-    raise ValueError("%s must be int32 or int64, not %s" % (what, t.dtype))
-
-
-def _rows(t, what, dev, rows=None, dim=None):
-    """Checks a matrix whose rows are contiguous; returns its row stride."""
-    if t.dim() != 2 or t.device != dev:
-        raise ValueError("%s must be a matrix on %s" % (what, dev))
-    n, d = t.shape
-    if (rows is not None and n != rows) or (dim is not None and d != dim):
-        raise ValueError("%s is %d x %d where %s x %s is needed"
-                         % (what, n, d, "any" if rows is None else rows,
-                            "any" if dim is None else dim))
-    if d != 1 and t.stride(1) != 1:
-        raise ValueError("the rows of %s must be contiguous" % what)
-    if n > 1 and t.stride(0) < d:
-        raise ValueError("the rows of %s overlap" % what)
-    return t.stride(0) if n > 1 else d
-
-
-def _vector(t, what, dev, n, dtype=None):
-    if t.dim() != 1 or t.device != dev or t.numel() != n or not t.is_contiguous() or \
-            (dtype is not None and t.dtype != dtype):
-        raise ValueError("%s must be a contiguous vector of %d%s on %s"
-                         % (what, n, "" if dtype is None else " " + str(dtype), dev))
-
-
-def _on_gpu(t):
-    if not t.is_cuda:
-        raise ValueError("the operators take tensors on a CUDA device, not on %s" % t.device)
-
-
-def _output(t, what, like, shape, dtype):
-    """The caller's output, checked, or a new one."""
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device or \
-            not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (what, dtype, tuple(shape), like.device))
-    return t
-
-
-def _workspace(t, like, need):
-    import torch
-    if t is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
-    if t.device != like.device or not t.is_contiguous():
-        raise ValueError("the workspace must be a contiguous tensor on %s" % like.device)
-    return t
-
-
-def embedding_forward(table, ids, scale=1.0, out=None, out_dtype=None, stream=None):
-    """rcc_embedding_forward: scale * table[ids], a row of zeros for an id
-    outside the table.  Returns out [tokens, dim] of out_dtype (the table's)."""
-    dev = table.device
-    ld = _rows(table, "table", dev)
-    vocab, dim = table.shape
-    _vector(ids, "ids", dev, ids.numel())
-    out = _output(out, "out", table, (ids.numel(), dim),
-                  (table.dtype if out_dtype is None else out_dtype) if out is None else out.dtype)
-    _on_gpu(table)
-    _check(lib().rcc_embedding_forward(
-        table.data_ptr(), _type(table.dtype, "table"), ld, ids.data_ptr(), _index(ids, "ids"),
-        ids.numel(), vocab, dim, scale, out.data_ptr(), _type(out.dtype, "out"),
-        _stream(stream)))
-    return out
-
-
-def embedding_backward_workspace(tokens, vocab, dim):
-    return int(lib().rcc_embedding_backward_workspace(tokens, vocab, dim))
-
-
-def embedding_backward(dout, ids, dtable, scale=1.0, accumulate=False, workspace=None,
-                       stream=None):
-    """rcc_embedding_backward: the gradient of embedding_forward's table, into
-    dtable [vocab, dim] (added to it with accumulate).  Returns dtable."""
-    dev = dout.device
-    vocab, dim = dtable.shape
-    ld = _rows(dout, "dout", dev, dim=dim)
-    tokens = dout.shape[0]
-    _vector(ids, "ids", dev, tokens)
-    _output(dtable, "dtable", dout, (vocab, dim), dtable.dtype)
-    ws = _workspace(workspace, dout, embedding_backward_workspace(tokens, vocab, dim))
-    _on_gpu(dout)
-    _check(lib().rcc_embedding_backward(
-        dout.data_ptr(), _type(dout.dtype, "dout"), ld, ids.data_ptr(), _index(ids, "ids"),
-        tokens, vocab, dim, scale, dtable.data_ptr(), _type(dtable.dtype, "dtable"),
-        int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
-    return dtable
-
-
-KEEP_GROUP = 128   # columns that share one scale of the 8-bit form
-
-
-class Kept:
-    """A norm's input in 8 bits: values [tokens, 128 G] int8 and scales
-    [tokens, G] float32 of its `dim` columns, G = ceil(dim / 128)."""
-
-    __slots__ = ("values", "scales", "dim")
-
-    def __init__(self, values, scales, dim):
-        self.values, self.scales, self.dim = values, scales, dim
-
-    @classmethod
-    def empty(cls, tokens, dim, device):
-        import torch
-        groups = -(-dim // KEEP_GROUP)
-        return cls(torch.empty(tokens, groups * KEEP_GROUP, dtype=torch.int8, device=device),
-                   torch.empty(tokens, groups, dtype=torch.float32, device=device), dim)
-
-    def dequantize(self):
-        """What it stands for, [tokens, dim] float32."""
-        t, g = self.scales.shape
-        v = self.values.view(t, g, KEEP_GROUP) * self.scales[:, :, None]
-        return v.view(t, g * KEEP_GROUP)[:, :self.dim]
-
-    def _checked(self, tokens, dim, like):
-        import torch
-        groups = -(-dim // KEEP_GROUP)
-        if self.dim != dim:
-            raise ValueError("kept holds %d columns where %d are needed" % (self.dim, dim))
-        _output(self.values, "kept.values", like, (tokens, groups * KEEP_GROUP), torch.int8)
-        _output(self.scales, "kept.scales", like, (tokens, groups), torch.float32)
-        return self.values.data_ptr(), self.scales.data_ptr()
-
-
-def rmsnorm_forward(x, weight, eps=1e-6, keep=False, out=None, stream=None):
-    """rcc_rmsnorm_forward.  Returns y, or (y, kept) with keep: True, or a Kept
-    to be written."""
-    import torch
-    dev = x.device
-    ld = _rows(x, "x", dev)
-    tokens, dim = x.shape
-    _vector(weight, "weight", dev, dim, torch.float32)
-    y = _output(out, "out", x, (tokens, dim), x.dtype)
-    kept = Kept.empty(tokens, dim, dev) if keep is True else keep or None
-    q, s = (None, None) if kept is None else kept._checked(tokens, dim, x)
-    _on_gpu(x)
-    _check(lib().rcc_rmsnorm_forward(x.data_ptr(), _type(x.dtype, "x"), ld, weight.data_ptr(),
-                                     eps, tokens, dim, y.data_ptr(), q, s, _stream(stream)))
-    return y if kept is None else (y, kept)
-
-
-def rmsnorm_backward_workspace(tokens, dim):
-    return int(lib().rcc_rmsnorm_backward_workspace(tokens, dim))
-
-
-def rmsnorm_backward(dy, kept, weight, eps=1e-6, dx=None, dweight=None, accumulate=False,
-                     workspace=None, stream=None):
-    """rcc_rmsnorm_backward from a Kept.  Returns (dx, dweight); with accumulate
-    dweight is passed and added to."""
-    import torch
-    dev = dy.device
-    ld = _rows(dy, "dy", dev)
-    tokens, dim = dy.shape
-    q, s = kept._checked(tokens, dim, dy)
-    _vector(weight, "weight", dev, dim, torch.float32)
-    if accumulate and dweight is None:
-        raise ValueError("accumulate needs the dweight to add to")
-    dx = _output(dx, "dx", dy, (tokens, dim), dy.dtype)
-    dweight = _output(dweight, "dweight", dy, (dim,), torch.float32)
-    ws = _workspace(workspace, dy, rmsnorm_backward_workspace(tokens, dim))
-    _on_gpu(dy)
-    _check(lib().rcc_rmsnorm_backward(
-        dy.data_ptr(), _type(dy.dtype, "dy"), ld, q, s, weight.data_ptr(), eps, tokens, dim,
-        dx.data_ptr(), dweight.data_ptr(), int(accumulate), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream)))
-    return dx, dweight
-
-
-def linear_ce_workspace(tokens, vocab, dim, backward=False, grad_dtype=None):
-    grad = BF16 if grad_dtype is None else _type(grad_dtype, "grad_dtype")
-    return int(lib().rcc_linear_ce_workspace(tokens, vocab, dim, int(backward), grad))
-
-
-def _ce_inputs(x, w, labels):
-    import torch
-    dev = x.device
-    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
-        raise ValueError("x and w must be bfloat16")
-    ld_x, ld_w = _rows(x, "x", dev), _rows(w, "w", dev, dim=x.shape[1])
-    _vector(labels, "labels", dev, x.shape[0])
-    return ld_x, ld_w, _index(labels, "labels"), x.shape[0], w.shape[0], x.shape[1]
-
-
-def linear_ce_forward(x, w, labels, loss=None, lse=None, workspace=None, stream=None):
-    """rcc_linear_ce_forward: softmax cross entropy of the logits x w^T.
-    Returns (loss, lse), [tokens] float32 each."""
-    import torch
-    ld_x, ld_w, index, tokens, vocab, dim = _ce_inputs(x, w, labels)
-    loss = _output(loss, "loss", x, (tokens,), torch.float32)
-    lse = _output(lse, "lse", x, (tokens,), torch.float32)
-    ws = _workspace(workspace, x, linear_ce_workspace(tokens, vocab, dim))
-    _on_gpu(x)
-    _check(lib().rcc_linear_ce_forward(
-        x.data_ptr(), ld_x, w.data_ptr(), ld_w, labels.data_ptr(), index, tokens, vocab, dim,
-        loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-        _stream(stream)))
-    return loss, lse
-
-
-def linear_ce_backward(x, w, labels, lse, dloss, grad_dtype=None, dx=None, dw=None,
-                       accumulate=False, workspace=None, need_dx=True, need_dw=True,
-                       stream=None):
-    """rcc_linear_ce_backward: gradients of sum(dloss * loss).  Returns (dx, dw)
-    of grad_dtype (a passed output's, else bfloat16); None for one that is not
-    needed.  With accumulate dw is passed and added to."""
-    import torch
-    ld_x, ld_w, index, tokens, vocab, dim = _ce_inputs(x, w, labels)
-    _vector(lse, "lse", x.device, tokens, torch.float32)
-    _vector(dloss, "dloss", x.device, tokens, torch.float32)
-    if accumulate and dw is None:
-        raise ValueError("accumulate needs the dw to add to")
-    if grad_dtype is None:
-        given = dx if dx is not None else dw
-        grad_dtype = torch.bfloat16 if given is None else given.dtype
-    grad = _type(grad_dtype, "grad_dtype")
-    dx = _output(dx, "dx", x, (tokens, dim), grad_dtype) if need_dx else None
-    dw = _output(dw, "dw", x, (vocab, dim), grad_dtype) if need_dw else None
-    ws = _workspace(workspace, x, linear_ce_workspace(tokens, vocab, dim, True, grad_dtype))
-    _on_gpu(x)
-    _check(lib().rcc_linear_ce_backward(
-        x.data_ptr(), ld_x, w.data_ptr(), ld_w, labels.data_ptr(), index, lse.data_ptr(),
-        dloss.data_ptr(), tokens, vocab, dim, _ptr(dx), _ptr(dw), grad, int(accumulate),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
-    return dx, dw
+def __getattr__(name):
+    if name in _LM_NAMES:
+        from gradient_sync_rcc_gb300 import lm
+        globals().update((n, getattr(lm, n)) for n in _LM_NAMES)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 # ------------------------------------------------------------- raw calls (status only)
