@@ -93,6 +93,14 @@ struct GradPlan {
   int passes, bits;       // digits, and bits of each
 };
 
+// the list after its last digit
+__device__ __forceinline__ const uint32_t* sorted_keys(const GradPlan& p) {
+  return p.passes & 1 ? p.keys[1] : p.keys[0];
+}
+__device__ __forceinline__ const uint32_t* sorted_order(const GradPlan& p) {
+  return p.passes & 1 ? p.order[1] : p.order[0];
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -111,6 +119,7 @@ __global__ void __launch_bounds__(kSortThreads)
   uint32_t* counts = sm;                          // [warps][digits]
   uint32_t* total = sm + kSortWarps * kDigits;    // [digits]: this block's
   uint32_t* base = total + kDigits;               // [digits]
+  __shared__ uint32_t warp_total[kDigits / 32];
   pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x;  // the grid is one cluster
@@ -129,10 +138,10 @@ __global__ void __launch_bounds__(kSortThreads)
 
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
-    const uint32_t* kin = p.keys[pass & 1];
-    const uint32_t* oin = p.order[pass & 1];
-    uint32_t* kout = p.keys[(pass & 1) ^ 1];
-    uint32_t* oout = p.order[(pass & 1) ^ 1];
+    const uint32_t* kin = pass & 1 ? p.keys[1] : p.keys[0];
+    const uint32_t* oin = pass & 1 ? p.order[1] : p.order[0];
+    uint32_t* kout = pass & 1 ? p.keys[0] : p.keys[1];
+    uint32_t* oout = pass & 1 ? p.order[0] : p.order[1];
     uint32_t* mine = counts + warp * kDigits;
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
@@ -147,50 +156,57 @@ __global__ void __launch_bounds__(kSortThreads)
       atomicAdd(&mine[(key >> shift) & (digits - 1)], 1u);
     }
     __syncthreads();
-    // counts of the warps before this one, and the block's totals
-    for (int d = tid; d < digits; d += kSortThreads) {
-      uint32_t s = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = counts[w * kDigits + d];
-        counts[w * kDigits + d] = s;
-        s += c;
+    // counts of the warps before this one, and the block's totals: two threads
+    // a digit, 16 warps each (every thread takes part in the exchange)
+    {
+      static_assert(kSortThreads == 2 * kDigits, "two threads a digit");
+      const int d = tid >> 1;
+      uint32_t* c = counts + (tid & 1) * (kSortWarps / 2) * kDigits + d;
+      uint32_t v[kSortWarps / 2], s = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps / 2; ++w) v[w] = d < digits ? c[w * kDigits] : 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps / 2; ++w) s += v[w];
+      const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+      uint32_t run = tid & 1 ? other : 0;
+      if (d < digits) {
+#pragma unroll
+        for (int w = 0; w < kSortWarps / 2; ++w) {
+          c[w * kDigits] = run;
+          run += v[w];
+        }
+        if (tid & 1) total[d] = run;
       }
-      total[d] = s;
     }
     cluster_sync();
     // places before this block's first of each digit: smaller digits of all
     // blocks, and the same digit of earlier blocks
-    if (tid < digits) {
-      uint32_t before = 0, all = 0;
-      for (int b = 0; b < kSortBlocks; ++b) {
-        const uint32_t c = peer_word(&total[tid], b);
-        before += b < rank ? c : 0;
-        all += c;
-      }
-      base[tid] = all;
-      counts[tid] += before;  // warp 0's row holds zeros: it carries the block's offset
-    }
-    __syncthreads();
-    // exclusive prefix sum of base over the digits (at most 512), by warp 0
-    if (warp == 0) {
-      uint32_t run = 0;
-      for (int d0 = 0; d0 < digits; d0 += 32) {
-        const uint32_t c = d0 + lane < digits ? base[d0 + lane] : 0;
-        uint32_t s = c;
+    uint32_t before = 0, all = 0, upto = 0;
+    if (tid < kDigits) {  // whole warps
+      if (tid < digits) {
+        uint32_t c[kSortBlocks];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-          if (lane >= o) s += u;
+        for (int b = 0; b < kSortBlocks; ++b) c[b] = peer_word(&total[tid], b);
+#pragma unroll
+        for (int b = 0; b < kSortBlocks; ++b) {
+          before += b < rank ? c[b] : 0;
+          all += c[b];
         }
-        if (d0 + lane < digits) base[d0 + lane] = run + s - c;
-        run += __shfl_sync(0xFFFFFFFFu, s, 31);
       }
+      upto = all;  // with the digits before it in the warp
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      if (lane == 31) warp_total[warp] = upto;
     }
     __syncthreads();
-    for (int d = tid; d < digits; d += kSortThreads) {
-      const uint32_t before = counts[d];  // earlier blocks
-      base[d] += before;
-      counts[d] = 0;
+    if (tid < digits) {
+      uint32_t s = upto - all + before;
+#pragma unroll
+      for (int w = 0; w < kDigits / 32; ++w) s += w < warp ? warp_total[w] : 0;
+      base[tid] = s;
     }
     __syncthreads();
     for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
@@ -223,7 +239,7 @@ __global__ void __launch_bounds__(kSortThreads)
   }
 
   // items: runs of one key, cut where a window ends
-  const uint32_t* keys = p.keys[p.passes & 1];
+  const uint32_t* keys = sorted_keys(p);
   for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
     const uint32_t i = i0 + lane;
     bool starts = false;
@@ -243,81 +259,159 @@ __global__ void __launch_bounds__(kSortThreads)
 
 // ---- the sums --------------------------------------------------------------------
 
+// G threads take one slab of 8 G columns of a row or an item; a block has
+// kRowThreads / G such groups.
+template <int G>
+struct Groups {
+  static constexpr int kCount = kRowThreads / G;
+  static constexpr int kColumns = G * 8;
+};
+
+// The sum of an item's rows of dout, in the order of the list.  The places are
+// read 32 at a time, the rows four at a time.
+template <typename T, bool VEC>
+__device__ __forceinline__ void sum_item(const EmbedGradArgs& a, const uint32_t* keys,
+                                         const uint32_t* order, uint32_t key, uint32_t start,
+                                         uint32_t stop, size_t col, bool live, float (&s)[8],
+                                         uint32_t& end) {
+  const int lane = threadIdx.x & 31;
+  const T* dout = static_cast<const T*>(a.dout);
+  for (uint32_t i0 = start; i0 < stop; i0 += 32) {
+    const uint32_t i = i0 + lane;
+    const bool mine = i < stop && keys[i] == key;
+    const uint32_t tok = mine ? order[i] : 0;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine));  // a run: the first n lanes
+    for (int j = 0; j < n; j += 4) {
+      float v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t t = __shfl_sync(0xFFFFFFFFu, tok, j + u);
+        if (live && j + u < n) {
+          load_row8<VEC>(dout + (size_t)t * a.ld_dout, col, a.dim, v[u]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j + u < n) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+        }
+    }
+    end = i0 + n;
+    if (n < 32) break;
+  }
+}
+
 // Every row of dW without a token is set to zero (when not accumulating), and
-// every item is summed.  Work is (row or item, slab of columns), dealt to the
-// blocks in turn; which block takes which changes no result.
-template <typename T, typename G, bool VEC>
+// every item is summed.  Work is dealt to the blocks in turn; which block
+// takes which changes no result.  Half of the blocks begin with the zeros, so
+// that writing and summing overlap.
+template <typename T, typename O, bool VEC, int G>
 __global__ void __launch_bounds__(kRowThreads) sum_kernel(const EmbedGradArgs a, const GradPlan p) {
+  using Gr = Groups<G>;
   pdl_wait_then_release();
-  const size_t slabs = (a.dim + kSlab - 1) / kSlab;
-  const uint32_t* keys = p.keys[p.passes & 1];
-  const uint32_t* order = p.order[p.passes & 1];
+  const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
+  const uint32_t* keys = sorted_keys(p);
+  const uint32_t* order = sorted_order(p);
   const uint32_t tokens = (uint32_t)a.tokens;
+  const size_t group = (size_t)blockIdx.x * Gr::kCount + threadIdx.x / G;
+  const size_t all_groups = (size_t)gridDim.x * Gr::kCount;
+  const size_t lane_col = (threadIdx.x % G) * 8;
+
+  auto zeros = [&]() {
+    // a byte of the bit map, eight rows, at a time
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const size_t units = (a.vocab + 7) / 8 * slabs;
+    for (size_t j = group; j < units; j += all_groups) {
+      const size_t col = j % slabs * Gr::kColumns + lane_col, row0 = j / slabs * 8;
+      const uint32_t bits = reinterpret_cast<const uint8_t*>(p.present)[row0 / 8];
+      if (col >= a.dim) continue;
+      O* out = static_cast<O*>(a.dtable) + row0 * a.dim;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (row0 + r < a.vocab && !(bits >> r & 1u))
+          store_row8<VEC>(out + r * a.dim, col, a.dim, zero);
+    }
+  };
+  const bool zeros_first = blockIdx.x & 1;
+  if (!a.accumulate && zeros_first) zeros();
+
   const size_t items = (size_t)*p.count * slabs;
-  for (size_t j = blockIdx.x; j < items; j += gridDim.x) {
-    const size_t col = j % slabs * kSlab + threadIdx.x * 8;
-    if (col >= a.dim) continue;
+  for (size_t j = group; j < items; j += all_groups) {
+    const size_t col = j % slabs * Gr::kColumns + lane_col;
+    const bool live = col < a.dim;
     const uint32_t start = p.starts[j / slabs];
     const uint32_t key = keys[start];
     const uint32_t stop = min(tokens, (start / p.window + 1) * p.window);
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint32_t i = start;
-    for (; i < stop && keys[i] == key; ++i) {
-      float v[8];
-      load_row8<VEC>(static_cast<const T*>(a.dout) + (size_t)order[i] * a.ld_dout, col, a.dim, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += v[e];
-    }
     const bool before = start > 0 && keys[start - 1] == key;
-    const bool after = i < tokens && keys[i] == key;
+    const bool after = stop < tokens && keys[stop] == key && keys[stop - 1] == key;
+    O* out = static_cast<O*>(a.dtable) + (size_t)key * a.dim;
+    float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.accumulate && live && !before && !after) load_row8<VEC>(out, col, a.dim, old);
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint32_t end = start;
+    sum_item<T, VEC>(a, keys, order, key, start, stop, col, live, s, end);
+    if (!live) continue;
     if (before || after) {
       // a run that goes on: slot 2w when it comes from the window before, else 2w + 1
       store8(p.part + (size_t)(2 * (start / p.window) + (before ? 0 : 1)) *
                           ((a.dim + 7) / 8 * 8) + col, s);
     } else {
-      G* out = static_cast<G*>(a.dtable) + (size_t)key * a.dim;
-      float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a.accumulate) load_row8<VEC>(out, col, a.dim, old);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] = old[e] + s[e] * a.scale;
       store_row8<VEC>(out, col, a.dim, s);
     }
   }
-  if (a.accumulate) return;
-  const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (size_t j = blockIdx.x; j < a.vocab * slabs; j += gridDim.x) {
-    const size_t col = j % slabs * kSlab + threadIdx.x * 8, row = j / slabs;
-    if (col < a.dim && !(p.present[row / 32] >> (row % 32) & 1u))
-      store_row8<VEC>(static_cast<G*>(a.dtable) + row * a.dim, col, a.dim, zero);
-  }
+  if (!a.accumulate && !zeros_first) zeros();
 }
 
 // Joins a run that crosses windows, at the window where it begins: that
 // window's slot 2w + 1, then slot 2w of each window the run reaches.
-template <typename G, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) join_kernel(const EmbedGradArgs a, const GradPlan p) {
+template <typename O, bool VEC, int G>
+__global__ void __launch_bounds__(kRowThreads) join_kernel(const EmbedGradArgs a, const GradPlan p,
+                                                           uint32_t windows) {
+  using Gr = Groups<G>;
   pdl_wait_then_release();
-  const size_t slabs = (a.dim + kSlab - 1) / kSlab;
-  const size_t w = blockIdx.x / slabs;
-  const size_t col = blockIdx.x % slabs * kSlab + threadIdx.x * 8;
-  if (col >= a.dim) return;
-  const uint32_t* keys = p.keys[p.passes & 1];
-  const size_t next = (w + 1) * p.window;  // < tokens: one block less than windows
+  const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
+  const size_t j = (size_t)blockIdx.x * Gr::kCount + threadIdx.x / G;
+  const uint32_t w = (uint32_t)(j / slabs);
+  if (w + 1 >= windows) return;  // whole warps
+  const size_t col = j % slabs * Gr::kColumns + (threadIdx.x % G) * 8;
+  const uint32_t* keys = sorted_keys(p);
+  const uint32_t next = (w + 1) * p.window;  // < tokens
   const uint32_t key = keys[next];
   if (key >= a.vocab || keys[next - 1] != key) return;  // no run crosses here
-  if (keys[w * p.window] == key && w > 0 && keys[w * p.window - 1] == key) return;  // begun earlier
+  if (w > 0 && keys[w * p.window] == key && keys[w * p.window - 1] == key) return;  // begun earlier
+  const int lane = threadIdx.x & 31;
+  const bool live = col < a.dim;
   const size_t ld = (a.dim + 7) / 8 * 8;
-  float s[8];
-  load8(p.part + (2 * w + 1) * ld + col, s);
-  for (size_t at = next; at < a.tokens && keys[at] == key; at += p.window) {
-    float v[8];
-    load8(p.part + 2 * (at / p.window) * ld + col, v);
+  O* out = static_cast<O*>(a.dtable) + (size_t)key * a.dim;
+  float s[8], old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live) load8(p.part + (2 * (size_t)w + 1) * ld + col, s);
+  if (live && a.accumulate) load_row8<VEC>(out, col, a.dim, old);
+  for (uint32_t v0 = w + 1; v0 < windows; v0 += 32) {
+    const uint32_t at = v0 + lane;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, at < windows && keys[at * p.window] == key));
+    if (live) {
+      for (int i = 0; i < n; i += 8) {
+        float v[8][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] += v[e];
+        for (int u = 0; u < 8; ++u)
+          if (i + u < n) load8(p.part + 2 * (size_t)(v0 + i + u) * ld + col, v[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (i + u < n) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+          }
+      }
+    }
+    if (n < 32) break;
   }
-  G* out = static_cast<G*>(a.dtable) + (size_t)key * a.dim;
-  float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (a.accumulate) load_row8<VEC>(out, col, a.dim, old);
+  if (!live) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = old[e] + s[e] * a.scale;
   store_row8<VEC>(out, col, a.dim, s);
@@ -352,29 +446,36 @@ GradPlan grad_plan(void* ws, size_t tokens, size_t vocab, size_t dim, size_t* by
   return p;
 }
 
-template <typename T, typename G, bool VEC>
-cudaError_t sums_of(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t stream,
+template <typename T, typename O, bool VEC, int G>
+cudaError_t sums_by(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t stream,
                     uint64_t* launches) {
-  const size_t slabs = (a.dim + kSlab - 1) / kSlab;
-  const size_t most = (a.tokens + (a.accumulate ? 0 : a.vocab)) * slabs;
+  using Gr = Groups<G>;
+  const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
+  const size_t most = (a.tokens + (a.accumulate ? 0 : (a.vocab + 7) / 8)) * slabs;
+  const size_t blocks = (most + Gr::kCount - 1) / Gr::kCount;
   const size_t fill = (size_t)sm_count() * 8;
-  cudaError_t e = launch_kernel(sum_kernel<T, G, VEC>, dim3((unsigned)std::min(most, fill)),
+  cudaError_t e = launch_kernel(sum_kernel<T, O, VEC, G>, dim3((unsigned)std::min(blocks, fill)),
                                 dim3(kRowThreads), 0, stream, a, p);
   if (e != cudaSuccess) return e;
   ++*launches;
   const size_t windows = (a.tokens + p.window - 1) / p.window;
   if (windows < 2) return cudaSuccess;
-  e = launch_kernel(join_kernel<G, VEC>, dim3((unsigned)((windows - 1) * slabs)),
-                    dim3(kRowThreads), 0, stream, a, p);
+  e = launch_kernel(join_kernel<O, VEC, G>,
+                    dim3((unsigned)(((windows - 1) * slabs + Gr::kCount - 1) / Gr::kCount)),
+                    dim3(kRowThreads), 0, stream, a, p, (uint32_t)windows);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
 
-template <typename T, typename G>
+// A warp to a row up to 512 columns (in slabs of 256), else a whole block
+template <typename T, typename O>
 cudaError_t sums_of(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t stream,
                     uint64_t* launches) {
-  return a.vec ? sums_of<T, G, true>(a, p, stream, launches)
-               : sums_of<T, G, false>(a, p, stream, launches);
+  if (a.dim <= 512)
+    return a.vec ? sums_by<T, O, true, 32>(a, p, stream, launches)
+                 : sums_by<T, O, false, 32>(a, p, stream, launches);
+  return a.vec ? sums_by<T, O, true, kRowThreads>(a, p, stream, launches)
+               : sums_by<T, O, false, kRowThreads>(a, p, stream, launches);
 }
 
 }  // namespace

@@ -206,6 +206,7 @@ struct GemmArgs {
   size_t ld_c, split_stride;  // elements
   int c_type;
   int add;               // C += instead of C =
+  int wide;              // C is on a 32-byte boundary
 };
 
 // Shared-memory descriptor of a tile in rows of 128 bytes, swizzled by 128.
@@ -339,7 +340,14 @@ __device__ __forceinline__ void epilogue_out(const GemmArgs& g, const float (&v)
     if (c >= left) break;
     float o[8];
     if (g.add) {
-      load8(out + c, o);
+      if constexpr (sizeof(T) == 2) {
+        load8(out + c, o);
+      } else {  // 16-byte accesses: the caller's buffer may be on any such boundary
+        const float4 a = reinterpret_cast<const float4*>(out + c)[0];
+        const float4 b = reinterpret_cast<const float4*>(out + c)[1];
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = 0.f;
@@ -349,7 +357,14 @@ __device__ __forceinline__ void epilogue_out(const GemmArgs& g, const float (&v)
       o[e] += v[c + e];
       if (failed) o[e] = __uint_as_float(0x7FC00000u);
     }
-    store8(out + c, o);
+    if constexpr (sizeof(T) == 2) {
+      store8(out + c, o);
+    } else if (g.wide) {
+      store8(out + c, o);
+    } else {
+      reinterpret_cast<float4*>(out + c)[0] = make_float4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<float4*>(out + c)[1] = make_float4(o[4], o[5], o[6], o[7]);
+    }
   }
 }
 
@@ -566,7 +581,7 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts)
 // out = the sum of the slices, eight elements a thread
 template <typename T>
 __global__ void __launch_bounds__(256)
-    join_slices_kernel(const float* part, int slices, size_t n, T* out) {
+    join_slices_kernel(const float* part, int slices, size_t n, T* out, bool wide) {
   pdl_wait_then_release();
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (i >= n) return;
@@ -578,7 +593,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] += v[e];
   }
-  store8(out + i, s);
+  if (wide || sizeof(T) == 2) {
+    store8(out + i, s);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) from_f32(s[e], out[i + e]);
+  }
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -753,6 +773,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.ld_c = a.dim;
       g.split_stride = a.tokens * a.dim;
       g.add = i > 0;
+      g.wide = (reinterpret_cast<uintptr_t>(g.c) & 31u) == 0;
       for (int k = 0; k < p.parts; ++k)
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBM)) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBK)) return cudaErrorInvalidValue;
@@ -770,6 +791,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.c_type = a.grad_type;
       g.ld_c = a.dim;
       g.add = a.accumulate;
+      g.wide = (reinterpret_cast<uintptr_t>(g.c) & 31u) == 0;
       for (int k = 0; k < p.parts; ++k)
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBK)) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, kBK)) return cudaErrorInvalidValue;
@@ -787,9 +809,11 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
     const dim3 grid((unsigned)ceil_div(n, 256 * 8));
     e = a.grad_type == RCC_F32
             ? launch_kernel(join_slices_kernel<float>, grid, dim3(256), 0, stream,
-                            (const float*)slices, p.splits, n, static_cast<float*>(a.dx))
+                            (const float*)slices, p.splits, n, static_cast<float*>(a.dx),
+                            (reinterpret_cast<uintptr_t>(a.dx) & 31u) == 0)
             : launch_kernel(join_slices_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
-                            (const float*)slices, p.splits, n, static_cast<__nv_bfloat16*>(a.dx));
+                            (const float*)slices, p.splits, n, static_cast<__nv_bfloat16*>(a.dx),
+                            true);
     if (e != cudaSuccess) return e;
     ++*launches;
   }

@@ -44,12 +44,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Eight consecutive elements.  The vector forms want a 16-byte boundary.
+// Eight consecutive elements on a boundary of eight: one access, so that the
+// threads of a warp fill whole 32-byte sectors (two 16-byte accesses would
+// leave every sector half written, twice).
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0];
-  const float4 b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(p) : "memory");
 }
 __device__ __forceinline__ void widen2(uint32_t w, float& lo, float& hi) {
   lo = __uint_as_float(w << 16);
@@ -63,8 +65,9 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   widen2(a.w, v[6], v[7]);
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -87,14 +90,6 @@ __device__ __forceinline__ void store_upto8(T* p, size_t left, const float (&v)[
   for (int e = 0; e < 8; ++e)
     if (e < left) from_f32(v[e], p[e]);
 }
-// The same as four pairs
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float2 (&v)[4]) {
-  float f[8];
-  load8(p, f);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
-}
 template <bool VEC, typename T>
 __device__ __forceinline__ void load_row8(const T* row, size_t col, size_t dim, float (&v)[8]) {
   if constexpr (VEC) {
@@ -110,24 +105,6 @@ __device__ __forceinline__ void store_row8(T* row, size_t col, size_t dim, const
   } else {
     store_upto8(row + col, dim - col, v);
   }
-}
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_row8(const T* row, size_t col, size_t dim, float2 (&v)[4]) {
-  float f[8];
-  load_row8<VEC>(row, col, dim, f);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_row8(T* row, size_t col, size_t dim, const float2 (&v)[4]) {
-  float f[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = v[e].x;
-    f[2 * e + 1] = v[e].y;
-  }
-  store_row8<VEC>(row, col, dim, f);
 }
 
 // A token id or label; one outside [0, vocab) comes back as -1 (padding).

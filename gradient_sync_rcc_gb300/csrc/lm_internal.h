@@ -22,7 +22,7 @@ struct EmbedArgs {
   size_t ld_table;  // elements between rows of the table
   size_t tokens, vocab, dim;
   int table_type, out_type, ids64;
-  bool vec;  // rows of 8-element vectors, every one on a 16-byte boundary
+  bool vec;  // rows of whole 8-element vectors, each on a boundary of its size
   float scale;
 };
 cudaError_t launch_embedding_forward(const EmbedArgs& a, cudaStream_t stream);

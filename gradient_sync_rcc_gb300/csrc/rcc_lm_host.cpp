@@ -28,9 +28,9 @@ size_t extent(size_t rows, size_t ld, size_t dim, size_t size) {
   return rows ? ((rows - 1) * ld + dim) * size : 0;
 }
 
-// Rows of 8-element vectors on 16-byte boundaries
-bool vectors(const void* p, size_t ld, size_t dim, size_t size) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && dim % 8 == 0 && (ld * size) % 16 == 0;
+// Rows of whole vectors of eight elements, each on a boundary of `align` bytes
+bool vectors(const void* p, size_t ld, size_t dim, size_t size, size_t align) {
+  return reinterpret_cast<uintptr_t>(p) % align == 0 && dim % 8 == 0 && (ld * size) % align == 0;
 }
 
 struct Buffer {
@@ -156,7 +156,7 @@ rcc_status rcc_embedding_forward(const void* table, rcc_dtype table_type, size_t
   a.table_type = table_type;
   a.out_type = out_type;
   a.ids64 = index == RCC_I64;
-  a.vec = vectors(table, ld_table, dim, ts) && vectors(out, dim, dim, os);
+  a.vec = vectors(table, ld_table, dim, ts, 8 * ts) && vectors(out, dim, dim, os, 8 * os);
   a.scale = scale;
   return done(launch_embedding_forward(a, reinterpret_cast<cudaStream_t>(stream)),
               "rcc_embedding_forward", 1);
@@ -207,7 +207,7 @@ rcc_status rcc_embedding_backward(const void* dout, rcc_dtype dout_type, size_t 
   a.dout_type = dout_type;
   a.dtable_type = dtable_type;
   a.ids64 = index == RCC_I64;
-  a.vec = vectors(dout, ld_dout, dim, ds) && vectors(dtable, dim, dim, gs);
+  a.vec = vectors(dout, ld_dout, dim, ds, 8 * ds) && vectors(dtable, dim, dim, gs, 8 * gs);
   a.accumulate = accumulate != 0;
   a.scale = scale;
   uint64_t launches = 0;
@@ -248,7 +248,7 @@ rcc_status rcc_rmsnorm_forward(const void* x, rcc_dtype type, size_t ld_x, const
   a.tokens = tokens;
   a.dim = dim;
   a.type = type;
-  a.vec = vectors(x, ld_x, dim, s) && vectors(y, dim, dim, s) && aligned16(weight);
+  a.vec = vectors(x, ld_x, dim, s, 16) && vectors(y, dim, dim, s, 16) && aligned16(weight);
   a.eps = eps;
   return done(launch_rmsnorm_forward(a, reinterpret_cast<cudaStream_t>(stream)),
               "rcc_rmsnorm_forward", 1);
@@ -304,7 +304,7 @@ rcc_status rcc_rmsnorm_backward(const void* dy, rcc_dtype type, size_t ld_dy, co
   a.tokens = tokens;
   a.dim = dim;
   a.type = type;
-  a.vec = vectors(dy, ld_dy, dim, s) && vectors(dx, dim, dim, s) && aligned16(weight);
+  a.vec = vectors(dy, ld_dy, dim, s, 16) && vectors(dx, dim, dim, s, 16) && aligned16(weight);
   a.accumulate = accumulate != 0;
   a.eps = eps;
   uint64_t launches = 0;
