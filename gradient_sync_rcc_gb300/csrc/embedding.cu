@@ -32,8 +32,9 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
   pdl_wait_then_release();
   const size_t slabs = (a.dim + kSlab - 1) / kSlab;
   const size_t t0 = blockIdx.x / slabs * kTokensPerBlock;
-  const size_t col = blockIdx.x % slabs * kSlab + threadIdx.x * 8;
-  if (col >= a.dim) return;
+  const size_t base = blockIdx.x % slabs * kSlab;
+  const int t = threadIdx.x;
+  if (!slab_live<VEC, kRowThreads>(base, t, a.dim)) return;
   int64_t id[kTokensPerBlock];
 #pragma unroll
   for (int i = 0; i < kTokensPerBlock; ++i)
@@ -42,7 +43,8 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
 #pragma unroll
   for (int i = 0; i < kTokensPerBlock; ++i) {
     if (id[i] >= 0) {
-      load_row8<VEC>(static_cast<const T*>(a.table) + (size_t)id[i] * a.ld_table, col, a.dim, v[i]);
+      load_slab<VEC, kRowThreads>(static_cast<const T*>(a.table) + (size_t)id[i] * a.ld_table, base,
+                                  t, a.dim, v[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] *= a.scale;
     }
-    store_row8<VEC>(static_cast<O*>(a.out) + (t0 + i) * a.dim, col, a.dim, v[i]);
+    store_slab<VEC, kRowThreads>(static_cast<O*>(a.out) + (t0 + i) * a.dim, base, t, a.dim, v[i]);
   }
 }
 
@@ -76,6 +78,7 @@ cudaError_t embed_of(const EmbedArgs& a, cudaStream_t stream) {
 constexpr int kSortBlocks = 8;       // one cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kHold = 4;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr size_t kSortShared = (size_t)(kSortWarps * kDigits + 2 * kDigits) * sizeof(uint32_t);
@@ -85,7 +88,7 @@ constexpr size_t kSortShared = (size_t)(kSortWarps * kDigits + 2 * kDigits) * si
 struct GradPlan {
   uint32_t* keys[2];      // [tokens] each: the list before and after a digit
   uint32_t* order[2];     // [tokens] each: token of each place of the list
-  uint32_t* starts;       // [tokens]: first places of the items, in no order
+  uint2* items;           // [tokens]: (first place, key) of the items, in no order
   uint32_t* count;        // [1]: how many items there are
   uint32_t* present;      // [ceil(vocab/32)]: one bit for each row with a token
   float* part;            // [2 windows][dim]: sums of runs that cross windows
@@ -145,15 +148,30 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t* mine = counts + warp * kDigits;
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
-    for (uint32_t i = lo + lane; i < hi; i += 32) {
-      uint32_t key;
-      if (pass == 0) {
-        const int64_t id = load_id(ids, ids64, i, vocab);
-        key = id < 0 ? vocab : (uint32_t)id;
-      } else {
-        key = kin[i];
+    // kHold groups of 32 places are read at once
+    uint32_t key[kHold], tok[kHold];
+    auto read = [&](uint32_t i0) {
+#pragma unroll
+      for (int h = 0; h < kHold; ++h) {
+        const uint32_t i = i0 + h * 32 + lane;
+        key[h] = vocab;
+        tok[h] = i;
+        if (i < hi) {
+          if (pass == 0) {
+            const int64_t id = load_id(ids, ids64, i, vocab);
+            key[h] = id < 0 ? vocab : (uint32_t)id;
+          } else {
+            key[h] = kin[i];
+            tok[h] = oin[i];
+          }
+        }
       }
-      atomicAdd(&mine[(key >> shift) & (digits - 1)], 1u);
+    };
+    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * kHold) {
+      read(i0);
+#pragma unroll
+      for (int h = 0; h < kHold; ++h)
+        if (i0 + h * 32 + lane < hi) atomicAdd(&mine[(key[h] >> shift) & (digits - 1)], 1u);
     }
     __syncthreads();
     // counts of the warps before this one, and the block's totals: two threads
@@ -209,30 +227,24 @@ __global__ void __launch_bounds__(kSortThreads)
       base[tid] = s;
     }
     __syncthreads();
-    for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const bool live = i < hi;
-      uint32_t key = 0, tok = i;
-      if (live) {
-        if (pass == 0) {
-          const int64_t id = load_id(ids, ids64, i, vocab);
-          key = id < 0 ? vocab : (uint32_t)id;
-        } else {
-          key = kin[i];
-          tok = oin[i];
+    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * kHold) {
+      if (piece > 32 * kHold) read(i0);  // a piece of up to kHold groups is still held
+#pragma unroll
+      for (int h = 0; h < kHold; ++h) {
+        if (i0 + h * 32 >= hi) break;
+        const bool live = i0 + h * 32 + lane < hi;
+        const uint32_t d = live ? (key[h] >> shift) & (digits - 1) : 0xFFFFFFFFu;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
+        const uint32_t ahead = __popc(same & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (live) at = base[d] + mine[d] + ahead;
+        __syncwarp();
+        if (live && ahead == 0) mine[d] += __popc(same);
+        __syncwarp();
+        if (live) {
+          kout[at] = key[h];
+          oout[at] = tok[h];
         }
-      }
-      const uint32_t d = live ? (key >> shift) & (digits - 1) : 0xFFFFFFFFu;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
-      const uint32_t ahead = __popc(same & ((1u << lane) - 1u));
-      uint32_t at = 0;
-      if (live) at = base[d] + mine[d] + ahead;
-      __syncwarp();
-      if (live && ahead == 0) mine[d] += __popc(same);
-      __syncwarp();
-      if (live) {
-        kout[at] = key;
-        oout[at] = tok;
       }
     }
     cluster_sync();  // the list is whole, and no block still reads `total`
@@ -243,8 +255,9 @@ __global__ void __launch_bounds__(kSortThreads)
   for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
     const uint32_t i = i0 + lane;
     bool starts = false;
+    uint32_t key = vocab;
     if (i < hi) {
-      const uint32_t key = keys[i];
+      key = keys[i];
       const bool first = i == 0 || keys[i - 1] != key;
       starts = key < vocab && (first || i % p.window == 0);
       if (key < vocab && first) atomicOr(&p.present[key / 32], 1u << (key % 32));
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t at = 0;
     if (lane == 0 && who) at = atomicAdd(p.count, (uint32_t)__popc(who));
     at = __shfl_sync(0xFFFFFFFFu, at, 0);
-    if (starts) p.starts[at + __popc(who & ((1u << lane) - 1u))] = i;
+    if (starts) p.items[at + __popc(who & ((1u << lane) - 1u))] = make_uint2(i, key);
   }
 }
 
@@ -267,50 +280,62 @@ struct Groups {
   static constexpr int kColumns = G * 8;
 };
 
+// s += U rows of dout, whose tokens lanes j to j + U - 1 hold.  All rows are
+// asked for before the first is used: a thread whose columns do not exist
+// reads the slab's first ones (t = 0) rather than waiting behind a branch.
+template <int U, typename T, bool VEC, int G>
+__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint32_t tok, int j, size_t base,
+                                         int t, float (&s)[8]) {
+  float v[U][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t of = __shfl_sync(0xFFFFFFFFu, tok, j + u);
+    load_slab<VEC, G>(static_cast<const T*>(a.dout) + (size_t)of * a.ld_dout, base, t, a.dim, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+}
+
 // The sum of an item's rows of dout, in the order of the list.  The places are
 // read 32 at a time, the rows four at a time.
-template <typename T, bool VEC>
+template <typename T, bool VEC, int G>
 __device__ __forceinline__ void sum_item(const EmbedGradArgs& a, const uint32_t* keys,
                                          const uint32_t* order, uint32_t key, uint32_t start,
-                                         uint32_t stop, size_t col, bool live, float (&s)[8],
-                                         uint32_t& end) {
+                                         uint32_t stop, size_t base, int t, float (&s)[8]) {
   const int lane = threadIdx.x & 31;
-  const T* dout = static_cast<const T*>(a.dout);
   for (uint32_t i0 = start; i0 < stop; i0 += 32) {
     const uint32_t i = i0 + lane;
-    const bool mine = i < stop && keys[i] == key;
-    const uint32_t tok = mine ? order[i] : 0;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine));  // a run: the first n lanes
-    for (int j = 0; j < n; j += 4) {
-      float v[4][8];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t t = __shfl_sync(0xFFFFFFFFu, tok, j + u);
-        if (live && j + u < n) {
-          load_row8<VEC>(dout + (size_t)t * a.ld_dout, col, a.dim, v[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j + u < n) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] += v[u][e];
-        }
+    uint32_t k = ~0u, tok = 0;
+    if (i < stop) {
+      k = keys[i];
+      tok = order[i];
     }
-    end = i0 + n;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, k == key));  // a run: the first n lanes
+    int j = 0;
+    for (; j + 4 <= n; j += 4) add_rows<4, T, VEC, G>(a, tok, j, base, t, s);
+    if (n - j >= 2) {
+      add_rows<2, T, VEC, G>(a, tok, j, base, t, s);
+      j += 2;
+    }
+    if (n - j >= 1) add_rows<1, T, VEC, G>(a, tok, j, base, t, s);
     if (n < 32) break;
   }
 }
+
+// Blocks of the sums for each SM, of which kSumResident are there at a time:
+// the more, the evener the load, as items differ in length.  32,768 tokens,
+// 131,072 x 4,096 in fp32 (8,191 tokens added to 50,021 x 2,048): 64 blocks 403
+// (43.7) us, 32 411 (43.4), 16 420 (44.0), 8 450 (46.8).
+constexpr int kSumBlocks = 64, kSumResident = 4;
 
 // Every row of dW without a token is set to zero (when not accumulating), and
 // every item is summed.  Work is dealt to the blocks in turn; which block
 // takes which changes no result.  Half of the blocks begin with the zeros, so
 // that writing and summing overlap.
 template <typename T, typename O, bool VEC, int G>
-__global__ void __launch_bounds__(kRowThreads) sum_kernel(const EmbedGradArgs a, const GradPlan p) {
+__global__ void __launch_bounds__(kRowThreads, kSumResident) sum_kernel(const EmbedGradArgs a, const GradPlan p) {
   using Gr = Groups<G>;
   pdl_wait_then_release();
   const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
@@ -319,50 +344,52 @@ __global__ void __launch_bounds__(kRowThreads) sum_kernel(const EmbedGradArgs a,
   const uint32_t tokens = (uint32_t)a.tokens;
   const size_t group = (size_t)blockIdx.x * Gr::kCount + threadIdx.x / G;
   const size_t all_groups = (size_t)gridDim.x * Gr::kCount;
-  const size_t lane_col = (threadIdx.x % G) * 8;
+  const int t = threadIdx.x % G;
 
   auto zeros = [&]() {
     // a byte of the bit map, eight rows, at a time
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const size_t units = (a.vocab + 7) / 8 * slabs;
     for (size_t j = group; j < units; j += all_groups) {
-      const size_t col = j % slabs * Gr::kColumns + lane_col, row0 = j / slabs * 8;
+      const size_t base = j % slabs * Gr::kColumns, row0 = j / slabs * 8;
       const uint32_t bits = reinterpret_cast<const uint8_t*>(p.present)[row0 / 8];
-      if (col >= a.dim) continue;
+      if (!slab_live<VEC, G>(base, t, a.dim)) continue;
       O* out = static_cast<O*>(a.dtable) + row0 * a.dim;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
         if (row0 + r < a.vocab && !(bits >> r & 1u))
-          store_row8<VEC>(out + r * a.dim, col, a.dim, zero);
+          store_slab<VEC, G>(out + r * a.dim, base, t, a.dim, zero);
     }
   };
   const bool zeros_first = blockIdx.x & 1;
   if (!a.accumulate && zeros_first) zeros();
 
   const size_t items = (size_t)*p.count * slabs;
+  uint2 next = make_uint2(0u, 0u);
+  if (group < items) next = p.items[group / slabs];
   for (size_t j = group; j < items; j += all_groups) {
-    const size_t col = j % slabs * Gr::kColumns + lane_col;
-    const bool live = col < a.dim;
-    const uint32_t start = p.starts[j / slabs];
-    const uint32_t key = keys[start];
+    const size_t base = j % slabs * Gr::kColumns;
+    const bool live = slab_live<VEC, G>(base, t, a.dim);
+    const uint32_t start = next.x, key = next.y;
+    if (j + all_groups < items) next = p.items[(j + all_groups) / slabs];
     const uint32_t stop = min(tokens, (start / p.window + 1) * p.window);
     const bool before = start > 0 && keys[start - 1] == key;
     const bool after = stop < tokens && keys[stop] == key && keys[stop - 1] == key;
     O* out = static_cast<O*>(a.dtable) + (size_t)key * a.dim;
     float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (a.accumulate && live && !before && !after) load_row8<VEC>(out, col, a.dim, old);
+    if (a.accumulate && live && !before && !after)
+      load_slab<VEC, G>(out, base, t, a.dim, old);
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint32_t end = start;
-    sum_item<T, VEC>(a, keys, order, key, start, stop, col, live, s, end);
+    sum_item<T, VEC, G>(a, keys, order, key, start, stop, base, live ? t : 0, s);
     if (!live) continue;
     if (before || after) {
       // a run that goes on: slot 2w when it comes from the window before, else 2w + 1
-      store8(p.part + (size_t)(2 * (start / p.window) + (before ? 0 : 1)) *
-                          ((a.dim + 7) / 8 * 8) + col, s);
+      store_slab<VEC, G>(p.part + (size_t)(2 * (start / p.window) + (before ? 0 : 1)) * a.dim, base,
+                         t, a.dim, s);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] = old[e] + s[e] * a.scale;
-      store_row8<VEC>(out, col, a.dim, s);
+      store_slab<VEC, G>(out, base, t, a.dim, s);
     }
   }
   if (!a.accumulate && !zeros_first) zeros();
@@ -379,19 +406,19 @@ __global__ void __launch_bounds__(kRowThreads) join_kernel(const EmbedGradArgs a
   const size_t j = (size_t)blockIdx.x * Gr::kCount + threadIdx.x / G;
   const uint32_t w = (uint32_t)(j / slabs);
   if (w + 1 >= windows) return;  // whole warps
-  const size_t col = j % slabs * Gr::kColumns + (threadIdx.x % G) * 8;
+  const size_t base = j % slabs * Gr::kColumns;
+  const int t = threadIdx.x % G;
   const uint32_t* keys = sorted_keys(p);
   const uint32_t next = (w + 1) * p.window;  // < tokens
   const uint32_t key = keys[next];
   if (key >= a.vocab || keys[next - 1] != key) return;  // no run crosses here
   if (w > 0 && keys[w * p.window] == key && keys[w * p.window - 1] == key) return;  // begun earlier
   const int lane = threadIdx.x & 31;
-  const bool live = col < a.dim;
-  const size_t ld = (a.dim + 7) / 8 * 8;
+  const bool live = slab_live<VEC, G>(base, t, a.dim);
   O* out = static_cast<O*>(a.dtable) + (size_t)key * a.dim;
   float s[8], old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) load8(p.part + (2 * (size_t)w + 1) * ld + col, s);
-  if (live && a.accumulate) load_row8<VEC>(out, col, a.dim, old);
+  if (live) load_slab<VEC, G>(p.part + (2 * (size_t)w + 1) * a.dim, base, t, a.dim, s);
+  if (live && a.accumulate) load_slab<VEC, G>(out, base, t, a.dim, old);
   for (uint32_t v0 = w + 1; v0 < windows; v0 += 32) {
     const uint32_t at = v0 + lane;
     const int n = __popc(__ballot_sync(0xFFFFFFFFu, at < windows && keys[at * p.window] == key));
@@ -400,7 +427,8 @@ __global__ void __launch_bounds__(kRowThreads) join_kernel(const EmbedGradArgs a
         float v[8][8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (i + u < n) load8(p.part + 2 * (size_t)(v0 + i + u) * ld + col, v[u]);
+          if (i + u < n)
+            load_slab<VEC, G>(p.part + 2 * (size_t)(v0 + i + u) * a.dim, base, t, a.dim, v[u]);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (i + u < n) {
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(kRowThreads) join_kernel(const EmbedGradArgs a
   if (!live) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = old[e] + s[e] * a.scale;
-  store_row8<VEC>(out, col, a.dim, s);
+  store_slab<VEC, G>(out, base, t, a.dim, s);
 }
 
 // A run of c tokens costs its window's length in one block, then c / window
@@ -434,10 +462,10 @@ GradPlan grad_plan(void* ws, size_t tokens, size_t vocab, size_t dim, size_t* by
   const size_t windows = (tokens + p.window - 1) / p.window;
   for (int k = 0; k < 2; ++k) p.keys[k] = static_cast<uint32_t*>(take(tokens * 4));
   for (int k = 0; k < 2; ++k) p.order[k] = static_cast<uint32_t*>(take(tokens * 4));
-  p.starts = static_cast<uint32_t*>(take(tokens * 4));
+  p.items = static_cast<uint2*>(take(tokens * sizeof(uint2)));
   p.count = static_cast<uint32_t*>(take(4));
   p.present = static_cast<uint32_t*>(take((vocab + 31) / 32 * 4));
-  p.part = static_cast<float*>(take(windows > 1 ? 2 * windows * ((dim + 7) / 8 * 8) * 4 : 0));
+  p.part = static_cast<float*>(take(windows > 1 ? 2 * windows * dim * 4 : 0));
   int need = 1;  // bits that hold ids and `vocab`, the padding's key
   while (need < 32 && (vocab >> need)) ++need;
   p.passes = (need + kDigitBits - 1) / kDigitBits;
@@ -453,7 +481,7 @@ cudaError_t sums_by(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t stre
   const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
   const size_t most = (a.tokens + (a.accumulate ? 0 : (a.vocab + 7) / 8)) * slabs;
   const size_t blocks = (most + Gr::kCount - 1) / Gr::kCount;
-  const size_t fill = (size_t)sm_count() * 8;
+  const size_t fill = (size_t)sm_count() * kSumBlocks;
   cudaError_t e = launch_kernel(sum_kernel<T, O, VEC, G>, dim3((unsigned)std::min(blocks, fill)),
                                 dim3(kRowThreads), 0, stream, a, p);
   if (e != cudaSuccess) return e;

@@ -77,33 +77,35 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
                                             pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
-// The same for any alignment and a row that ends inside the eight: `left`
-// elements are there, the others read as zero and are not written.
-template <typename T>
-__device__ __forceinline__ void load_upto8(const T* p, size_t left, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < left ? to_f32(p[e]) : 0.f;
+// Eight columns of a row of `dim`, for thread t of the G that share a slab of
+// 8 G columns beginning at `base`: eight neighbours (VEC: aligned rows of whole
+// vectors), or, for any alignment and length, every G-th column, so that a
+// warp's accesses stay side by side.  Columns past the row read as zero and are
+// not written.
+template <bool VEC, int G>
+__device__ __forceinline__ bool slab_live(size_t base, int t, size_t dim) {
+  return base + (VEC ? t * 8 : t) < dim;
 }
-template <typename T>
-__device__ __forceinline__ void store_upto8(T* p, size_t left, const float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) from_f32(v[e], p[e]);
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_row8(const T* row, size_t col, size_t dim, float (&v)[8]) {
+template <bool VEC, int G, typename T>
+__device__ __forceinline__ void load_slab(const T* row, size_t base, int t, size_t dim,
+                                          float (&v)[8]) {
   if constexpr (VEC) {
-    load8(row + col, v);
+    load8(row + base + t * 8, v);
   } else {
-    load_upto8(row + col, dim - col, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = base + e * G + t < dim ? to_f32(row[base + e * G + t]) : 0.f;
   }
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_row8(T* row, size_t col, size_t dim, const float (&v)[8]) {
+template <bool VEC, int G, typename T>
+__device__ __forceinline__ void store_slab(T* row, size_t base, int t, size_t dim,
+                                           const float (&v)[8]) {
   if constexpr (VEC) {
-    store8(row + col, v);
+    store8(row + base + t * 8, v);
   } else {
-    store_upto8(row + col, dim - col, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (base + e * G + t < dim) from_f32(v[e], row[base + e * G + t]);
   }
 }
 
