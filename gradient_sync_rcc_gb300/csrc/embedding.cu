@@ -526,8 +526,8 @@ cudaError_t launch_embedding_backward(const EmbedGradArgs& a, cudaStream_t strea
                                       uint64_t* launches) {
   size_t bytes = 0;
   const GradPlan p = grad_plan(a.workspace, a.tokens, a.vocab, a.dim, &bytes);
-  cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSortShared);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared(sort_kernel, (int)kSortShared, allowed);
   if (e != cudaSuccess) return e;
   e = launch_cluster(sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), kSortShared, kSortBlocks,
                      stream, a.ids, a.ids64, (uint32_t)a.tokens, (uint32_t)a.vocab, p);

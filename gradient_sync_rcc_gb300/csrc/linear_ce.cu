@@ -184,7 +184,9 @@ enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
 struct GemmArgs {
   CUtensorMap a[2], b;   // a[1]: the second bf16 number of A's values
   int m, n;              // of C
-  int m_tiles, n_tiles;  // of kBM * CG rows, of kBN columns
+  int m_tiles, n_tiles;  // of kBM * CG rows, of bn columns
+  int bn;                // columns of a tile, a multiple of 16 up to kBN
+  int a_rows;            // rows of A's box (not MN), a multiple of 8 up to kBM
   int k_blocks, splits;  // of kBK; pieces of the sum, each with a C of its own
   int chunk;             // k_blocks that one accumulator takes
   int group;             // tiles of rows that share a run over the columns
@@ -261,17 +263,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// 32 bytes on a boundary of 32
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Half a row of scores: (max, sum of exp) of the columns that exist.
 __device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHalf], int row,
-                                               int col0, bool failed) {
-  const int left = g.n - col0;
-  if (row >= g.m || left <= 0) {
-    if (row < g.m) g.part[(size_t)(col0 / kHalf) * g.m + row] = make_float2(-INFINITY, 0.f);
+                                               int col0, int left, int slot, bool failed) {
+  if (row >= g.m) return;
+  float2* part = g.part + (size_t)slot * g.m + row;
+  if (left <= 0) {
+    *part = make_float2(-INFINITY, 0.f);
     return;
   }
   const float nan = __uint_as_float(0x7FC00000u);
   const int64_t at = load_id(g.labels, g.labels64, row, g.vocab) - col0;
-  if (at >= 0 && at < kHalf) {
+  if (at >= 0 && at < left && at < kHalf) {
     float z = v[0];
 #pragma unroll
     for (int i = 1; i < kHalf; ++i) z = i == at ? v[i] : z;
@@ -290,14 +300,12 @@ __device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHa
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kHalf; ++i) sum[i & 3] += exp2_fast(fmaf(v[i], kLog2e, -ml));
-  g.part[(size_t)(col0 / kHalf) * g.m + row] =
-      failed ? make_float2(nan, nan) : make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+  *part = failed ? make_float2(nan, nan) : make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 // dz of half a row; columns past the piece are not written.
 __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf], int row,
-                                            int col0, bool failed) {
-  const int left = g.n - col0;
+                                            int col0, int left, bool failed) {
   if (row >= g.m || left <= 0) return;
   const int64_t label = load_id(g.labels, g.labels64, row, g.vocab);
   const int64_t at = label - (g.b_row0 + col0);
@@ -306,64 +314,78 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
   __nv_bfloat16* out = g.dz[0] + (size_t)row * g.ld_dz + col0;
   __nv_bfloat16* rest = g.dz[1] ? g.dz[1] + (size_t)row * g.ld_dz + col0 : nullptr;
 #pragma unroll
-  for (int c = 0; c < kHalf; c += 8) {
-    // ld_dz is a multiple of 256, so whole vectors stay inside the row
+  for (int c = 0; c < kHalf; c += 16) {
+    // ld_dz is a multiple of 256 and the piece begins on a boundary of 256, so
+    // whole 32-byte vectors stay inside the row
     if (c >= left) break;
-    uint32_t w[4], u[4];
+    uint32_t w[8], u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float p = exp2_fast(fmaf(v[c + i], kLog2e, -ll));
       float d = label < 0 ? 0.f : f * (c + i == at ? p - 1.f : p);
       if (failed) d = __uint_as_float(0x7FC00000u);
       v[c + i] = d;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
       float lo, hi;
       widen2(w[i], lo, hi);
       u[i] = pack2(v[c + 2 * i] - lo, v[c + 2 * i + 1] - hi);
     }
-    *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (rest) *reinterpret_cast<uint4*>(rest + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    store_words(out + c, w);
+    if (rest) store_words(rest + c, u);
   }
 }
 
+// Half a row of C.  Whole 32-byte sectors where C's rows allow it (wide).
 template <typename T>
-__device__ __forceinline__ void epilogue_out(const GemmArgs& g, const float (&v)[kHalf], int row,
-                                             int col0, int split, bool failed) {
-  const int left = g.n - col0;  // n is a multiple of 8
+__device__ __forceinline__ void epilogue_out(const GemmArgs& g, float (&v)[kHalf], int row,
+                                             int col0, int left, int split, bool failed) {
   if (row >= g.m) return;
+  constexpr int kE = 16 / (int)sizeof(T);  // elements of 16 bytes
   T* out = static_cast<T*>(g.c) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
 #pragma unroll
-  for (int c = 0; c < kHalf; c += 8) {
-    if (c >= left) break;
-    float o[8];
+  for (int c = 0; c < kHalf; c += 2 * kE) {
+    if (c >= left) break;  // left is a multiple of 8, and of 16 where wide
     if (g.add) {
-      if constexpr (sizeof(T) == 2) {
-        load8(out + c, o);
-      } else {  // 16-byte accesses: the caller's buffer may be on any such boundary
-        const float4 a = reinterpret_cast<const float4*>(out + c)[0];
-        const float4 b = reinterpret_cast<const float4*>(out + c)[1];
-        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+#pragma unroll
+      for (int h = 0; h < 2 * kE; h += kE) {
+        if (c + h >= left) break;
+        const uint4 o = *reinterpret_cast<const uint4*>(out + c + h);
+        if constexpr (kE == 4) {
+          v[c + h] += __uint_as_float(o.x);
+          v[c + h + 1] += __uint_as_float(o.y);
+          v[c + h + 2] += __uint_as_float(o.z);
+          v[c + h + 3] += __uint_as_float(o.w);
+        } else {
+          float f[8];
+          widen2(o.x, f[0], f[1]);
+          widen2(o.y, f[2], f[3]);
+          widen2(o.z, f[4], f[5]);
+          widen2(o.w, f[6], f[7]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[c + h + e] += f[e];
+        }
       }
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (kE == 4)
+        w[i] = __float_as_uint(v[c + i]);
+      else
+        w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
+      if (failed) w[i] = kE == 4 ? 0x7FC00000u : 0x7FC07FC0u;
+    }
+    if (g.wide) {
+      store_words(out + c, w);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      o[e] += v[c + e];
-      if (failed) o[e] = __uint_as_float(0x7FC00000u);
-    }
-    if constexpr (sizeof(T) == 2) {
-      store8(out + c, o);
-    } else if (g.wide) {
-      store8(out + c, o);
-    } else {
-      reinterpret_cast<float4*>(out + c)[0] = make_float4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<float4*>(out + c)[1] = make_float4(o[4], o[5], o[6], o[7]);
+      for (int h = 0; h < 2; ++h)
+        if (c + h * kE < left)
+          *reinterpret_cast<uint4*>(out + c + h * kE) =
+              make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
     }
   }
 }
@@ -410,18 +432,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     if (lane == 0) {
       // what earlier kernels wrote by ordinary stores, before copies by TMA
       asm volatile("fence.proxy.async;" ::: "memory");
+      // B's box has g.bn / CG rows.  A's may have less than kBM: the rows of
+      // shared memory past it hold anything, and their sums are not used.
+      const uint32_t stage_bytes = (PARTS * (A_MN ? kBM : g.a_rows) +
+                                    (B_MN ? S::kBRows : g.bn / CG)) * kRowBytes;
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
         const Tile tile = tile_of(g, t);
         const int m0 = (tile.m * CG + (int)rank) * kBM;
-        const int n0 = tile.n * kBN + (int)rank * S::kBRows;
+        const int n0 = tile.n * g.bn + (int)rank * S::kBRows;
         for (int k = tile.k0; k < tile.k1; ++k) {
           if (!(ok = bar_wait(empty + 8 * s, phase ^ 1))) break;
           const uint32_t at = base + s * S::kBytes;
           const uint32_t bar = CG == 2 ? peer_addr(full + 8 * s, 0) : full + 8 * s;
-          bar_expect(bar, S::kBytes);
+          bar_expect(bar, stage_bytes);
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
             const uint32_t to = at + p * S::kABytes;
@@ -460,7 +486,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
-                             ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(kBN / 8) << 17) |
+                             ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(g.bn / 8) << 17) |
                              ((uint32_t)(kBM * CG / 16) << 24);
       int s = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
@@ -525,16 +551,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         if ((buf ^= 1) == 0) acc_phase ^= 1;
       }
       const int row = (tile.m * CG + (int)rank) * kBM + quarter * 32 + lane;
-      const int col0 = tile.n * kBN + half * kHalf;
+      const int col0 = tile.n * g.bn + half * kHalf;
+      // columns of this half that are the tile's and exist
+      const int left = min(g.n - tile.n * g.bn, g.bn) - half * kHalf;
       if constexpr (EPI == kEpiStats) {
-        epilogue_stats(g, v, row, col0, !ok);
+        epilogue_stats(g, v, row, col0, left, 2 * tile.n + half, !ok);
       } else if constexpr (EPI == kEpiDz) {
-        epilogue_dz(g, v, row, col0, !ok);
+        epilogue_dz(g, v, row, col0, left, !ok);
       } else {
         if (g.c_type == RCC_F32)
-          epilogue_out<float>(g, v, row, col0, tile.split, !ok);
+          epilogue_out<float>(g, v, row, col0, left, tile.split, !ok);
         else
-          epilogue_out<__nv_bfloat16>(g, v, row, col0, tile.split, !ok);
+          epilogue_out<__nv_bfloat16>(g, v, row, col0, left, tile.split, !ok);
       }
       __syncwarp();
     }
@@ -551,7 +579,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 
 constexpr int kJoinRows = 32, kJoinParts = 32;
 
-// lse and loss of a row from its (max, sum) pairs.
+// (max, sum of exp) of two sets of scores; -inf: an empty set
+__device__ __forceinline__ float2 join_pair(float2 a, float2 b) {
+  if (b.x == -INFINITY) return a;
+  if (a.x == -INFINITY) return b;
+  const float m = fmaxf(a.x, b.x);
+  return make_float2(m, a.y * exp2_fast((a.x - m) * kLog2e) + b.y * exp2_fast((b.x - m) * kLog2e));
+}
+
+// lse and loss of a row from its (max, sum) pairs: a thread takes every 32nd
+// pair of its row, eight loads under way; then a warp joins a row's 32 threads.
 __global__ void __launch_bounds__(kJoinRows* kJoinParts)
     join_stats_kernel(const float2* part, int parts, const float* zlab, const void* labels,
                       int labels64, size_t tokens, size_t vocab, float* loss, float* lse) {
@@ -559,40 +596,69 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts)
   pdl_wait_then_release();
   const int x = threadIdx.x % kJoinRows, y = threadIdx.x / kJoinRows;
   const size_t row = (size_t)blockIdx.x * kJoinRows + x;
-  float top = -INFINITY, sum = 0.f;
-  auto add = [&](float2 p) {
-    if (p.x == -INFINITY) return;  // nothing in it
-    const float m = fmaxf(top, p.x);
-    sum = sum * exp2f((top - m) * kLog2e) + p.y * exp2f((p.x - m) * kLog2e);
-    top = m;
-  };
-  if (row < tokens)
-    for (int j = y; j < parts; j += kJoinParts) add(part[(size_t)j * tokens + row]);
-  red[y][x] = make_float2(top, sum);
+  float2 all = make_float2(-INFINITY, 0.f);
+  if (row < tokens) {
+    for (int j = y; j < parts; j += 8 * kJoinParts) {
+      float2 p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        p[i] = j + i * kJoinParts < parts ? part[(size_t)(j + i * kJoinParts) * tokens + row]
+                                          : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2 * o) p[i] = join_pair(p[i], p[i + o]);
+      all = join_pair(all, p[0]);
+    }
+  }
+  red[y][x] = all;
   __syncthreads();
-  if (y == 0 && row < tokens) {
-    for (int j = 1; j < kJoinParts; ++j) add(red[j][x]);
-    const float l = top + logf(sum);
-    lse[row] = l;
-    loss[row] = load_id(labels, labels64, row, vocab) >= 0 ? l - zlab[row] : 0.f;
+  all = red[x][y];  // lane x: thread x of row y
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float2 b = make_float2(__shfl_xor_sync(0xFFFFFFFFu, all.x, o),
+                                 __shfl_xor_sync(0xFFFFFFFFu, all.y, o));
+    all = x & o ? join_pair(b, all) : join_pair(all, b);  // the same order in both lanes
+  }
+  const size_t t = (size_t)blockIdx.x * kJoinRows + y;
+  if (x == 0 && t < tokens) {
+    const float l = all.x + logf(all.y);
+    lse[t] = l;
+    loss[t] = load_id(labels, labels64, t, vocab) >= 0 ? l - zlab[t] : 0.f;
   }
 }
 
-// out = the sum of the slices, eight elements a thread
+constexpr int kSliceParts = 8;
+
+// out = the sum of the slices: 32 threads of eight elements, eight sums each
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kSliceParts)
     join_slices_kernel(const float* part, int slices, size_t n, T* out, bool wide) {
+  __shared__ float red[kSliceParts][8][33];
   pdl_wait_then_release();
-  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  float s[8];
-  load8(part + i, s);
-  for (int k = 1; k < slices; ++k) {
-    float v[8];
-    load8(part + (size_t)k * n + i, v);
+  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+  const size_t i = ((size_t)blockIdx.x * 32 + x) * 8;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (i < n) {
+    for (int k = y; k < slices; k += 4 * kSliceParts) {
+      float v[4][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] += v[e];
+      for (int u = 0; u < 4; ++u)  // past the last slice: it again, not added
+        load8(part + (size_t)min(k + u * kSliceParts, slices - 1) * n + i, v[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += k + u * kSliceParts < slices ? v[u][e] : 0.f;
+    }
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[y][e][x] = s[e];
+  __syncthreads();
+  if (y != 0 || i >= n) return;
+#pragma unroll
+  for (int k = 1; k < kSliceParts; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += red[k][e][x];
   if (wide || sizeof(T) == 2) {
     store8(out + i, s);
   } else {
@@ -643,22 +709,29 @@ template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_gemm_of(GemmArgs& g, cudaStream_t stream) {
   using S = Stage<CG, PARTS>;
   auto kernel = gemm_kernel<CG, PARTS, A_MN, B_MN, EPI>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       S::kShared);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared(kernel, S::kShared, allowed);
   if (e != cudaSuccess) return e;
   const int tiles = g.m_tiles * g.n_tiles * g.splits;
   const int units = std::min(tiles, sm_count() / CG);
   return launch_cluster(kernel, dim3(units * CG), dim3(kGemmThreads), S::kShared, CG, stream, g);
 }
 
+// Rows of A's box: those that exist, in whole swizzle atoms.  A box that is
+// mostly filled with zeros is slow: one token against 131,072 x 4,096 took
+// 254 us with 128 rows, 64 tokens 169.
+int box_rows(size_t rows) { return (int)std::min<size_t>(kBM, (rows + 7) / 8 * 8); }
+
 // Rows of C, columns, and the extent of the sum; the maps are the caller's.
 template <int PARTS, bool A_MN, bool B_MN, int EPI>
-cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, int splits,
+cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, int bn, int splits,
                         int group, cudaStream_t stream) {
   g.m = (int)m;
   g.n = (int)n;
   g.m_tiles = (int)ceil_div(m, kBM * (pair ? 2 : 1));
-  g.n_tiles = (int)ceil_div(n, kBN);
+  g.bn = bn;
+  g.a_rows = box_rows(m);
+  g.n_tiles = (int)ceil_div(n, bn);
   g.k_blocks = (int)ceil_div(k, kBK);
   g.splits = splits;
   g.group = group;
@@ -672,7 +745,20 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // Two SMs share a tile of 256 rows unless 128 rows are all there are.
 bool paired(size_t rows) { return rows > (size_t)kBM; }
 
+// Columns of a tile of scores.  With few tokens a pass is bound by reading W,
+// so its rows are shared out evenly: the same number of tiles for every SM.
+int score_width(size_t tokens, size_t vocab) {
+  if (paired(tokens)) return kBN;
+  const size_t sms = sm_count(), turns = ceil_div(vocab, sms * kBN);
+  return (int)(ceil_div(ceil_div(vocab, sms * turns), 16) * 16);
+}
+
 constexpr int kScoreGroup = 32, kGradGroup = 8;
+
+// Rows of whole 32-byte sectors
+bool wide_rows(const void* c, size_t dim, size_t size) {
+  return (reinterpret_cast<uintptr_t>(c) & 31u) == 0 && dim * size % 32 == 0;
+}
 
 // The backward pass's pieces of the vocabulary and what it keeps of each.
 struct Pieces {
@@ -683,7 +769,10 @@ struct Pieces {
   size_t dz_bytes;   // of one part
   size_t dx_bytes;   // of the fp32 slices of dx, 0: summed in dx itself
 };
-constexpr size_t kDzBytes = (size_t)512 << 20;
+#ifndef CE_DZ
+#define CE_DZ 512
+#endif
+constexpr size_t kDzBytes = (size_t)CE_DZ << 20;
 
 Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
   Pieces p;
@@ -706,14 +795,17 @@ Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
 }  // namespace
 
 size_t linear_ce_workspace(size_t tokens, size_t vocab, size_t dim, bool backward, int grad_type) {
-  if (!backward) return up256(2 * ceil_div(vocab, kBN) * tokens * sizeof(float2)) + up256(tokens * 4);
+  if (!backward)
+    return up256(2 * ceil_div(vocab, score_width(tokens, vocab)) * tokens * sizeof(float2)) +
+           up256(tokens * 4);
   const Pieces p = pieces_of(tokens, vocab, dim, grad_type);
   return p.parts * p.dz_bytes + p.dx_bytes;
 }
 
 cudaError_t launch_linear_ce_forward(const CeArgs& a, cudaStream_t stream, uint64_t* launches) {
   const bool pair = paired(a.tokens);
-  const int parts = 2 * (int)ceil_div(a.vocab, kBN);  // one for each half of a tile's columns
+  const int bn = score_width(a.tokens, a.vocab);
+  const int parts = 2 * (int)ceil_div(a.vocab, bn);  // one for each half of a tile's columns
   GemmArgs g = {};
   g.part = static_cast<float2*>(a.workspace);
   g.zlab = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
@@ -721,10 +813,10 @@ cudaError_t launch_linear_ce_forward(const CeArgs& a, cudaStream_t stream, uint6
   g.labels = a.labels;
   g.labels64 = a.labels64;
   g.vocab = (int)a.vocab;
-  if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, kBM) ||
-      !make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBN / (pair ? 2 : 1)))
+  if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, box_rows(a.tokens)) ||
+      !make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, bn / (pair ? 2 : 1)))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_gemm<1, false, false, kEpiStats>(g, pair, a.tokens, a.vocab, a.dim, 1,
+  cudaError_t e = launch_gemm<1, false, false, kEpiStats>(g, pair, a.tokens, a.vocab, a.dim, bn, 1,
                                                           kScoreGroup, stream);
   if (e != cudaSuccess) return e;
   e = launch_kernel(join_stats_kernel, dim3((unsigned)ceil_div(a.tokens, kJoinRows)),
@@ -757,10 +849,11 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.dz[0] = dz[0];
       g.dz[1] = dz[1];
       g.ld_dz = p.width;
-      if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, kBM) ||
-          !make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBN / (pair ? 2 : 1)))
+      const int bn = score_width(a.tokens, width);
+      if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, box_rows(a.tokens)) ||
+          !make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, bn / (pair ? 2 : 1)))
         return cudaErrorInvalidValue;
-      e = launch_gemm<1, false, false, kEpiDz>(g, pair, a.tokens, width, a.dim, 1, kScoreGroup,
+      e = launch_gemm<1, false, false, kEpiDz>(g, pair, a.tokens, width, a.dim, bn, 1, kScoreGroup,
                                                stream);
       if (e != cudaSuccess) return e;
       ++*launches;
@@ -773,15 +866,15 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.ld_c = a.dim;
       g.split_stride = a.tokens * a.dim;
       g.add = i > 0;
-      g.wide = (reinterpret_cast<uintptr_t>(g.c) & 31u) == 0;
+      g.wide = wide_rows(g.c, a.dim, slices ? 4 : grad_size);
       for (int k = 0; k < p.parts; ++k)
-        if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBM)) return cudaErrorInvalidValue;
+        if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, box_rows(a.tokens))) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBK)) return cudaErrorInvalidValue;
       const int splits = (int)std::min<size_t>(p.splits, ceil_div(width, kBK));
       e = p.parts == 2 ? launch_gemm<2, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
-                                                              splits, kGradGroup, stream)
+                                                              kBN, splits, kGradGroup, stream)
                        : launch_gemm<1, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
-                                                              splits, kGradGroup, stream);
+                                                              kBN, splits, kGradGroup, stream);
       if (e != cudaSuccess) return e;
       ++*launches;
     }
@@ -791,14 +884,14 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.c_type = a.grad_type;
       g.ld_c = a.dim;
       g.add = a.accumulate;
-      g.wide = (reinterpret_cast<uintptr_t>(g.c) & 31u) == 0;
+      g.wide = wide_rows(g.c, a.dim, grad_size);
       for (int k = 0; k < p.parts; ++k)
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBK)) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, kBK)) return cudaErrorInvalidValue;
       const bool wide = paired(width);
-      e = p.parts == 2 ? launch_gemm<2, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, 1,
+      e = p.parts == 2 ? launch_gemm<2, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, kBN, 1,
                                                              kGradGroup, stream)
-                       : launch_gemm<1, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, 1,
+                       : launch_gemm<1, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, kBN, 1,
                                                              kGradGroup, stream);
       if (e != cudaSuccess) return e;
       ++*launches;
@@ -806,12 +899,12 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
   }
   if (a.dx && slices) {
     const size_t n = a.tokens * a.dim;
-    const dim3 grid((unsigned)ceil_div(n, 256 * 8));
+    const dim3 grid((unsigned)ceil_div(n, 32 * 8)), block(32 * kSliceParts);
     e = a.grad_type == RCC_F32
-            ? launch_kernel(join_slices_kernel<float>, grid, dim3(256), 0, stream,
+            ? launch_kernel(join_slices_kernel<float>, grid, block, 0, stream,
                             (const float*)slices, p.splits, n, static_cast<float*>(a.dx),
                             (reinterpret_cast<uintptr_t>(a.dx) & 31u) == 0)
-            : launch_kernel(join_slices_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
+            : launch_kernel(join_slices_kernel<__nv_bfloat16>, grid, block, 0, stream,
                             (const float*)slices, p.splits, n, static_cast<__nv_bfloat16*>(a.dx),
                             true);
     if (e != cudaSuccess) return e;

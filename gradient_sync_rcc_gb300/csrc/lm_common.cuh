@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -137,15 +138,39 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// SMs of the current device (152 on GB300).
+constexpr int kMaxDevices = 64;  // whose properties are remembered
+
+inline int current_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+  return dev;
+}
+
+// SMs of the current device (152 on GB300), asked for once a device.
 inline int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+  static std::atomic<int> known[kMaxDevices];
+  const int dev = current_device();
+  int n = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
     cudaGetLastError();
     return 152;
   }
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
   return n;
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device;
+// `done`, one bit a device, says where that has been asked for already.
+template <typename K>
+inline cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  const int dev = current_device();
+  const uint64_t bit = dev < kMaxDevices ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace lm

@@ -582,9 +582,9 @@ cudaError_t forward_of(const NormArgs& a, cudaStream_t stream) {
   return with_shape(s, [&](auto g, auto nv) {
     using F = NormFore<T, decltype(g)::value, decltype(nv)::value, VEC>;
     auto kernel = norm_forward_kernel<T, decltype(g)::value, decltype(nv)::value, VEC>;
-    if (F::kShared > 40 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kShared);
+    if (F::kShared > 40 * 1024) {  // with what is static, more than every kernel may have
+      static std::atomic<uint64_t> allowed{0};
+      const cudaError_t e = allow_shared(kernel, F::kShared, allowed);
       if (e != cudaSuccess) return e;
     }
     return launch_kernel(kernel, dim3((unsigned)norm_blocks(a.tokens, s, F::kPerSm)),
@@ -600,9 +600,9 @@ cudaError_t backward_of(const NormGradArgs& a, cudaStream_t stream, size_t* bloc
     constexpr int G = decltype(g)::value;
     using B = NormBack<T, G, decltype(nv)::value, VEC>;
     auto kernel = norm_backward_kernel<T, G, decltype(nv)::value, VEC>;
-    if (B::kShared > 40 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, B::kShared);
+    if (B::kShared > 40 * 1024) {  // with what is static, more than every kernel may have
+      static std::atomic<uint64_t> allowed{0};
+      const cudaError_t e = allow_shared(kernel, B::kShared, allowed);
       if (e != cudaSuccess) return e;
     }
     *blocks = norm_blocks(a.tokens, s, B::kPerSm);

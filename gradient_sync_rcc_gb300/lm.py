@@ -14,6 +14,8 @@ import torch
 
 from gradient_sync_rcc_gb300.rcc import BF16, F32, I32, I64, OK, RccError, last_error, lib
 
+_lib = lib()
+
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -111,14 +113,14 @@ def embedding_forward(table, ids, scale=1.0, out=None, out_dtype=None, stream=No
         out = torch.empty((tokens, dim), dtype=out_dtype or table.dtype, device=table.device)
     else:
         _output(out, "out", table, (tokens, dim), out_dtype or out.dtype)
-    _check(lib().rcc_embedding_forward(
+    _check(_lib.rcc_embedding_forward(
         table.data_ptr(), kind, ld, ids.data_ptr(), index, tokens, vocab, dim, scale,
         out.data_ptr(), _type(out, "out"), _stream(stream, dev)))
     return out
 
 
 def embedding_backward_workspace(tokens, vocab, dim):
-    return lib().rcc_embedding_backward_workspace(tokens, vocab, dim)
+    return _lib.rcc_embedding_backward_workspace(tokens, vocab, dim)
 
 
 def embedding_backward(dout, ids, dtable, scale=1.0, accumulate=False, workspace=None,
@@ -134,7 +136,7 @@ def embedding_backward(dout, ids, dtable, scale=1.0, accumulate=False, workspace
     _output(dtable, "dtable", dout, (vocab, dim), dtable.dtype)
     kinds = _type(dout, "dout"), _type(dtable, "dtable")
     ws, at, have = _workspace(workspace, dout, embedding_backward_workspace(tokens, vocab, dim))
-    _check(lib().rcc_embedding_backward(
+    _check(_lib.rcc_embedding_backward(
         dout.data_ptr(), kinds[0], ld, ids.data_ptr(), index, tokens, vocab, dim, scale,
         dtable.data_ptr(), kinds[1], 1 if accumulate else 0, at, have, _stream(stream, dev)))
     return dtable
@@ -190,13 +192,13 @@ def rmsnorm_forward(x, weight, eps=1e-6, keep=False, out=None, stream=None):
     elif keep:
         kept = keep
         q, s = kept._checked(tokens, dim, x)
-    _check(lib().rcc_rmsnorm_forward(x.data_ptr(), kind, ld, w, eps, tokens, dim, y.data_ptr(),
+    _check(_lib.rcc_rmsnorm_forward(x.data_ptr(), kind, ld, w, eps, tokens, dim, y.data_ptr(),
                                      q, s, _stream(stream, dev)))
     return y if kept is None else (y, kept)
 
 
 def rmsnorm_backward_workspace(tokens, dim):
-    return lib().rcc_rmsnorm_backward_workspace(tokens, dim)
+    return _lib.rcc_rmsnorm_backward_workspace(tokens, dim)
 
 
 def rmsnorm_backward(dy, kept, weight, eps=1e-6, dx=None, dweight=None, accumulate=False,
@@ -213,7 +215,7 @@ def rmsnorm_backward(dy, kept, weight, eps=1e-6, dx=None, dweight=None, accumula
     dx = _output(dx, "dx", dy, (tokens, dim), dy.dtype)
     dweight = _output(dweight, "dweight", dy, (dim,), torch.float32)
     ws, at, have = _workspace(workspace, dy, rmsnorm_backward_workspace(tokens, dim))
-    _check(lib().rcc_rmsnorm_backward(
+    _check(_lib.rcc_rmsnorm_backward(
         dy.data_ptr(), kind, ld, q, s, w, eps, tokens, dim, dx.data_ptr(), dweight.data_ptr(),
         1 if accumulate else 0, at, have, _stream(stream, dev)))
     return dx, dweight
@@ -222,7 +224,7 @@ def rmsnorm_backward(dy, kept, weight, eps=1e-6, dx=None, dweight=None, accumula
 # ------------------------------------------------------------- output layer + cross entropy
 
 def linear_ce_workspace(tokens, vocab, dim, backward=False, grad_dtype=torch.bfloat16):
-    return lib().rcc_linear_ce_workspace(tokens, vocab, dim, 1 if backward else 0,
+    return _lib.rcc_linear_ce_workspace(tokens, vocab, dim, 1 if backward else 0,
                                          _TYPES[grad_dtype])
 
 
@@ -243,8 +245,8 @@ def linear_ce_forward(x, w, labels, loss=None, lse=None, workspace=None, stream=
     dev, tokens, vocab, dim, ld_x, ld_w, index = _ce_inputs(x, w, labels)
     loss = _output(loss, "loss", x, (tokens,), torch.float32)
     lse = _output(lse, "lse", x, (tokens,), torch.float32)
-    ws, at, have = _workspace(workspace, x, lib().rcc_linear_ce_workspace(tokens, vocab, dim, 0, F32))
-    _check(lib().rcc_linear_ce_forward(
+    ws, at, have = _workspace(workspace, x, _lib.rcc_linear_ce_workspace(tokens, vocab, dim, 0, F32))
+    _check(_lib.rcc_linear_ce_forward(
         x.data_ptr(), ld_x, w.data_ptr(), ld_w, labels.data_ptr(), index, tokens, vocab, dim,
         loss.data_ptr(), lse.data_ptr(), at, have, _stream(stream, dev)))
     return loss, lse
@@ -269,8 +271,8 @@ def linear_ce_backward(x, w, labels, lse, dloss, grad_dtype=None, dx=None, dw=No
     dx = _output(dx, "dx", x, (tokens, dim), grad_dtype) if need_dx else None
     dw = _output(dw, "dw", x, (vocab, dim), grad_dtype) if need_dw else None
     ws, at, have = _workspace(workspace, x,
-                              lib().rcc_linear_ce_workspace(tokens, vocab, dim, 1, grad))
-    _check(lib().rcc_linear_ce_backward(
+                              _lib.rcc_linear_ce_workspace(tokens, vocab, dim, 1, grad))
+    _check(_lib.rcc_linear_ce_backward(
         x.data_ptr(), ld_x, w.data_ptr(), ld_w, labels.data_ptr(), index, at_lse, at_dloss,
         tokens, vocab, dim, None if dx is None else dx.data_ptr(),
         None if dw is None else dw.data_ptr(), grad, 1 if accumulate else 0, at, have,
