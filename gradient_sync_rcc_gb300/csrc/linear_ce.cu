@@ -162,6 +162,40 @@ __device__ __forceinline__ void tmem_add16(uint32_t at, float* v) {
   for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
 
+// v = 128 columns of this thread's row; the whole warp calls it
+#define RCC_8(v, i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), \
+                    "=f"(v[i + 4]), "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
+#define RCC_32(v, i) RCC_8(v, i), RCC_8(v, i + 8), RCC_8(v, i + 16), RCC_8(v, i + 24)
+__device__ __forceinline__ void tmem_load128(uint32_t at, float (&v)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%32, %33, %34, %35, %36, %37, %38, %39, "
+      "%40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, "
+      "%56, %57, %58, %59, %60, %61, %62, %63}, [%129];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%64, %65, %66, %67, %68, %69, %70, %71, "
+      "%72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, "
+      "%88, %89, %90, %91, %92, %93, %94, %95}, [%130];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%96, %97, %98, %99, %100, %101, %102, %103, "
+      "%104, %105, %106, %107, %108, %109, %110, %111, "
+      "%112, %113, %114, %115, %116, %117, %118, %119, "
+      "%120, %121, %122, %123, %124, %125, %126, %127}, [%131];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : RCC_32(v, 0), RCC_32(v, 32), RCC_32(v, 64), RCC_32(v, 96)
+      : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
+      : "memory");
+}
+#undef RCC_32
+#undef RCC_8
+
 // ---- the product -------------------------------------------------------------------
 
 constexpr int kBM = 128;   // rows of C of one block
@@ -532,16 +566,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     for (int t = first; t < tiles; t += stride) {
       const Tile tile = tile_of(g, t);
       float v[kHalf];
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) v[i] = 0.f;
       for (int k0 = tile.k0; k0 < tile.k1; k0 += g.chunk) {
         // A wait that ran out leaves NaN in everything this block still owes.
         ok = ok && bar_wait(acc_full + 8 * buf, acc_phase);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tmem_fence_after();
         const uint32_t acc = tmem + buf * kBN + half * kHalf + ((uint32_t)(quarter * 32) << 16);
+        if (k0 == tile.k0) {
+          tmem_load128(acc, v);
+        } else {
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 16) tmem_add16(acc + c, v + c);
+          for (int c = 0; c < kHalf; c += 16) tmem_add16(acc + c, v + c);
+        }
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -628,37 +664,43 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts)
   }
 }
 
-constexpr int kSliceParts = 8;
+constexpr int kSliceThreads = 256, kSliceParts = 8;
 
-// out = the sum of the slices: 32 threads of eight elements, eight sums each
+// out = the sum of the slices: `parts` sums of eight elements each, a power of
+// two up to kSliceParts, which the first one adds up
 template <typename T>
-__global__ void __launch_bounds__(32 * kSliceParts)
-    join_slices_kernel(const float* part, int slices, size_t n, T* out, bool wide) {
-  __shared__ float red[kSliceParts][8][33];
+__global__ void __launch_bounds__(kSliceThreads)
+    join_slices_kernel(const float* part, int slices, size_t n, T* out, bool wide, int parts) {
+  __shared__ float red[kSliceThreads * 8 + 8 * kSliceParts];
   pdl_wait_then_release();
-  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const size_t i = ((size_t)blockIdx.x * 32 + x) * 8;
+  const int across = kSliceThreads / parts;
+  const int x = threadIdx.x % across, y = threadIdx.x / across;
+  const size_t i = ((size_t)blockIdx.x * across + x) * 8;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (i < n) {
-    for (int k = y; k < slices; k += 4 * kSliceParts) {
+    for (int k = y; k < slices; k += 4 * parts) {
       float v[4][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)  // past the last slice: it again, not added
-        load8(part + (size_t)min(k + u * kSliceParts, slices - 1) * n + i, v[u]);
+      for (int u = 0; u < 4; ++u)
+        if (k + u * parts < slices) load8(part + (size_t)(k + u * parts) * n + i, v[u]);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
+        if (k + u * parts < slices) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += k + u * kSliceParts < slices ? v[u][e] : 0.f;
+          for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+        }
     }
   }
+  if (parts > 1) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[y][e][x] = s[e];
-  __syncthreads();
-  if (y != 0 || i >= n) return;
+    for (int e = 0; e < 8; ++e) red[(y * 8 + e) * (across + 1) + x] = s[e];
+    __syncthreads();
+    if (y != 0) return;
+    for (int k = 1; k < parts; ++k)
 #pragma unroll
-  for (int k = 1; k < kSliceParts; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] += red[k][e][x];
+      for (int e = 0; e < 8; ++e) s[e] += red[(k * 8 + e) * (across + 1) + x];
+  }
+  if (i >= n) return;
   if (wide || sizeof(T) == 2) {
     store8(out + i, s);
   } else {
@@ -785,8 +827,20 @@ Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
   const int cg = paired(tokens) ? 2 : 1;
   const size_t tiles = ceil_div(tokens, kBM * cg) * ceil_div(dim, kBN);
   const size_t units = sm_count() / cg, k_blocks = p.width / kBK;
-  // few tiles and a long sum: split the sum until every SM has some
-  p.splits = (int)std::max<size_t>(1, std::min(units / tiles, k_blocks / 8));
+  // Pieces of the sum of dx, each added up by itself: the fewest turns of all
+  // SMs, at 0.27 us for a stage's products, against writing and reading a
+  // slice more, at 6 TB/s.
+  p.splits = 1;
+  double best = 0;
+  for (size_t s = 1; s <= 64 && s <= std::max<size_t>(1, k_blocks / 8); ++s) {
+    const double turns = (double)ceil_div(tiles * s, units);
+    const double us = turns * (double)ceil_div(k_blocks, s) * 0.27 * p.parts +
+                      (s > 1 ? (double)(s * tokens * dim) * 8 / 6e6 + 4 : 0);
+    if (s == 1 || us < best) {
+      best = us;
+      p.splits = (int)s;
+    }
+  }
   const bool direct = p.splits == 1 && (p.count == 1 || grad_type == RCC_F32);
   p.dx_bytes = direct ? 0 : up256(p.splits * tokens * dim * 4);
   return p;
@@ -899,14 +953,16 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
   }
   if (a.dx && slices) {
     const size_t n = a.tokens * a.dim;
-    const dim3 grid((unsigned)ceil_div(n, 32 * 8)), block(32 * kSliceParts);
+    int parts = 1;
+    while (parts < kSliceParts && 2 * parts <= p.splits) parts *= 2;
+    const dim3 grid((unsigned)ceil_div(n, kSliceThreads / parts * 8)), block(kSliceThreads);
     e = a.grad_type == RCC_F32
             ? launch_kernel(join_slices_kernel<float>, grid, block, 0, stream,
                             (const float*)slices, p.splits, n, static_cast<float*>(a.dx),
-                            (reinterpret_cast<uintptr_t>(a.dx) & 31u) == 0)
+                            (reinterpret_cast<uintptr_t>(a.dx) & 31u) == 0, parts)
             : launch_kernel(join_slices_kernel<__nv_bfloat16>, grid, block, 0, stream,
                             (const float*)slices, p.splits, n, static_cast<__nv_bfloat16*>(a.dx),
-                            true);
+                            true, parts);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
