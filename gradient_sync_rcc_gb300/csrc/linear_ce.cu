@@ -221,7 +221,8 @@ struct GemmArgs {
   int m_tiles, n_tiles;  // of kBM * CG rows, of bn columns
   int bn;                // columns of a tile, a multiple of 16 up to kBN
   int a_rows;            // rows of A's box (not MN), a multiple of 8 up to kBM
-  int k_blocks, splits;  // of kBK; pieces of the sum, each with a C of its own
+  int k_blocks, splits;  // of bk; pieces of the sum, each with a C of its own
+  int bk;                // of the sum per stage, a multiple of 16 up to kBK
   int chunk;             // k_blocks that one accumulator takes
   int group;             // tiles of rows that share a run over the columns
   int b_row0;            // first row of B (vocabulary entry) of this piece
@@ -248,11 +249,11 @@ struct GemmArgs {
 // Shared-memory descriptor of a tile in rows of 128 bytes, swizzled by 128.
 // Along the sum (K major): a row holds 64 of the sum, eight rows are 1,024
 // bytes.  Across it (MN major): a row holds 64 rows of the matrix, eight of
-// the sum are 1,024 bytes, and 64 rows of the matrix a block of 8,192.
+// the sum are 1,024 bytes, and 64 rows of the matrix a block of 128 bk.
 template <bool MN>
-__device__ __forceinline__ uint64_t smem_desc(uint32_t at) {
+__device__ __forceinline__ uint64_t smem_desc(uint32_t at, int bk) {
   uint64_t d = (uint64_t)((at >> 4) & 0x3FFF);
-  d |= (uint64_t)(MN ? (kBK * 128) >> 4 : 1) << 16;  // between blocks of 64 rows
+  d |= (uint64_t)(MN ? (bk * 128) >> 4 : 1) << 16;  // between blocks of 64 rows
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
@@ -442,6 +443,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const uint32_t rank = CG == 2 ? cta_rank() : 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
   const int tiles = g.m_tiles * g.n_tiles * g.splits;
+  // A short sum of both MN major takes stages of less than kBK: rows that do
+  // not exist are not copied as zeros.
+  const int bk = A_MN && B_MN ? g.bk : kBK;
 
   if (tid == 0) {
     for (int s = 0; s < S::kCount; ++s) {
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       // B's box has g.bn / CG rows.  A's may have less than kBM: the rows of
       // shared memory past it hold anything, and their sums are not used.
       const uint32_t stage_bytes = (PARTS * (A_MN ? kBM : g.a_rows) +
-                                    (B_MN ? S::kBRows : g.bn / CG)) * kRowBytes;
+                                    (B_MN ? S::kBRows : g.bn / CG)) * bk * 2;
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             if constexpr (A_MN) {
 #pragma unroll
               for (int j = 0; j < kBM / 64; ++j)
-                tma_load<CG>(to + j * kBK * 128, &g.a[p], m0 + 64 * j, k * kBK, bar);
+                tma_load<CG>(to + j * bk * 128, &g.a[p], m0 + 64 * j, k * bk, bar);
             } else {
               tma_load<CG>(to, &g.a[p], k * kBK, m0, bar);
             }
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           if constexpr (B_MN) {
 #pragma unroll
             for (int j = 0; j < S::kBRows / 64; ++j)
-              tma_load<CG>(to + j * kBK * 128, &g.b, n0 + 64 * j, g.b_row0 + k * kBK, bar);
+              tma_load<CG>(to + j * bk * 128, &g.b, n0 + 64 * j, g.b_row0 + k * bk, bar);
           } else {
             tma_load<CG>(to, &g.b, k * kBK, g.b_row0 + n0, bar);
           }
@@ -536,15 +540,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             if (!(ok = bar_wait(full + 8 * s, phase))) break;
             tmem_fence_after();
             const uint32_t at = base + s * S::kBytes;
-            const uint64_t b = smem_desc<B_MN>(at + PARTS * S::kABytes);
+            const uint64_t b = smem_desc<B_MN>(at + PARTS * S::kABytes, bk);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
-              const uint64_t a = smem_desc<A_MN>(at + p * S::kABytes);
+              const uint64_t a = smem_desc<A_MN>(at + p * S::kABytes, bk);
 #pragma unroll
-              for (int i = 0; i < kBK / 16; ++i)
+              for (int i = 0; i < kBK / 16; ++i) {
+                if (A_MN && B_MN && i * 16 >= bk) break;
                 // 16 of the sum: 32 bytes along a row, or 16 rows of 128 bytes
                 mma<CG>(d, a + i * ((A_MN ? 2048 : 32) >> 4), b + i * ((B_MN ? 2048 : 32) >> 4),
                         idesc, k > k0 || p > 0 || i > 0);
+              }
             }
             mma_commit<CG>(empty + 8 * s);
             if (++s == S::kCount) {
@@ -764,6 +770,12 @@ cudaError_t launch_gemm_of(GemmArgs& g, cudaStream_t stream) {
 // 254 us with 128 rows, 64 tokens 169.
 int box_rows(size_t rows) { return (int)std::min<size_t>(kBM, (rows + 7) / 8 * 8); }
 
+// Of a sum of k per stage: as even as multiples of 16 allow
+int stage_rows(size_t k) {
+  const size_t stages = ceil_div(k, kBK);
+  return (int)(ceil_div(ceil_div(k, stages), 16) * 16);
+}
+
 // Rows of C, columns, and the extent of the sum; the maps are the caller's.
 template <int PARTS, bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, int bn, int splits,
@@ -774,7 +786,8 @@ cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, in
   g.bn = bn;
   g.a_rows = box_rows(m);
   g.n_tiles = (int)ceil_div(n, bn);
-  g.k_blocks = (int)ceil_div(k, kBK);
+  g.bk = A_MN && B_MN ? stage_rows(k) : kBK;
+  g.k_blocks = (int)ceil_div(k, g.bk);
   g.splits = splits;
   g.group = group;
   g.chunk = EPI == kEpiOut && g.c_type == RCC_BF16 ? g.k_blocks : kChunkMmas / (PARTS * (kBK / 16));
@@ -940,8 +953,8 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.add = a.accumulate;
       g.wide = wide_rows(g.c, a.dim, grad_size);
       for (int k = 0; k < p.parts; ++k)
-        if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, kBK)) return cudaErrorInvalidValue;
-      if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, kBK)) return cudaErrorInvalidValue;
+        if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, stage_rows(a.tokens))) return cudaErrorInvalidValue;
+      if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, stage_rows(a.tokens))) return cudaErrorInvalidValue;
       const bool wide = paired(width);
       e = p.parts == 2 ? launch_gemm<2, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, kBN, 1,
                                                              kGradGroup, stream)
