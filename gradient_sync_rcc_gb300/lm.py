@@ -46,9 +46,12 @@ def _type(t, what):
 
 def _matrix(t, what, dev):
     """Rows, columns and row stride of a matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.get_device() != dev:
+    shape = t.shape
+    if len(shape) != 2 or t.get_device() != dev:
         raise ValueError("%s must be a matrix on the inputs' device" % what)
-    n, d = t.shape
+    n, d = shape
+    if t.is_contiguous():
+        return n, d, d
     ld, step = t.stride()
     if step != 1 and d != 1:
         raise ValueError("the rows of %s must be contiguous" % what)
@@ -110,12 +113,20 @@ def embedding_forward(table, ids, scale=1.0, out=None, out_dtype=None, stream=No
     index = _index(ids, "ids", dev, tokens)
     kind = _type(table, "table")
     if out is None:
-        out = torch.empty((tokens, dim), dtype=out_dtype or table.dtype, device=table.device)
+        if out_dtype is None:
+            out_dtype = table.dtype
+        out_kind = _TYPES.get(out_dtype)
+        if out_kind is None:
+            raise ValueError("out_dtype must be float32 or bfloat16, not %s" % out_dtype)
+        out = torch.empty((tokens, dim), dtype=out_dtype, device=table.device)
     else:
         _output(out, "out", table, (tokens, dim), out_dtype or out.dtype)
-    _check(_lib.rcc_embedding_forward(
+        out_kind = _type(out, "out")
+    st = _lib.rcc_embedding_forward(
         table.data_ptr(), kind, ld, ids.data_ptr(), index, tokens, vocab, dim, scale,
-        out.data_ptr(), _type(out, "out"), _stream(stream, dev)))
+        out.data_ptr(), out_kind, _stream(stream, dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -149,51 +160,58 @@ KEEP_GROUP = 128   # columns that share one scale of the 8-bit form
 
 class Kept:
     """A norm's input in 8 bits: values [tokens, 128 G] int8 and scales
-    [tokens, G] float32 of its `dim` columns, G = ceil(dim / 128)."""
+    [tokens, G] float32 of its `dim` columns, G = ceil(dim / 128), one after
+    the other in one buffer."""
 
-    __slots__ = ("values", "scales", "dim")
+    __slots__ = ("data", "tokens", "dim", "groups", "_scales_at")
 
-    def __init__(self, values, scales, dim):
-        self.values, self.scales, self.dim = values, scales, dim
+    def __init__(self, tokens, dim, device):
+        self.tokens, self.dim, self.groups = tokens, dim, -(-dim // KEEP_GROUP)
+        self._scales_at = tokens * self.groups * KEEP_GROUP
+        self.data = torch.empty(self._scales_at + tokens * self.groups * 4, dtype=torch.uint8,
+                                device=device)
 
-    @classmethod
-    def empty(cls, tokens, dim, device):
-        groups = -(-dim // KEEP_GROUP)
-        return cls(torch.empty((tokens, groups * KEEP_GROUP), dtype=torch.int8, device=device),
-                   torch.empty((tokens, groups), dtype=torch.float32, device=device), dim)
+    @property
+    def values(self):
+        return self.data[:self._scales_at].view(torch.int8).view(self.tokens,
+                                                                 self.groups * KEEP_GROUP)
+
+    @property
+    def scales(self):
+        return self.data[self._scales_at:].view(torch.float32).view(self.tokens, self.groups)
 
     def dequantize(self):
         """What it stands for, [tokens, dim] float32."""
-        t, g = self.scales.shape
+        t, g = self.tokens, self.groups
         v = self.values.view(t, g, KEEP_GROUP) * self.scales[:, :, None]
         return v.view(t, g * KEEP_GROUP)[:, :self.dim]
 
-    def _checked(self, tokens, dim, like):
-        groups = -(-dim // KEEP_GROUP)
-        if self.dim != dim:
-            raise ValueError("kept holds %d columns where %d are needed" % (self.dim, dim))
-        _output(self.values, "kept.values", like, (tokens, groups * KEEP_GROUP), torch.int8)
-        _output(self.scales, "kept.scales", like, (tokens, groups), torch.float32)
-        return self.values.data_ptr(), self.scales.data_ptr()
+    def _checked(self, tokens, dim, dev):
+        """The addresses of the values and the scales."""
+        if self.dim != dim or self.tokens != tokens or self.data.get_device() != dev:
+            raise ValueError("kept holds %d x %d on %s where %d x %d on the inputs' device is needed"
+                             % (self.tokens, self.dim, self.data.device, tokens, dim))
+        at = self.data.data_ptr()
+        return at, at + self._scales_at
 
 
 def rmsnorm_forward(x, weight, eps=1e-6, keep=False, out=None, stream=None):
     """rcc_rmsnorm_forward.  Returns y, or (y, kept) with keep: True, or a Kept
-    to be written."""
+    of these sizes to be written."""
     dev = x.get_device()
     tokens, dim, ld = _matrix(x, "x", dev)
     kind = _type(x, "x")
     w = _floats(weight, "weight", dev, dim)
-    y = _output(out, "out", x, (tokens, dim), x.dtype)
+    y = torch.empty_like(x) if out is None and ld == dim else \
+        _output(out, "out", x, (tokens, dim), x.dtype)
     kept = q = s = None
-    if keep is True:
-        kept = Kept.empty(tokens, dim, x.device)
-        q, s = kept.values.data_ptr(), kept.scales.data_ptr()
-    elif keep:
-        kept = keep
-        q, s = kept._checked(tokens, dim, x)
-    _check(_lib.rcc_rmsnorm_forward(x.data_ptr(), kind, ld, w, eps, tokens, dim, y.data_ptr(),
-                                     q, s, _stream(stream, dev)))
+    if keep:
+        kept = Kept(tokens, dim, x.device) if keep is True else keep
+        q, s = kept._checked(tokens, dim, dev)
+    st = _lib.rcc_rmsnorm_forward(x.data_ptr(), kind, ld, w, eps, tokens, dim, y.data_ptr(), q, s,
+                                  _stream(stream, dev))
+    if st:
+        _check(st)
     return y if kept is None else (y, kept)
 
 
@@ -208,11 +226,12 @@ def rmsnorm_backward(dy, kept, weight, eps=1e-6, dx=None, dweight=None, accumula
     dev = dy.get_device()
     tokens, dim, ld = _matrix(dy, "dy", dev)
     kind = _type(dy, "dy")
-    q, s = kept._checked(tokens, dim, dy)
+    q, s = kept._checked(tokens, dim, dev)
     w = _floats(weight, "weight", dev, dim)
     if accumulate and dweight is None:
         raise ValueError("accumulate needs the dweight to add to")
-    dx = _output(dx, "dx", dy, (tokens, dim), dy.dtype)
+    dx = torch.empty_like(dy) if dx is None and ld == dim else \
+        _output(dx, "dx", dy, (tokens, dim), dy.dtype)
     dweight = _output(dweight, "dweight", dy, (dim,), torch.float32)
     ws, at, have = _workspace(workspace, dy, rmsnorm_backward_workspace(tokens, dim))
     _check(_lib.rcc_rmsnorm_backward(

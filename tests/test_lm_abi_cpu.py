@@ -136,11 +136,11 @@ def test_binding_refuses_what_the_pointers_hide(L):
             L.rmsnorm_forward(*args)
     with pytest.raises(ValueError, match="CUDA device"):
         L.rmsnorm_forward(x, weight, keep=True)
-    kept = L.Kept.empty(4, 255, "cpu")
+    kept = L.Kept(4, 255, "cpu")
     with pytest.raises(ValueError):
         L.rmsnorm_backward(x, kept, weight)
     with pytest.raises(ValueError):
-        L.rmsnorm_backward(x, L.Kept.empty(4, 256, "cpu"), weight, accumulate=True)
+        L.rmsnorm_backward(x, L.Kept(4, 256, "cpu"), weight, accumulate=True)
     x, w = torch.zeros(4, 64, dtype=b), torch.zeros(100, 64, dtype=b)
     lab, v = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
     for args in ((x.to(f), w, lab), (x, w.to(f), lab), (x, w[:, :32], lab), (x, w, lab[:2])):
