@@ -79,15 +79,25 @@ __device__ __forceinline__ void widen4(uint32_t q, float2& a, float2& b) {
 template <int G>
 constexpr int kBlock = G > 256 ? G : 256;
 
-// A thread holds parts of 16 bytes: kE consecutive elements, as they lie in
-// memory or as kE / 2 fp32 pairs.  Part p of thread t of the G that share a row
-// begins at column (p G + t) kE, so neighbouring threads read neighbouring
-// parts, and 128 / kE threads hold a group of 128 columns.
-template <typename T>
+// A thread holds parts of 16 bytes, kE elements, as they lie in memory or as
+// kE / 2 fp32 pairs; a part's columns are p G kE after those of part 0.
+//   VEC (aligned rows of whole parts): kE neighbouring columns from t kE of
+//   thread t of the G that share a row, so that 128 / kE threads hold a group
+//   of 128 columns.
+//   else (any alignment and width): every 32nd column of the warp's 32 kE, so
+//   that a warp's single elements lie side by side; four of them on all lanes
+//   are a group, so a part has kE / 4 groups.
+template <typename T, bool VEC>
 struct Part {
   static constexpr int kE = 16 / (int)sizeof(T);
   static constexpr int kPairs = kE / 2;
   static constexpr int kBytes8 = kE / 4;  // words of the 8-bit form
+  static constexpr int kScales = VEC ? 1 : kE / 4;
+  static constexpr int kLanes = VEC ? (int)kKeepGroup / kE : 32;  // that share a group
+  static constexpr int kStep = VEC ? 1 : 32;  // columns from an element to the next
+  static __device__ __forceinline__ int first_column(int t) {
+    return VEC ? t * kE : t / 32 * 32 * kE + t % 32;
+  }
 };
 __device__ __forceinline__ void widen(const uint4& r, float2 (&v)[4], __nv_bfloat16) {
   widen2(r.x, v[0].x, v[0].y);
@@ -107,31 +117,30 @@ __device__ __forceinline__ uint4 narrow(const float2 (&v)[2], float) {
   return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
                     __float_as_uint(v[1].y));
 }
-// A part at p: whole and aligned (VEC), or of any alignment with `left`
-// elements there, what lies past them as zeros and not written
+// A part at p; past `left` columns its elements are zeros and not written
 template <bool VEC, typename T>
 __device__ __forceinline__ uint4 load_part(const T* p, int left) {
   if constexpr (VEC) {
     return *reinterpret_cast<const uint4*>(p);
   } else {
-    float2 v[Part<T>::kPairs];
+    float2 v[Part<T, VEC>::kPairs];
 #pragma unroll
-    for (int e = 0; e < Part<T>::kPairs; ++e) {
-      v[e].x = 2 * e < left ? to_f32(p[2 * e]) : 0.f;
-      v[e].y = 2 * e + 1 < left ? to_f32(p[2 * e + 1]) : 0.f;
+    for (int e = 0; e < Part<T, VEC>::kPairs; ++e) {
+      v[e].x = 64 * e < left ? to_f32(p[64 * e]) : 0.f;
+      v[e].y = 64 * e + 32 < left ? to_f32(p[64 * e + 32]) : 0.f;
     }
     return narrow(v, T());
   }
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_part(T* p, int left, const float2 (&v)[Part<T>::kPairs]) {
+template <bool VEC, typename T, int PAIRS>
+__device__ __forceinline__ void store_part(T* p, int left, const float2 (&v)[PAIRS]) {
   if constexpr (VEC) {
     *reinterpret_cast<uint4*>(p) = narrow(v, T());
   } else {
 #pragma unroll
-    for (int e = 0; e < Part<T>::kPairs; ++e) {
-      if (2 * e < left) from_f32(v[e].x, p[2 * e]);
-      if (2 * e + 1 < left) from_f32(v[e].y, p[2 * e + 1]);
+    for (int e = 0; e < PAIRS; ++e) {
+      if (64 * e < left) from_f32(v[e].x, p[64 * e]);
+      if (64 * e + 32 < left) from_f32(v[e].y, p[64 * e + 32]);
     }
   }
 }
@@ -139,10 +148,45 @@ __device__ __forceinline__ void store_part(T* p, int left, const float2 (&v)[Par
 template <bool VEC, int PAIRS>
 __device__ __forceinline__ void load_weight(const float* w, int left, float2 (&v)[PAIRS]) {
 #pragma unroll
-  for (int e = 0; e < PAIRS; e += 2) {
-    const uint4 f = load_part<VEC>(w + 2 * e, left - 2 * e);
+  for (int e = 0; e < PAIRS; e += 2) {  // four columns at a time: a part of fp32
+    const int at = VEC ? 2 * e : 64 * e;
+    const uint4 f = load_part<VEC>(w + at, left - at);
     v[e] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
     v[e + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+  }
+}
+// The bytes of a part: kBytes8 words, whatever the layout
+template <bool VEC, int WORDS>
+__device__ __forceinline__ void load_bytes(const int8_t* p, int left, uint32_t (&q)[WORDS]) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      q[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((4 * i + e) * 32 < left)
+          q[i] |= (uint32_t)(uint8_t)p[(4 * i + e) * 32] << (8 * e);
+    }
+  } else if constexpr (WORDS == 2) {
+    const uint2 two = *reinterpret_cast<const uint2*>(p);
+    q[0] = two.x;
+    q[1] = two.y;
+  } else {
+    q[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+template <bool VEC, int WORDS>
+__device__ __forceinline__ void store_bytes(int8_t* p, int left, const uint32_t (&q)[WORDS]) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((4 * i + e) * 32 < left) p[(4 * i + e) * 32] = (int8_t)(q[i] >> (8 * e));
+  } else if constexpr (WORDS == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(p) = q[0];
   }
 }
 
@@ -189,7 +233,7 @@ constexpr int blocks_per_sm(int all, int threads, int shared) {
 template <typename T, int G, int NV, bool VEC>
 struct NormFore {
   static constexpr int kThreads = kBlock<G>;
-  static constexpr int kParts = NV * 8 / Part<T>::kE;
+  static constexpr int kParts = NV * 8 / Part<T, VEC>::kE;
   static constexpr int kStage = kThreads * kParts * 16;
   static constexpr int kFit = kSharedMost / kStage;
   static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kForeStages ? kFit : kForeStages) : 0;
@@ -202,7 +246,7 @@ struct NormFore {
 template <typename T, int G, int NV, bool VEC>
 __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs a) {
   using F = NormFore<T, G, NV, VEC>;
-  using P = Part<T>;
+  using P = Part<T, VEC>;
   constexpr int kThreads = F::kThreads, kRows = kThreads / G, kStages = F::kStages;
   constexpr int kParts = F::kParts;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -210,17 +254,18 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
   pdl_wait_then_release();
   const int tid = threadIdx.x, t = tid % G;
   constexpr int kSpan = G * P::kE;  // columns from a thread's part to its next
-  const int dim = (int)a.dim, left = dim - t * P::kE;
+  const int col = P::first_column(t);
+  const int dim = (int)a.dim, left = dim - col;
   const int groups = (dim + (int)kKeepGroup - 1) / (int)kKeepGroup;
-  const int kept_left = groups * (int)kKeepGroup - t * P::kE;
+  const int kept_left = groups * (int)kKeepGroup - col;
   const float inv_dim = 1.f / (float)dim;
   // this thread's first part of its row, here and in the row that is copied ahead
   size_t row = (size_t)blockIdx.x * kRows + tid / G;
   const size_t step = (size_t)gridDim.x * kRows;
-  const T* ahead = static_cast<const T*>(a.x) + row * a.ld_x + t * P::kE;
-  T* y = static_cast<T*>(a.y) + row * a.ld_y + t * P::kE;
-  int8_t* kept = a.kept + row * groups * kKeepGroup + t * P::kE;
-  float* scales = a.scales + row * groups + t * P::kE / (int)kKeepGroup;
+  const T* ahead = static_cast<const T*>(a.x) + row * a.ld_x + col;
+  T* y = static_cast<T*>(a.y) + row * a.ld_y + col;
+  int8_t* kept = a.kept + row * groups * kKeepGroup + col;
+  float* scales = a.scales + row * groups + col / (int)kKeepGroup;
   size_t ahead_row = row;
   auto x_at = [&](int s, int p) {
     return reinterpret_cast<uint4*>(smem + s * F::kStage) + p * kThreads + tid;
@@ -240,7 +285,7 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
 #pragma unroll
   for (int p = 0; p < kParts; ++p)
     if (left > p * kSpan)
-      load_weight<VEC>(a.weight + t * P::kE + p * kSpan, left - p * kSpan, w[p]);
+      load_weight<VEC>(a.weight + col + p * kSpan, left - p * kSpan, w[p]);
   int stage = 0, flip = 0;
   for (size_t first = (size_t)blockIdx.x * kRows; first < a.tokens; first += step, row += step) {
     const bool live = kRows == 1 || row < a.tokens;
@@ -269,30 +314,38 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       if (a.kept) {
-        float amax = 0.f;
+        constexpr int kOf = P::kPairs / P::kScales;  // pairs of one group
+        float amax[P::kScales];
 #pragma unroll
-        for (int e = 0; e < P::kPairs; ++e)
-          amax = max_nan(max_nan(amax, fabsf(v[p][e].x)), fabsf(v[p][e].y));
+        for (int i = 0; i < P::kScales; ++i) {
+          amax[i] = 0.f;
 #pragma unroll
-        for (int o = (int)kKeepGroup / P::kE / 2; o > 0; o >>= 1)
-          amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          for (int e = i * kOf; e < (i + 1) * kOf; ++e)
+            amax[i] = max_nan(max_nan(amax[i], fabsf(v[p][e].x)), fabsf(v[p][e].y));
+#pragma unroll
+          for (int o = P::kLanes / 2; o > 0; o >>= 1)
+            amax[i] = max_nan(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], o));
+        }
         if (live && kept_left > p * kSpan) {
-          // a NaN or infinity: zeros and a NaN scale; next to nothing: zeros
-          const bool fine = amax >= kTiny && amax < INFINITY;
-          const float inv = fine ? 127.f * __frcp_rn(amax) : 0.f;
           uint32_t q[P::kBytes8];
 #pragma unroll
-          for (int i = 0; i < P::kBytes8; ++i)
-            q[i] = __byte_perm(quantize2(v[p][2 * i], inv), quantize2(v[p][2 * i + 1], inv),
-                               0x5410);
-          if (!fine) q[0] = q[P::kBytes8 - 1] = 0u;
-          if constexpr (P::kBytes8 == 2)
-            *reinterpret_cast<uint2*>(kept + p * kSpan) = make_uint2(q[0], q[P::kBytes8 - 1]);
-          else
-            *reinterpret_cast<uint32_t*>(kept + p * kSpan) = q[0];
-          if (t % ((int)kKeepGroup / P::kE) == 0)
-            scales[p * (kSpan / (int)kKeepGroup)] =
-                fine ? amax * (1.f / 127.f) : amax < kTiny ? 0.f : __uint_as_float(0x7FC00000u);
+          for (int i = 0; i < P::kScales; ++i) {
+            // a NaN or infinity: zeros and a NaN scale; next to nothing: zeros
+            const bool fine = amax[i] >= kTiny && amax[i] < INFINITY;
+            const float inv = fine ? 127.f * __frcp_rn(amax[i]) : 0.f;
+            constexpr int kWords = P::kBytes8 / P::kScales;
+#pragma unroll
+            for (int k = i * kWords; k < (i + 1) * kWords; ++k) {
+              q[k] = __byte_perm(quantize2(v[p][2 * k], inv), quantize2(v[p][2 * k + 1], inv),
+                                 0x5410);
+              if (!fine) q[k] = 0u;
+            }
+            if (t % P::kLanes == 0 && kept_left > p * kSpan + i * (int)kKeepGroup)
+              scales[p * (kSpan / (int)kKeepGroup) + i] =
+                  fine ? amax[i] * (1.f / 127.f)
+                       : amax[i] < kTiny ? 0.f : __uint_as_float(0x7FC00000u);
+          }
+          store_bytes<VEC>(kept + p * kSpan, kept_left - p * kSpan, q);
         }
       }
       if (live && left > p * kSpan) {
@@ -318,8 +371,8 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
 template <typename T, int G, int NV, bool VEC>
 struct NormBack {
   static constexpr int kThreads = kBlock<G>;
-  static constexpr int kParts = NV * 8 / Part<T>::kE;
-  static constexpr int kStage = kThreads * kParts * (16 + Part<T>::kE + 4);
+  static constexpr int kParts = NV * 8 / Part<T, VEC>::kE;
+  static constexpr int kStage = kThreads * kParts * (16 + Part<T, VEC>::kE + 4);
   static constexpr bool kHoldWeight = kThreads * NV * 32 + 2 * kStage <= kSharedMost;
   static constexpr int kWeight = kHoldWeight ? kThreads * NV * 32 : 0;
   static constexpr int kFit = (kSharedMost - kWeight) / kStage;
@@ -334,9 +387,10 @@ struct NormBack {
 // Bandwidth bound: rows are copied ahead into shared memory (aligned rows,
 // VEC) while the current one is reduced.
 template <typename T, int G, int NV, bool VEC>
-__global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC>::kPerSm)
+    norm_backward_kernel(const NormGradArgs a) {
   using B = NormBack<T, G, NV, VEC>;
-  using P = Part<T>;
+  using P = Part<T, VEC>;
   constexpr int kThreads = B::kThreads, kRows = kThreads / G, kStages = B::kStages;
   constexpr int kParts = B::kParts;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -344,16 +398,17 @@ __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGrad
   pdl_wait_then_release();
   const int tid = threadIdx.x, t = tid % G;
   constexpr int kSpan = G * P::kE;  // columns from a thread's part to its next
-  const int dim = (int)a.dim, left = dim - t * P::kE;
+  const int col = P::first_column(t);
+  const int dim = (int)a.dim, left = dim - col;
   const int groups = (dim + (int)kKeepGroup - 1) / (int)kKeepGroup;
   const float inv_dim = 1.f / (float)dim;
   size_t row = (size_t)blockIdx.x * kRows + tid / G;
   const size_t step = (size_t)gridDim.x * kRows;
   // this thread's first part of the row that is copied ahead, and of its output
-  const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + t * P::kE;
-  const int8_t* kept = a.kept + row * groups * kKeepGroup + t * P::kE;
-  const float* scales = a.scales + row * groups + t * P::kE / (int)kKeepGroup;
-  T* dx_out = static_cast<T*>(a.dx) + row * a.ld_dx + t * P::kE;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + col;
+  const int8_t* kept = a.kept + row * groups * kKeepGroup + col;
+  const float* scales = a.scales + row * groups + col / (int)kKeepGroup;
+  T* dx_out = static_cast<T*>(a.dx) + row * a.ld_dx + col;
   size_t ahead_row = row;
   // what neighbouring threads hold of one kind lies side by side
   auto weight_at = [&](int p, int h) {
@@ -380,7 +435,7 @@ __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGrad
         w[2 * h + 1] = make_float2(f.z, f.w);
       }
     } else {
-      load_weight<VEC>(a.weight + t * P::kE + p * kSpan, left - p * kSpan, w);
+      load_weight<VEC>(a.weight + col + p * kSpan, left - p * kSpan, w);
     }
   };
   auto next_row = [&]() {
@@ -410,7 +465,7 @@ __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGrad
   for (int p = 0; p < kParts; ++p) {
     if (B::kHoldWeight && left > p * kSpan) {
       float2 w[P::kPairs];
-      load_weight<VEC>(a.weight + t * P::kE + p * kSpan, left - p * kSpan, w);
+      load_weight<VEC>(a.weight + col + p * kSpan, left - p * kSpan, w);
 #pragma unroll
       for (int h = 0; h < P::kBytes8; ++h)
         *weight_at(p, h) = make_float4(w[2 * h].x, w[2 * h].y, w[2 * h + 1].x, w[2 * h + 1].y);
@@ -429,41 +484,41 @@ __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGrad
     uint4 raw[kParts];
     uint32_t q[kParts][P::kBytes8];
     float2 dw[kParts][P::kPairs];
-    float scale[kParts];
+    float scale[kParts][P::kScales];
     float2 xx = both(0.f), dx = both(0.f);  // sums of x'^2, of dy w x'
+    constexpr int kOf = P::kPairs / P::kScales;  // pairs of one scale
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       if (live && left > p * kSpan) {
-        const uint32_t* bytes;
         if constexpr (kStages > 0) {
           raw[p] = *dy_at(stage, p);
-          bytes = q_at(stage, p);
-          scale[p] = *scale_at(stage, p);
+          load_bytes<VEC>(reinterpret_cast<const int8_t*>(q_at(stage, p)), P::kE, q[p]);
+          scale[p][0] = *scale_at(stage, p);
         } else {
           raw[p] = load_part<VEC>(dy + p * kSpan, left - p * kSpan);
-          bytes = reinterpret_cast<const uint32_t*>(kept + p * kSpan);
-          scale[p] = scales[p * (kSpan / (int)kKeepGroup)];
+          load_bytes<VEC>(kept + p * kSpan, left - p * kSpan, q[p]);
+#pragma unroll
+          for (int i = 0; i < P::kScales; ++i)
+            scale[p][i] = left > p * kSpan + i * (int)kKeepGroup
+                              ? scales[p * (kSpan / (int)kKeepGroup) + i] : 0.f;
         }
-        if constexpr (P::kBytes8 == 2) {
-          const uint2 two = *reinterpret_cast<const uint2*>(bytes);
-          q[p][0] = two.x;
-          q[p][P::kBytes8 - 1] = two.y;
-        } else {
-          q[p][0] = bytes[0];
-        }
-        float2 x[P::kPairs], d[P::kPairs], w[P::kPairs], qq = both(0.f), dq = both(0.f);
+        float2 x[P::kPairs], d[P::kPairs], w[P::kPairs];
         weight(p, w);
         widen(raw[p], d, T());
 #pragma unroll
         for (int i = 0; i < P::kBytes8; ++i) widen4(q[p][i], x[2 * i], x[2 * i + 1]);
 #pragma unroll
-        for (int e = 0; e < P::kPairs; ++e) {  // of whole numbers; the group's scale comes after
-          dw[p][e] = mul2(d[e], w[e]);
-          qq = fma2(x[e], x[e], qq);
-          dq = fma2(dw[p][e], x[e], dq);
+        for (int i = 0; i < P::kScales; ++i) {
+          float2 qq = both(0.f), dq = both(0.f);
+#pragma unroll
+          for (int e = i * kOf; e < (i + 1) * kOf; ++e) {  // of whole numbers; their scale after
+            dw[p][e] = mul2(d[e], w[e]);
+            qq = fma2(x[e], x[e], qq);
+            dq = fma2(dw[p][e], x[e], dq);
+          }
+          xx = fma2(qq, both(scale[p][i] * scale[p][i]), xx);
+          dx = fma2(dq, both(scale[p][i]), dx);
         }
-        xx = fma2(qq, both(scale[p] * scale[p]), xx);
-        dx = fma2(dq, both(scale[p]), dx);
       }
     }
     float sum[2] = {xx.x + xx.y, dx.x + dx.y};
@@ -477,10 +532,9 @@ __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGrad
         widen(raw[p], d, T());
 #pragma unroll
         for (int i = 0; i < P::kBytes8; ++i) widen4(q[p][i], x[2 * i], x[2 * i + 1]);
-        const float rs = r * scale[p];
 #pragma unroll
         for (int e = 0; e < P::kPairs; ++e) {
-          const float2 n = mul2(x[e], both(rs));
+          const float2 n = mul2(x[e], both(r * scale[p][e / kOf]));
           acc[p][e] = fma2(d[e], n, acc[p][e]);
           out[e] = mul2(fma2(n, both(-m), dw[p][e]), both(r));
         }
@@ -494,15 +548,17 @@ __global__ void __launch_bounds__(kBlock<G>) norm_backward_kernel(const NormGrad
   }
   // one row of partial sums for each group of threads
   const int ld = groups * (int)kKeepGroup;
-  float* part = static_cast<float*>(a.workspace) +
-                ((size_t)blockIdx.x * kRows + tid / G) * ld + t * P::kE;
+  float* part = static_cast<float*>(a.workspace) + ((size_t)blockIdx.x * kRows + tid / G) * ld + col;
 #pragma unroll
-  for (int p = 0; p < kParts; ++p)
-    if (ld - t * P::kE > p * kSpan)
+  for (int p = 0; p < kParts; ++p) {
+    if (left <= p * kSpan) continue;
 #pragma unroll
-      for (int e = 0; e < P::kPairs; e += 2)
-        *reinterpret_cast<float4*>(part + p * kSpan + 2 * e) =
-            make_float4(acc[p][e].x, acc[p][e].y, acc[p][e + 1].x, acc[p][e + 1].y);
+    for (int e = 0; e < P::kPairs; e += 2) {  // four columns at a time: a part of fp32
+      const int at = p * kSpan + 2 * e * P::kStep;
+      const float2 four[2] = {acc[p][e], acc[p][e + 1]};
+      store_part<VEC>(part + at, left - at, four);
+    }
+  }
 }
 
 constexpr int kSumCols = 32, kSumRows = 32;
