@@ -2,17 +2,21 @@
 // logits, and its gradients.
 //
 //   z = x W^T      lse_t = log sum_v exp z_tv      loss_t = lse_t - z_t,label
-//   dz = dloss_t (exp(z - lse_t) - [v = label])    dx = dz W      dW = dz^T x
+//   dz = dloss_t / F (exp(z - lse_t) - [v = label])
+//   dx = F dz W    dW = F dz^T x     F = the largest finite |dloss_t|
 //
 // Four matrix products on the tensor cores, all of them the one kernel below:
 //   scores   x W^T, whose epilogue leaves one (max, sum) pair per row and
 //            256 vocabulary entries; a small kernel joins the pairs
 //   dz       x W^T again for a piece of the vocabulary, whose epilogue writes
 //            dz of the piece in bf16 (for fp32 gradients as the sum of two
-//            bf16 numbers, so that both products keep fp32's accuracy)
+//            bf16 numbers, 2^-18 of its value off at most)
 //   dx       dz W, added up over the pieces
 //   dW       dz^T x, the piece's rows
-// Sums are fp32 in tensor memory, softmax statistics fp32.
+// Sums are fp32 in tensor memory, softmax statistics fp32.  The common factor F
+// stays out of dz: with one dloss for all tokens, as a mean has, its rounding
+// would put the same error on every label's term (3e-6 of an fp32 dW instead
+// of below 1e-6).
 #include <cuda.h>
 
 #include <algorithm>
@@ -54,8 +58,10 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
                    bar), "r"(bytes) : "memory");
 }
+// Relaxed: what the arrival announces are reads of tensor memory, which are
+// complete; a release would wait for this thread's stores of the tile before.
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
@@ -147,21 +153,6 @@ __device__ __forceinline__ void tmem_fence_before() {
 __device__ __forceinline__ void tmem_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// v += 16 columns of this thread's row; the whole warp calls it
-__device__ __forceinline__ void tmem_add16(uint32_t at, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
-}
-
 // v = 128 columns of this thread's row; the whole warp calls it
 #define RCC_8(v, i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), \
                     "=f"(v[i + 4]), "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
@@ -193,6 +184,22 @@ __device__ __forceinline__ void tmem_load128(uint32_t at, float (&v)[128]) {
       : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
       : "memory");
 }
+// v += 32 columns of this thread's row; the whole warp calls it
+__device__ __forceinline__ void tmem_add32(uint32_t at, float* v) {
+  float r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : RCC_32(r, 0)
+      : "r"(at) : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] += r[i];
+}
+
 #undef RCC_32
 #undef RCC_8
 
@@ -208,10 +215,13 @@ constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
 constexpr int kTmemCols = 512;  // two accumulators of kBN columns
 // Additions on the tensor cores drop what does not fit the accumulator instead
 // of rounding it, a loss that grows with their number (3.7e-5 of dx after
-// 4,000 of them).  So an accumulator of an fp32 result takes 64 instructions of
-// 16 products at most, and the epilogue adds it up in registers, rounding to
-// nearest; a result that is rounded to bf16 is taken whole.
-constexpr int kChunkMmas = 64;
+// 4,000 of them).  So an accumulator takes a few instructions of 16 products
+// each, and the epilogue adds the accumulators up in registers, rounding to
+// nearest.  For the scores 32 (16 where a pass waits for W anyway): 64 left the
+// loss 1.3 times as far from 64 bits as plain fp32 sums, 32 half as far, and
+// 32 cost 2% of a long pass's time, 16 25%.  For fp32 gradients 64; a gradient
+// that is rounded to bf16 is taken whole.
+constexpr int kScoreMmas = 32, kScoreMmasFew = 16, kOutMmas = 64;
 
 enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
 
@@ -226,16 +236,17 @@ struct GemmArgs {
   int chunk;             // k_blocks that one accumulator takes
   int group;             // tiles of rows that share a run over the columns
   int b_row0;            // first row of B (vocabulary entry) of this piece
-  int a_x0, b_y0;        // offsets of the maps' coordinates
   // stats
   float2* part;          // [2 n_tiles][m]
   float* zlab;           // [m]
   const void* labels;
   int labels64;
   int vocab;
+  // dz and out
+  const float* dloss;    // [tokens]
+  int tokens;
   // dz
   const float* lse;
-  const float* dloss;
   __nv_bfloat16* dz[2];  // [m][ld_dz], the second one NULL for bf16 gradients
   size_t ld_dz;
   // out
@@ -340,11 +351,11 @@ __device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHa
 
 // dz of half a row; columns past the piece are not written.
 __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf], int row,
-                                            int col0, int left, bool failed) {
+                                            int col0, int left, float scale, bool failed) {
   if (row >= g.m || left <= 0) return;
   const int64_t label = load_id(g.labels, g.labels64, row, g.vocab);
   const int64_t at = label - (g.b_row0 + col0);
-  const float f = label >= 0 ? g.dloss[row] : 0.f;
+  const float f = label >= 0 ? __fdiv_rn(g.dloss[row], scale) : 0.f;
   const float ll = g.lse[row] * kLog2e;
   __nv_bfloat16* out = g.dz[0] + (size_t)row * g.ld_dz + col0;
   __nv_bfloat16* rest = g.dz[1] ? g.dz[1] + (size_t)row * g.ld_dz + col0 : nullptr;
@@ -376,13 +387,16 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
 // Half a row of C.  Whole 32-byte sectors where C's rows allow it (wide).
 template <typename T>
 __device__ __forceinline__ void epilogue_out(const GemmArgs& g, float (&v)[kHalf], int row,
-                                             int col0, int left, int split, bool failed) {
+                                             int col0, int left, int split, float scale,
+                                             bool failed) {
   if (row >= g.m) return;
   constexpr int kE = 16 / (int)sizeof(T);  // elements of 16 bytes
   T* out = static_cast<T*>(g.c) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
 #pragma unroll
   for (int c = 0; c < kHalf; c += 2 * kE) {
     if (c >= left) break;  // left is a multiple of 8, and of 16 where wide
+#pragma unroll
+    for (int i = 0; i < 2 * kE; ++i) v[c + i] *= scale;
     if (g.add) {
 #pragma unroll
       for (int h = 0; h < 2 * kE; h += kE) {
@@ -425,6 +439,23 @@ __device__ __forceinline__ void epilogue_out(const GemmArgs& g, float (&v)[kHalf
   }
 }
 
+// F: the largest finite |dloss| of the tokens that count, 1 if there is none.
+// The epilogue's 256 threads read it while the first tile is summed.
+__device__ __forceinline__ float common_factor(const GemmArgs& g, int thread, float* red) {
+  float top = 0.f;
+  for (int t = thread; t < g.tokens; t += 32 * kEpiWarps) {
+    const float f = fabsf(g.dloss[t]);
+    if (f < INFINITY && load_id(g.labels, g.labels64, t, g.vocab) >= 0) top = fmaxf(top, f);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if (thread % 32 == 0) red[thread / 32] = top;
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+#pragma unroll
+  for (int w = 0; w < kEpiWarps; ++w) top = fmaxf(top, red[w]);
+  return top > 0.f ? top : 1.f;
+}
+
 // C = A B^T tile by tile, one block (CG = 1) or a pair of blocks on two SMs
 // (CG = 2) per tile, every block or pair taking tiles in turn.  Warp 0 fills
 // the stages by TMA, warp 1 issues the products, the last warps take the
@@ -432,6 +463,7 @@ __device__ __forceinline__ void epilogue_out(const GemmArgs& g, float (&v)[kHalf
 template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
   using S = Stage<CG, PARTS>;
+  __shared__ float factor[kEpiWarps];
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t bars = base + S::kCount * S::kBytes;
@@ -566,6 +598,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   } else if (warp >= 4) {
     const int quarter = warp & 3;  // the 32 rows of tensor memory this warp may read
     const int half = (warp - 4) >> 2;
+    float scale = 1.f;
+    if constexpr (EPI != kEpiStats) scale = common_factor(g, tid - 128, factor);
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -582,7 +616,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           tmem_load128(acc, v);
         } else {
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 16) tmem_add16(acc + c, v + c);
+          for (int c = 0; c < kHalf; c += 32) tmem_add32(acc + c, v + c);
         }
         tmem_fence_before();
         __syncwarp();
@@ -599,12 +633,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       if constexpr (EPI == kEpiStats) {
         epilogue_stats(g, v, row, col0, left, 2 * tile.n + half, !ok);
       } else if constexpr (EPI == kEpiDz) {
-        epilogue_dz(g, v, row, col0, left, !ok);
+        epilogue_dz(g, v, row, col0, left, scale, !ok);
       } else {
         if (g.c_type == RCC_F32)
-          epilogue_out<float>(g, v, row, col0, left, tile.split, !ok);
+          epilogue_out<float>(g, v, row, col0, left, tile.split, scale, !ok);
         else
-          epilogue_out<__nv_bfloat16>(g, v, row, col0, left, tile.split, !ok);
+          epilogue_out<__nv_bfloat16>(g, v, row, col0, left, tile.split, scale, !ok);
       }
       __syncwarp();
     }
@@ -790,7 +824,8 @@ cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, in
   g.k_blocks = (int)ceil_div(k, g.bk);
   g.splits = splits;
   g.group = group;
-  g.chunk = EPI == kEpiOut && g.c_type == RCC_BF16 ? g.k_blocks : kChunkMmas / (PARTS * (kBK / 16));
+  const int mmas = EPI == kEpiOut ? kOutMmas : pair ? kScoreMmas : kScoreMmasFew;
+  g.chunk = EPI == kEpiOut && g.c_type == RCC_BF16 ? g.k_blocks : mmas / (PARTS * (kBK / 16));
   return pair ? launch_gemm_of<2, PARTS, A_MN, B_MN, EPI>(g, stream)
               : launch_gemm_of<1, PARTS, A_MN, B_MN, EPI>(g, stream);
 }
@@ -824,10 +859,7 @@ struct Pieces {
   size_t dz_bytes;   // of one part
   size_t dx_bytes;   // of the fp32 slices of dx, 0: summed in dx itself
 };
-#ifndef CE_DZ
-#define CE_DZ 512
-#endif
-constexpr size_t kDzBytes = (size_t)CE_DZ << 20;
+constexpr size_t kDzBytes = (size_t)512 << 20;
 
 Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
   Pieces p;
@@ -893,6 +925,19 @@ cudaError_t launch_linear_ce_forward(const CeArgs& a, cudaStream_t stream, uint6
   return e;
 }
 
+namespace {
+// what all products of the backward pass need for the common factor
+GemmArgs grad_args(const CeArgs& a) {
+  GemmArgs g = {};
+  g.labels = a.labels;
+  g.labels64 = a.labels64;
+  g.vocab = (int)a.vocab;
+  g.tokens = (int)a.tokens;
+  g.dloss = a.dloss;
+  return g;
+}
+}  // namespace
+
 cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint64_t* launches) {
   const Pieces p = pieces_of(a.tokens, a.vocab, a.dim, a.grad_type);
   char* ws = static_cast<char*>(a.workspace);
@@ -906,13 +951,9 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
   for (size_t i = 0; i < p.count; ++i) {
     const size_t v0 = i * p.width, width = std::min(p.width, a.vocab - v0);
     {  // dz of the piece
-      GemmArgs g = {};
+      GemmArgs g = grad_args(a);
       g.b_row0 = (int)v0;
-      g.labels = a.labels;
-      g.labels64 = a.labels64;
-      g.vocab = (int)a.vocab;
       g.lse = a.lse;
-      g.dloss = a.dloss;
       g.dz[0] = dz[0];
       g.dz[1] = dz[1];
       g.ld_dz = p.width;
@@ -926,7 +967,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       ++*launches;
     }
     if (a.dx) {  // dx (+)= dz W
-      GemmArgs g = {};
+      GemmArgs g = grad_args(a);
       g.b_row0 = (int)v0;
       g.c = slices ? slices : a.dx;
       g.c_type = slices ? RCC_F32 : a.grad_type;
@@ -946,7 +987,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       ++*launches;
     }
     if (a.dw) {  // the piece's rows of dW (+)= dz^T x
-      GemmArgs g = {};
+      GemmArgs g = grad_args(a);
       g.c = static_cast<char*>(a.dw) + v0 * a.dim * grad_size;
       g.c_type = a.grad_type;
       g.ld_c = a.dim;
