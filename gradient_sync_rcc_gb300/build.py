@@ -1,4 +1,5 @@
-"""Build librcc.so in-tree: the CUDA kernels and the C-ABI host layer.
+"""Build librcc.so in-tree: the CUDA kernels and the C-ABI host layer; and
+_lm.so, the torch binding of the language-model operators.
 
 nvcc, one -gencode for sm_103a, the translation units compiled in parallel,
 static CUDA runtime, only the rcc_* symbols exported.  No fast-math: means use
@@ -14,6 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librcc.so")
+BINDING = os.path.join(HERE, "_lm.so")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,10 +38,26 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def binding_command(out: str):
+    """g++ on lm_binding.cpp with Python's and torch's headers and libraries."""
+    import importlib.util
+    import sysconfig
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    lib = os.path.join(torch_dir, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=1",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(torch_dir, "include"),
+            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+            "-isystem", cuda, os.path.join(CSRC, "lm_binding.cpp"), "-o", out,
+            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-Wl,-rpath," + lib]
 
 
 def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB,
@@ -70,6 +88,11 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
         if verbose:
             print(" ".join(cmd))
         procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding = None
+    if lib == LIB:
+        binding = BINDING + ".tmp%d" % os.getpid()
+        procs.append(("lm_binding", subprocess.Popen(
+            binding_command(binding), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -87,6 +110,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
         print(" ".join(link))
     subprocess.run(link, check=True)
     os.replace(tmp, lib)
+    if binding:
+        os.replace(binding, BINDING)
     return lib
 
 
