@@ -19,66 +19,86 @@ namespace lm {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kSlab = kRowThreads * 8;  // columns of a row that one block covers
+
+// G threads take one slab of 8 G columns of a row; a block has kRowThreads / G
+// such groups.  A warp to a row up to 512 columns, else the whole block.
+template <int G>
+struct Groups {
+  static constexpr int kCount = kRowThreads / G;
+  static constexpr int kColumns = G * 8;
+};
+constexpr size_t kWarpRow = 512;
 
 // ---- forward -------------------------------------------------------------------
 
-constexpr int kTokensPerBlock = 4;
+// Bound by its reads and writes: all rows of a group's tokens are asked for
+// before the first is used.  32,768 tokens of 4,096 fp32 columns out of 131,072
+// rows as bf16: 4 tokens 78.6 us (5.9 TB/s), 1 95.9, 8 79.5; of bf16 rows 64.8,
+// 87.2, 72.8.
+constexpr int kTokens = 4;
 
-// A block copies one slab of columns of kTokensPerBlock tokens: all of its
-// loads are issued before its first store.
-template <typename T, typename O, bool VEC>
+template <typename T, typename O, bool VEC, int G>
 __global__ void __launch_bounds__(kRowThreads) embed_kernel(const EmbedArgs a) {
+  using Gr = Groups<G>;
   pdl_wait_then_release();
-  const size_t slabs = (a.dim + kSlab - 1) / kSlab;
-  const size_t t0 = blockIdx.x / slabs * kTokensPerBlock;
-  const size_t base = blockIdx.x % slabs * kSlab;
-  const int t = threadIdx.x;
-  if (!slab_live<VEC, kRowThreads>(base, t, a.dim)) return;
-  int64_t id[kTokensPerBlock];
+  const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
+  const size_t j = (size_t)blockIdx.x * Gr::kCount + threadIdx.x / G;
+  const size_t t0 = j / slabs * kTokens, base = j % slabs * Gr::kColumns;
+  const int t = threadIdx.x % G;
+  if (t0 >= a.tokens || !slab_live<VEC, G>(base, t, a.dim)) return;
+  int64_t id[kTokens];
 #pragma unroll
-  for (int i = 0; i < kTokensPerBlock; ++i)
+  for (int i = 0; i < kTokens; ++i)
     id[i] = t0 + i < a.tokens ? load_id(a.ids, a.ids64, t0 + i, a.vocab) : -1;
-  float v[kTokensPerBlock][8];
+  float v[kTokens][8];
 #pragma unroll
-  for (int i = 0; i < kTokensPerBlock; ++i) {
+  for (int i = 0; i < kTokens; ++i) {
     if (id[i] >= 0) {
-      load_slab<VEC, kRowThreads>(static_cast<const T*>(a.table) + (size_t)id[i] * a.ld_table, base,
-                                  t, a.dim, v[i]);
+      load_slab<VEC, G>(static_cast<const T*>(a.table) + (size_t)id[i] * a.ld_table, base, t, a.dim,
+                        v[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
     }
   }
 #pragma unroll
-  for (int i = 0; i < kTokensPerBlock; ++i) {
+  for (int i = 0; i < kTokens; ++i) {
     if (t0 + i >= a.tokens) break;
     if (id[i] >= 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] *= a.scale;
     }
-    store_slab<VEC, kRowThreads>(static_cast<O*>(a.out) + (t0 + i) * a.dim, base, t, a.dim, v[i]);
+    store_slab<VEC, G>(static_cast<O*>(a.out) + (t0 + i) * a.dim, base, t, a.dim, v[i]);
   }
+}
+
+template <typename T, typename O, bool VEC, int G>
+cudaError_t embed_by(const EmbedArgs& a, cudaStream_t stream) {
+  using Gr = Groups<G>;
+  const size_t slabs = (a.dim + Gr::kColumns - 1) / Gr::kColumns;
+  const size_t groups = (a.tokens + kTokens - 1) / kTokens * slabs;
+  return launch_kernel(embed_kernel<T, O, VEC, G>,
+                       dim3((unsigned)((groups + Gr::kCount - 1) / Gr::kCount)), dim3(kRowThreads),
+                       0, stream, a);
 }
 
 template <typename T, typename O>
 cudaError_t embed_of(const EmbedArgs& a, cudaStream_t stream) {
-  const size_t slabs = (a.dim + kSlab - 1) / kSlab;
-  const dim3 grid((unsigned)((a.tokens + kTokensPerBlock - 1) / kTokensPerBlock * slabs));
-  return a.vec ? launch_kernel(embed_kernel<T, O, true>, grid, dim3(kRowThreads), 0, stream, a)
-               : launch_kernel(embed_kernel<T, O, false>, grid, dim3(kRowThreads), 0, stream, a);
+  if (a.dim <= kWarpRow)
+    return a.vec ? embed_by<T, O, true, 32>(a, stream) : embed_by<T, O, false, 32>(a, stream);
+  return a.vec ? embed_by<T, O, true, kRowThreads>(a, stream)
+               : embed_by<T, O, false, kRowThreads>(a, stream);
 }
 
 // ---- the sort --------------------------------------------------------------------
 
-// One cluster sorts all tokens by least-significant digits.  Each warp owns a
-// contiguous piece of the list, so counting its digits, a prefix sum over
-// (digit, block, warp) and handing out places in the piece's order keeps the
-// sort stable.
-constexpr int kSortBlocks = 8;       // one cluster
+// One block or one cluster of blocks sorts all tokens by least-significant
+// digits.  Each warp owns a contiguous piece of the list, so counting its
+// digits, a prefix sum over (digit, block, warp) and handing out places in the
+// piece's order keeps the sort stable.
+constexpr int kSortBlocks = 8;       // of the cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kHold = 4;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr size_t kSortShared = (size_t)(kSortWarps * kDigits + 2 * kDigits) * sizeof(uint32_t);
@@ -94,6 +114,7 @@ struct GradPlan {
   float* part;            // [2 windows][dim]: sums of runs that cross windows
   int window;             // places of the sorted list in one window
   int passes, bits;       // digits, and bits of each
+  bool mark;              // `present` is wanted
 };
 
 // the list after its last digit
@@ -116,6 +137,17 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, int rank) {
   return v;
 }
 
+// every thread of the sort: its block's, or the cluster's
+template <int BLOCKS>
+__device__ __forceinline__ void sort_sync() {
+  if constexpr (BLOCKS > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+
+// HOLD: groups of 32 places of its piece that a warp holds in registers
+template <int BLOCKS, int HOLD>
 __global__ void __launch_bounds__(kSortThreads)
     sort_kernel(const void* ids, int ids64, uint32_t tokens, uint32_t vocab, const GradPlan p) {
   extern __shared__ uint32_t sm[];
@@ -128,11 +160,12 @@ __global__ void __launch_bounds__(kSortThreads)
   const int rank = blockIdx.x;  // the grid is one cluster
   const int gtid = rank * kSortThreads + tid;
 
-  for (uint32_t i = gtid; i < (vocab + 31) / 32; i += kSortBlocks * kSortThreads) p.present[i] = 0;
+  if (p.mark)
+    for (uint32_t i = gtid; i < (vocab + 31) / 32; i += BLOCKS * kSortThreads) p.present[i] = 0;
   if (gtid == 0) *p.count = 0;
 
   // this warp's piece of the list, a multiple of 32 places
-  const uint32_t pieces = kSortBlocks * kSortWarps;
+  const uint32_t pieces = BLOCKS * kSortWarps;
   const uint32_t piece = ((tokens + pieces - 1) / pieces + 31) / 32 * 32;
   const uint64_t from = (uint64_t)(rank * kSortWarps + warp) * piece;
   const uint32_t lo = from < tokens ? (uint32_t)from : tokens;
@@ -148,11 +181,11 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t* mine = counts + warp * kDigits;
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
-    // kHold groups of 32 places are read at once
-    uint32_t key[kHold], tok[kHold];
+    // HOLD groups of 32 places are read at once
+    uint32_t key[HOLD], tok[HOLD];
     auto read = [&](uint32_t i0) {
 #pragma unroll
-      for (int h = 0; h < kHold; ++h) {
+      for (int h = 0; h < HOLD; ++h) {
         const uint32_t i = i0 + h * 32 + lane;
         key[h] = vocab;
         tok[h] = i;
@@ -167,10 +200,10 @@ __global__ void __launch_bounds__(kSortThreads)
         }
       }
     };
-    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * kHold) {
+    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * HOLD) {
       read(i0);
 #pragma unroll
-      for (int h = 0; h < kHold; ++h)
+      for (int h = 0; h < HOLD; ++h)
         if (i0 + h * 32 + lane < hi) atomicAdd(&mine[(key[h] >> shift) & (digits - 1)], 1u);
     }
     __syncthreads();
@@ -196,17 +229,18 @@ __global__ void __launch_bounds__(kSortThreads)
         if (tid & 1) total[d] = run;
       }
     }
-    cluster_sync();
+    sort_sync<BLOCKS>();
     // places before this block's first of each digit: smaller digits of all
     // blocks, and the same digit of earlier blocks
     uint32_t before = 0, all = 0, upto = 0;
     if (tid < kDigits) {  // whole warps
       if (tid < digits) {
-        uint32_t c[kSortBlocks];
+        uint32_t c[BLOCKS];
 #pragma unroll
-        for (int b = 0; b < kSortBlocks; ++b) c[b] = peer_word(&total[tid], b);
+        for (int b = 0; b < BLOCKS; ++b)
+          c[b] = BLOCKS > 1 ? peer_word(&total[tid], b) : total[tid];
 #pragma unroll
-        for (int b = 0; b < kSortBlocks; ++b) {
+        for (int b = 0; b < BLOCKS; ++b) {
           before += b < rank ? c[b] : 0;
           all += c[b];
         }
@@ -227,10 +261,10 @@ __global__ void __launch_bounds__(kSortThreads)
       base[tid] = s;
     }
     __syncthreads();
-    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * kHold) {
-      if (piece > 32 * kHold) read(i0);  // a piece of up to kHold groups is still held
+    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * HOLD) {
+      if (piece > 32 * HOLD) read(i0);  // a piece of up to HOLD groups is still held
 #pragma unroll
-      for (int h = 0; h < kHold; ++h) {
+      for (int h = 0; h < HOLD; ++h) {
         if (i0 + h * 32 >= hi) break;
         const bool live = i0 + h * 32 + lane < hi;
         const uint32_t d = live ? (key[h] >> shift) & (digits - 1) : 0xFFFFFFFFu;
@@ -247,7 +281,7 @@ __global__ void __launch_bounds__(kSortThreads)
         }
       }
     }
-    cluster_sync();  // the list is whole, and no block still reads `total`
+    sort_sync<BLOCKS>();  // the list is whole, and no block still reads `total`
   }
 
   // items: runs of one key, cut where a window ends
@@ -260,7 +294,7 @@ __global__ void __launch_bounds__(kSortThreads)
       key = keys[i];
       const bool first = i == 0 || keys[i - 1] != key;
       starts = key < vocab && (first || i % p.window == 0);
-      if (key < vocab && first) atomicOr(&p.present[key / 32], 1u << (key % 32));
+      if (p.mark && key < vocab && first) atomicOr(&p.present[key / 32], 1u << (key % 32));
     }
     const uint32_t who = __ballot_sync(0xFFFFFFFFu, starts);
     uint32_t at = 0;
@@ -270,15 +304,52 @@ __global__ void __launch_bounds__(kSortThreads)
   }
 }
 
-// ---- the sums --------------------------------------------------------------------
+// Few tokens: a thread a token, whose place is the number of smaller
+// (id, token) pairs.
+constexpr int kFewTokens = 256;
+__global__ void __launch_bounds__(kFewTokens)
+    sort_few_kernel(const void* ids, int ids64, uint32_t tokens, uint32_t vocab, const GradPlan p) {
+  __shared__ __align__(16) uint32_t keys[kFewTokens];
+  __shared__ uint32_t sorted[kFewTokens];
+  __shared__ uint32_t count;
+  pdl_wait_then_release();
+  const uint32_t i = threadIdx.x;
+  if (p.mark)
+    for (uint32_t w = i; w < (vocab + 31) / 32; w += kFewTokens) p.present[w] = 0;
+  uint32_t key = 0xFFFFFFFFu;
+  if (i < tokens) {
+    const int64_t id = load_id(ids, ids64, i, vocab);
+    key = id < 0 ? vocab : (uint32_t)id;
+  }
+  keys[i] = key;
+  if (i == 0) count = 0;
+  __syncthreads();
+  uint32_t at = 0;
+  for (uint32_t j = 0; j < tokens; j += 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + j);  // past the tokens: the largest
+    at += (k.x < key || (k.x == key && j < i)) + (k.y < key || (k.y == key && j + 1 < i)) +
+          (k.z < key || (k.z == key && j + 2 < i)) + (k.w < key || (k.w == key && j + 3 < i));
+  }
+  uint32_t* list = p.passes & 1 ? p.keys[1] : p.keys[0];
+  uint32_t* order = p.passes & 1 ? p.order[1] : p.order[0];
+  if (i < tokens) {
+    sorted[at] = key;
+    list[at] = key;
+    order[at] = i;
+  }
+  __syncthreads();
+  if (i < tokens) {
+    key = sorted[i];
+    const bool first = i == 0 || sorted[i - 1] != key;
+    if (key < vocab && (first || i % p.window == 0))
+      p.items[atomicAdd(&count, 1u)] = make_uint2(i, key);
+    if (p.mark && key < vocab && first) atomicOr(&p.present[key / 32], 1u << (key % 32));
+  }
+  __syncthreads();
+  if (i == 0) *p.count = count;
+}
 
-// G threads take one slab of 8 G columns of a row or an item; a block has
-// kRowThreads / G such groups.
-template <int G>
-struct Groups {
-  static constexpr int kCount = kRowThreads / G;
-  static constexpr int kColumns = G * 8;
-};
+// ---- the sums --------------------------------------------------------------------
 
 // s += U rows of dout, whose tokens lanes j to j + U - 1 hold.  All rows are
 // asked for before the first is used: a thread whose columns do not exist
@@ -447,7 +518,10 @@ __global__ void __launch_bounds__(kRowThreads) join_kernel(const EmbedGradArgs a
 
 // A run of c tokens costs its window's length in one block, then c / window
 // rows in the join: windows grow with the list.
-int grad_window(size_t tokens) { return tokens <= 4096 ? 32 : tokens <= 65536 ? 64 : 256; }
+// Up to 128 tokens are one window, and nothing has to be joined.
+int grad_window(size_t tokens) {
+  return tokens <= 128 ? 128 : tokens <= 4096 ? 32 : tokens <= 65536 ? 64 : 256;
+}
 
 GradPlan grad_plan(void* ws, size_t tokens, size_t vocab, size_t dim, size_t* bytes) {
   GradPlan p = {};
@@ -495,11 +569,10 @@ cudaError_t sums_by(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t stre
   return e;
 }
 
-// A warp to a row up to 512 columns (in slabs of 256), else a whole block
 template <typename T, typename O>
 cudaError_t sums_of(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t stream,
                     uint64_t* launches) {
-  if (a.dim <= 512)
+  if (a.dim <= kWarpRow)
     return a.vec ? sums_by<T, O, true, 32>(a, p, stream, launches)
                  : sums_by<T, O, false, 32>(a, p, stream, launches);
   return a.vec ? sums_by<T, O, true, kRowThreads>(a, p, stream, launches)
@@ -525,12 +598,29 @@ size_t embedding_backward_workspace(size_t tokens, size_t vocab, size_t dim) {
 cudaError_t launch_embedding_backward(const EmbedGradArgs& a, cudaStream_t stream,
                                       uint64_t* launches) {
   size_t bytes = 0;
-  const GradPlan p = grad_plan(a.workspace, a.tokens, a.vocab, a.dim, &bytes);
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_shared(sort_kernel, (int)kSortShared, allowed);
-  if (e != cudaSuccess) return e;
-  e = launch_cluster(sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), kSortShared, kSortBlocks,
-                     stream, a.ids, a.ids64, (uint32_t)a.tokens, (uint32_t)a.vocab, p);
+  GradPlan p = grad_plan(a.workspace, a.tokens, a.vocab, a.dim, &bytes);
+  p.mark = !a.accumulate;
+  // Measured, the whole gradient (50,021 x 2,048, accumulating): 8 tokens 4.9 us
+  // by counting, 8.8 in one block; 256 tokens 10.2 and 13.2; 1,000 tokens 17.7
+  // in one block, 19.6 in a cluster; 4,000 tokens 29.6 and 25.2.
+  cudaError_t e;
+  const uint32_t tokens = (uint32_t)a.tokens, vocab = (uint32_t)a.vocab;
+  if (a.tokens <= (size_t)kFewTokens) {
+    e = launch_kernel(sort_few_kernel, dim3(1), dim3(kFewTokens), 0, stream, a.ids, a.ids64, tokens,
+                      vocab, p);
+  } else if (a.tokens <= (size_t)kSortThreads) {
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_shared(sort_kernel<1, 1>, (int)kSortShared, allowed);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(sort_kernel<1, 1>, dim3(1), dim3(kSortThreads), kSortShared, stream, a.ids,
+                      a.ids64, tokens, vocab, p);
+  } else {
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_shared(sort_kernel<kSortBlocks, 4>, (int)kSortShared, allowed);
+    if (e != cudaSuccess) return e;
+    e = launch_cluster(sort_kernel<kSortBlocks, 4>, dim3(kSortBlocks), dim3(kSortThreads),
+                       kSortShared, kSortBlocks, stream, a.ids, a.ids64, tokens, vocab, p);
+  }
   if (e != cudaSuccess) return e;
   *launches = 1;
   if (a.dout_type == RCC_F32)
