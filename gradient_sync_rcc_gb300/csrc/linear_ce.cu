@@ -208,7 +208,6 @@ __device__ __forceinline__ void tmem_add32(uint32_t at, float* v) {
 constexpr int kBM = 128;   // rows of C of one block
 constexpr int kBN = 256;   // columns of C of one block (of a pair: the same)
 constexpr int kBK = 64;    // of the sum per stage: 128 bytes, one swizzle row
-constexpr int kRowBytes = kBK * 2;
 constexpr int kEpiWarps = 8;  // two for each 32 rows, half of the columns each
 constexpr int kHalf = kBN / 2;
 constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
@@ -231,6 +230,7 @@ struct GemmArgs {
   int m_tiles, n_tiles;  // of kBM * CG rows, of bn columns
   int bn;                // columns of a tile, a multiple of 16 up to kBN
   int a_rows;            // rows of A's box (not MN), a multiple of 8 up to kBM
+  int stages, stage_size, a_bytes;  // in shared memory: how many, of what size, of it A's
   int k_blocks, splits;  // of bk; pieces of the sum, each with a C of its own
   int bk;                // of the sum per stage, a multiple of 16 up to kBK
   int chunk;             // k_blocks that one accumulator takes
@@ -271,15 +271,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t at, int bk) {
   return d;
 }
 
-template <int CG, int PARTS>
-struct Stage {
-  static constexpr int kBRows = kBN / CG;  // columns of C whose B this block holds
-  static constexpr int kABytes = kBM * kRowBytes;
-  static constexpr int kBBytes = kBRows * kRowBytes;
-  static constexpr int kBytes = PARTS * kABytes + kBBytes;
-  static constexpr int kCount = (200 * 1024) / kBytes;
-  static constexpr int kShared = kCount * kBytes + 1024 + 256;
-};
+// Stages in shared memory: as many as fit, each a box of A (PARTS of them) and
+// one of B on boundaries of 1,024 bytes.
+constexpr int kStageMemory = 200 * 1024, kMaxStages = 8;
+constexpr int kGemmShared = kStageMemory + 1024 + 256;
 
 struct Tile {
   int m, n, k0, k1, split;
@@ -462,15 +457,17 @@ __device__ __forceinline__ float common_factor(const GemmArgs& g, int thread, fl
 // finished accumulator out of tensor memory while the next one is summed.
 template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
-  using S = Stage<CG, PARTS>;
+  constexpr int kBRows = kBN / CG;  // columns of C whose B this block holds
   __shared__ float factor[kEpiWarps];
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t bars = base + S::kCount * S::kBytes;
-  const uint32_t full = bars, empty = bars + 8 * S::kCount;
-  const uint32_t acc_full = empty + 8 * S::kCount, acc_empty = acc_full + 16;
+  const uint32_t bars = base + kStageMemory;
+  const uint32_t full = bars, empty = bars + 8 * kMaxStages;
+  const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
   const uint32_t tmem_slot = acc_empty + 16;
-  static_assert(16 * S::kCount + 36 <= 256, "barriers");
+  static_assert(16 * kMaxStages + 36 <= 256, "barriers");
+  const int stages = g.stages;
+  const uint32_t a_bytes = g.a_bytes, stage_size = g.stage_size;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cta_rank() : 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
@@ -480,7 +477,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const int bk = A_MN && B_MN ? g.bk : kBK;
 
   if (tid == 0) {
-    for (int s = 0; s < S::kCount; ++s) {
+    for (int s = 0; s < stages; ++s) {
       bar_init(full + 8 * s, CG);
       bar_init(empty + 8 * s, 1);
     }
@@ -505,22 +502,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       // B's box has g.bn / CG rows.  A's may have less than kBM: the rows of
       // shared memory past it hold anything, and their sums are not used.
       const uint32_t stage_bytes = (PARTS * (A_MN ? kBM : g.a_rows) +
-                                    (B_MN ? S::kBRows : g.bn / CG)) * bk * 2;
+                                    (B_MN ? kBRows : g.bn / CG)) * bk * 2;
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
         const Tile tile = tile_of(g, t);
         const int m0 = (tile.m * CG + (int)rank) * kBM;
-        const int n0 = tile.n * g.bn + (int)rank * S::kBRows;
+        const int n0 = tile.n * g.bn + (int)rank * kBRows;
         for (int k = tile.k0; k < tile.k1; ++k) {
           if (!(ok = bar_wait(empty + 8 * s, phase ^ 1))) break;
-          const uint32_t at = base + s * S::kBytes;
+          const uint32_t at = base + s * stage_size;
           const uint32_t bar = CG == 2 ? peer_addr(full + 8 * s, 0) : full + 8 * s;
           bar_expect(bar, stage_bytes);
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            const uint32_t to = at + p * S::kABytes;
+            const uint32_t to = at + p * a_bytes;
             if constexpr (A_MN) {
 #pragma unroll
               for (int j = 0; j < kBM / 64; ++j)
@@ -529,15 +526,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
               tma_load<CG>(to, &g.a[p], k * kBK, m0, bar);
             }
           }
-          const uint32_t to = at + PARTS * S::kABytes;
+          const uint32_t to = at + PARTS * a_bytes;
           if constexpr (B_MN) {
 #pragma unroll
-            for (int j = 0; j < S::kBRows / 64; ++j)
+            for (int j = 0; j < kBRows / 64; ++j)
               tma_load<CG>(to + j * bk * 128, &g.b, n0 + 64 * j, g.b_row0 + k * bk, bar);
           } else {
             tma_load<CG>(to, &g.b, k * kBK, g.b_row0 + n0, bar);
           }
-          if (++s == S::kCount) {
+          if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
@@ -545,9 +542,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       }
       // Until the products have read them, the copies may still be in flight:
       // the last use of every stage is waited for, so no copy outlives the block.
-      for (int i = 0; i < S::kCount; ++i) {
+      for (int i = 0; i < stages; ++i) {
         bar_wait(empty + 8 * s, phase ^ 1);
-        if (++s == S::kCount) {
+        if (++s == stages) {
           s = 0;
           phase ^= 1;
         }
@@ -571,11 +568,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           for (int k = k0; k < k1; ++k) {
             if (!(ok = bar_wait(full + 8 * s, phase))) break;
             tmem_fence_after();
-            const uint32_t at = base + s * S::kBytes;
-            const uint64_t b = smem_desc<B_MN>(at + PARTS * S::kABytes, bk);
+            const uint32_t at = base + s * stage_size;
+            const uint64_t b = smem_desc<B_MN>(at + PARTS * a_bytes, bk);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
-              const uint64_t a = smem_desc<A_MN>(at + p * S::kABytes, bk);
+              const uint64_t a = smem_desc<A_MN>(at + p * a_bytes, bk);
 #pragma unroll
               for (int i = 0; i < kBK / 16; ++i) {
                 if (A_MN && B_MN && i * 16 >= bk) break;
@@ -585,7 +582,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
               }
             }
             mma_commit<CG>(empty + 8 * s);
-            if (++s == S::kCount) {
+            if (++s == stages) {
               s = 0;
               phase ^= 1;
             }
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 
 // ---- joins ---------------------------------------------------------------------------
 
-constexpr int kJoinRows = 32, kJoinParts = 32;
+constexpr int kJoinRows = 8, kJoinParts = 128;
 
 // (max, sum of exp) of two sets of scores; -inf: an empty set
 __device__ __forceinline__ float2 join_pair(float2 a, float2 b) {
@@ -663,12 +660,12 @@ __device__ __forceinline__ float2 join_pair(float2 a, float2 b) {
   return make_float2(m, a.y * exp2_fast((a.x - m) * kLog2e) + b.y * exp2_fast((b.x - m) * kLog2e));
 }
 
-// lse and loss of a row from its (max, sum) pairs: a thread takes every 32nd
-// pair of its row, eight loads under way; then a warp joins a row's 32 threads.
+// lse and loss of a row from its (max, sum) pairs: a thread takes every 128th
+// pair of its row, eight loads under way; then a warp joins a row's 128 threads.
 __global__ void __launch_bounds__(kJoinRows* kJoinParts)
     join_stats_kernel(const float2* part, int parts, const float* zlab, const void* labels,
                       int labels64, size_t tokens, size_t vocab, float* loss, float* lse) {
-  __shared__ float2 red[kJoinParts][kJoinRows + 1];
+  __shared__ float2 red[kJoinRows][kJoinParts + 1];
   pdl_wait_then_release();
   const int x = threadIdx.x % kJoinRows, y = threadIdx.x / kJoinRows;
   const size_t row = (size_t)blockIdx.x * kJoinRows + x;
@@ -687,20 +684,29 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts)
       all = join_pair(all, p[0]);
     }
   }
-  red[y][x] = all;
+  red[x][y] = all;
   __syncthreads();
-  all = red[x][y];  // lane x: thread x of row y
+  const int of = threadIdx.x / 32, lane = threadIdx.x % 32;  // warp `of`: row `of`
+  const size_t t = (size_t)blockIdx.x * kJoinRows + of;
+  if (of >= kJoinRows || t >= tokens) return;
+  float z = 0.f;
+  bool hit = false;
+  if (lane == 0) {
+    hit = load_id(labels, labels64, t, vocab) >= 0;
+    if (hit) z = zlab[t];
+  }
+  all = join_pair(join_pair(red[of][lane], red[of][lane + 32]),
+                  join_pair(red[of][lane + 64], red[of][lane + 96]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float2 b = make_float2(__shfl_xor_sync(0xFFFFFFFFu, all.x, o),
                                  __shfl_xor_sync(0xFFFFFFFFu, all.y, o));
-    all = x & o ? join_pair(b, all) : join_pair(all, b);  // the same order in both lanes
+    all = lane & o ? join_pair(b, all) : join_pair(all, b);  // the same order in both lanes
   }
-  const size_t t = (size_t)blockIdx.x * kJoinRows + y;
-  if (x == 0 && t < tokens) {
+  if (lane == 0) {
     const float l = all.x + logf(all.y);
     lse[t] = l;
-    loss[t] = load_id(labels, labels64, t, vocab) >= 0 ? l - zlab[t] : 0.f;
+    loss[t] = hit ? l - z : 0.f;
   }
 }
 
@@ -789,14 +795,19 @@ size_t ceil_div(size_t a, size_t b) { return (a + b - 1) / b; }
 
 template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_gemm_of(GemmArgs& g, cudaStream_t stream) {
-  using S = Stage<CG, PARTS>;
+  // a block's boxes: their bytes, and the copies' that a stage waits for
+  const int a_rows = A_MN ? kBM : g.a_rows, b_rows = B_MN ? kBN / CG : g.bn / CG;
+  const auto up = [](int n) { return (n + 1023) / 1024 * 1024; };
+  g.a_bytes = up(a_rows * g.bk * 2);
+  g.stage_size = PARTS * g.a_bytes + up(b_rows * g.bk * 2);
+  g.stages = std::min(kMaxStages, kStageMemory / g.stage_size);
   auto kernel = gemm_kernel<CG, PARTS, A_MN, B_MN, EPI>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_shared(kernel, S::kShared, allowed);
+  cudaError_t e = allow_shared(kernel, kGemmShared, allowed);
   if (e != cudaSuccess) return e;
   const int tiles = g.m_tiles * g.n_tiles * g.splits;
   const int units = std::min(tiles, sm_count() / CG);
-  return launch_cluster(kernel, dim3(units * CG), dim3(kGemmThreads), S::kShared, CG, stream, g);
+  return launch_cluster(kernel, dim3(units * CG), dim3(kGemmThreads), kGemmShared, CG, stream, g);
 }
 
 // Rows of A's box: those that exist, in whole swizzle atoms.  A box that is
@@ -843,7 +854,10 @@ int score_width(size_t tokens, size_t vocab) {
   return (int)(ceil_div(ceil_div(vocab, sms * turns), 16) * 16);
 }
 
-constexpr int kScoreGroup = 32, kGradGroup = 8;
+// Tiles of rows that share a run over the columns: what a turn of all SMs reads
+// of A and B stays in L2.  Scores of 8,192 x 131,072 x 4,096: 16 tiles 4.57 ms,
+// 8 4.86, 32 4.87; the gradients' products do not tell 4, 8 and 16 apart.
+constexpr int kScoreGroup = 16, kGradGroup = 8;
 
 // Rows of whole 32-byte sectors
 bool wide_rows(const void* c, size_t dim, size_t size) {
