@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "lm_common.cuh"
 #include "lm_internal.h"
@@ -650,38 +651,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 
 // ---- joins ---------------------------------------------------------------------------
 
-constexpr int kJoinRows = 8, kJoinParts = 128;
+constexpr int kJoinRows = 8;
 
-// (max, sum of exp) of two sets of scores; -inf: an empty set
+// (max, sum of exp) of two sets of scores; (-inf, 0): an empty set.  A NaN in
+// either sum stays.
 __device__ __forceinline__ float2 join_pair(float2 a, float2 b) {
-  if (b.x == -INFINITY) return a;
-  if (a.x == -INFINITY) return b;
-  const float m = fmaxf(a.x, b.x);
-  return make_float2(m, a.y * exp2_fast((a.x - m) * kLog2e) + b.y * exp2_fast((b.x - m) * kLog2e));
+  const float m = fmaxf(a.x, b.x), from = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * exp2_fast((a.x - from) * kLog2e) +
+                            b.y * exp2_fast((b.x - from) * kLog2e));
 }
 
-// lse and loss of a row from its (max, sum) pairs: a thread takes every 128th
-// pair of its row, eight loads under way; then a warp joins a row's 128 threads.
-__global__ void __launch_bounds__(kJoinRows* kJoinParts)
+// lse and loss of a row from its (max, sum) pairs: PARTS threads take them in
+// turn, eight loads under way; then a warp joins a row's threads.
+template <int PARTS>
+__global__ void __launch_bounds__(kJoinRows* PARTS)
     join_stats_kernel(const float2* part, int parts, const float* zlab, const void* labels,
                       int labels64, size_t tokens, size_t vocab, float* loss, float* lse) {
-  __shared__ float2 red[kJoinRows][kJoinParts + 1];
+  __shared__ float2 red[kJoinRows][PARTS + 1];
   pdl_wait_then_release();
   const int x = threadIdx.x % kJoinRows, y = threadIdx.x / kJoinRows;
   const size_t row = (size_t)blockIdx.x * kJoinRows + x;
   float2 all = make_float2(-INFINITY, 0.f);
   if (row < tokens) {
-    for (int j = y; j < parts; j += 8 * kJoinParts) {
+    for (int j = y; j < parts; j += 8 * PARTS) {
       float2 p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        p[i] = j + i * kJoinParts < parts ? part[(size_t)(j + i * kJoinParts) * tokens + row]
-                                          : make_float2(-INFINITY, 0.f);
+        p[i] = j + i * PARTS < parts ? part[(size_t)(j + i * PARTS) * tokens + row]
+                                     : make_float2(-INFINITY, 0.f);
+      float m = all.x;
 #pragma unroll
-      for (int o = 1; o < 8; o *= 2)
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, p[i].x);
+      const float from = m == -INFINITY ? 0.f : m;
+      float sum = all.y * exp2_fast((all.x - from) * kLog2e);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2 * o) p[i] = join_pair(p[i], p[i + o]);
-      all = join_pair(all, p[0]);
+      for (int i = 0; i < 8; ++i)
+        if (j + i * PARTS < parts) sum = fmaf(p[i].y, exp2_fast((p[i].x - from) * kLog2e), sum);
+      all = make_float2(m, sum);
     }
   }
   red[x][y] = all;
@@ -695,8 +701,9 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts)
     hit = load_id(labels, labels64, t, vocab) >= 0;
     if (hit) z = zlab[t];
   }
-  all = join_pair(join_pair(red[of][lane], red[of][lane + 32]),
-                  join_pair(red[of][lane + 64], red[of][lane + 96]));
+  all = red[of][lane];
+#pragma unroll
+  for (int i = 32; i < PARTS; i += 32) all = join_pair(all, red[of][lane + i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float2 b = make_float2(__shfl_xor_sync(0xFFFFFFFFu, all.x, o),
@@ -855,8 +862,9 @@ int score_width(size_t tokens, size_t vocab) {
 }
 
 // Tiles of rows that share a run over the columns: what a turn of all SMs reads
-// of A and B stays in L2.  Scores of 8,192 x 131,072 x 4,096: 16 tiles 4.57 ms,
-// 8 4.86, 32 4.87; the gradients' products do not tell 4, 8 and 16 apart.
+// of A and B stays in L2.  Scores of 8,192 x 131,072 x 4,096 under the power
+// limit: 16 tiles 4.86 to 4.92 ms, 12 4.98, 20 5.04, 32 5.21 to 5.24; the
+// gradients' products do not tell 4, 8 and 16 apart.
 constexpr int kScoreGroup = 16, kGradGroup = 8;
 
 // Rows of whole 32-byte sectors
@@ -932,9 +940,16 @@ cudaError_t launch_linear_ce_forward(const CeArgs& a, cudaStream_t stream, uint6
   cudaError_t e = launch_gemm<1, false, false, kEpiStats>(g, pair, a.tokens, a.vocab, a.dim, bn, 1,
                                                           kScoreGroup, stream);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(join_stats_kernel, dim3((unsigned)ceil_div(a.tokens, kJoinRows)),
-                    dim3(kJoinRows * kJoinParts), 0, stream, (const float2*)g.part, parts,
-                    (const float*)g.zlab, a.labels, a.labels64, a.tokens, a.vocab, a.loss, a.lse);
+  // few rows: more threads to each
+  const auto join = [&](auto threads) {
+    constexpr int kParts = decltype(threads)::value;
+    return launch_kernel(join_stats_kernel<kParts>, dim3((unsigned)ceil_div(a.tokens, kJoinRows)),
+                         dim3(kJoinRows * kParts), 0, stream, (const float2*)g.part, parts,
+                         (const float*)g.zlab, a.labels, a.labels64, a.tokens, a.vocab, a.loss,
+                         a.lse);
+  };
+  e = a.tokens <= 1024 ? join(std::integral_constant<int, 128>())
+                       : join(std::integral_constant<int, 32>());
   if (e == cudaSuccess) *launches = 2;
   return e;
 }
