@@ -9,14 +9,14 @@
 //   scores   x W^T, whose epilogue leaves one (max, sum) pair per row and
 //            256 vocabulary entries; a small kernel joins the pairs
 //   dz       x W^T again for a piece of the vocabulary, whose epilogue writes
-//            dz of the piece in bf16 (for fp32 gradients as the sum of two
-//            bf16 numbers, 2^-18 of its value off at most)
+//            dz of the piece in bf16 (for fp32 gradients as the sum of three
+//            bf16 numbers, which hold all of its 24 bits)
 //   dx       dz W, added up over the pieces
 //   dW       dz^T x, the piece's rows
 // Sums are fp32 in tensor memory, softmax statistics fp32.  The common factor F
 // stays out of dz: with one dloss for all tokens, as a mean has, its rounding
-// would put the same error on every label's term (3e-6 of an fp32 dW instead
-// of below 1e-6).
+// would put the same error on every label's term (bf16 gradients 0.0026 off 64
+// bits instead of 0.0020, of which the output's own rounding is 0.0017).
 #include <cuda.h>
 
 #include <algorithm>
@@ -219,14 +219,20 @@ constexpr int kTmemCols = 512;  // two accumulators of kBN columns
 // each, and the epilogue adds the accumulators up in registers, rounding to
 // nearest.  For the scores 32 (16 where a pass waits for W anyway): 64 left the
 // loss 1.3 times as far from 64 bits as plain fp32 sums, 32 half as far, and
-// 32 cost 2% of a long pass's time, 16 25%.  For fp32 gradients 64; a gradient
-// that is rounded to bf16 is taken whole.
-constexpr int kScoreMmas = 32, kScoreMmasFew = 16, kOutMmas = 64;
+// 32 cost 2% of a long pass's time, 16 25%.  For fp32 gradients 48: 96 left them
+// 1.2e-6 off 64 bits, 48 7e-7, 24 4.5e-7 for 3% of the time.  A gradient that is
+// rounded to bf16 is taken whole.
+constexpr int kScoreMmas = 32, kScoreMmasFew = 16, kOutMmas = 48;
+
+// bf16 numbers that make one fp32 value of dz: 24 bits, eight each.  2,048 x
+// 32,000 x 1,024: three leave dx and dW 7e-7 off 64 bits (plain fp32: 3.2e-6
+// and 8e-7) and take 578 us, two 2.1e-6 and 1.9e-6 and 424 us.
+constexpr int kMaxParts = 3;
 
 enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
 
 struct GemmArgs {
-  CUtensorMap a[2], b;   // a[1]: the second bf16 number of A's values
+  CUtensorMap a[kMaxParts], b;  // a[i]: the i-th bf16 number of A's values
   int m, n;              // of C
   int m_tiles, n_tiles;  // of kBM * CG rows, of bn columns
   int bn;                // columns of a tile, a multiple of 16 up to kBN
@@ -248,7 +254,7 @@ struct GemmArgs {
   int tokens;
   // dz
   const float* lse;
-  __nv_bfloat16* dz[2];  // [m][ld_dz], the second one NULL for bf16 gradients
+  __nv_bfloat16* dz[kMaxParts];  // [m][ld_dz], NULL past the parts
   size_t ld_dz;
   // out
   void* c;
@@ -353,14 +359,12 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
   const int64_t at = label - (g.b_row0 + col0);
   const float f = label >= 0 ? __fdiv_rn(g.dloss[row], scale) : 0.f;
   const float ll = g.lse[row] * kLog2e;
-  __nv_bfloat16* out = g.dz[0] + (size_t)row * g.ld_dz + col0;
-  __nv_bfloat16* rest = g.dz[1] ? g.dz[1] + (size_t)row * g.ld_dz + col0 : nullptr;
+  const size_t at_row = (size_t)row * g.ld_dz + col0;
 #pragma unroll
   for (int c = 0; c < kHalf; c += 16) {
     // ld_dz is a multiple of 256 and the piece begins on a boundary of 256, so
     // whole 32-byte vectors stay inside the row
     if (c >= left) break;
-    uint32_t w[8], u[8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float p = exp2_fast(fmaf(v[c + i], kLog2e, -ll));
@@ -369,14 +373,19 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
       v[c + i] = d;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
-      float lo, hi;
-      widen2(w[i], lo, hi);
-      u[i] = pack2(v[c + 2 * i] - lo, v[c + 2 * i + 1] - hi);
+    for (int part = 0; part < kMaxParts; ++part) {
+      if (!g.dz[part]) break;
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
+        float lo, hi;
+        widen2(w[i], lo, hi);
+        v[c + 2 * i] -= lo;  // exact
+        v[c + 2 * i + 1] -= hi;
+      }
+      store_words(g.dz[part] + at_row + c, w);
     }
-    store_words(out + c, w);
-    if (rest) store_words(rest + c, u);
   }
 }
 
@@ -885,7 +894,7 @@ constexpr size_t kDzBytes = (size_t)512 << 20;
 
 Pieces pieces_of(size_t tokens, size_t vocab, size_t dim, int grad_type) {
   Pieces p;
-  p.parts = grad_type == RCC_F32 ? 2 : 1;
+  p.parts = grad_type == RCC_F32 ? kMaxParts : 1;
   const size_t most = std::max<size_t>(kBN, kDzBytes / (tokens * 2 * p.parts) / kBN * kBN);
   p.count = ceil_div(vocab, most);
   p.width = ceil_div(ceil_div(vocab, p.count), kBN) * kBN;
@@ -970,9 +979,9 @@ GemmArgs grad_args(const CeArgs& a) {
 cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint64_t* launches) {
   const Pieces p = pieces_of(a.tokens, a.vocab, a.dim, a.grad_type);
   char* ws = static_cast<char*>(a.workspace);
-  __nv_bfloat16* dz[2] = {reinterpret_cast<__nv_bfloat16*>(ws),
-                          p.parts == 2 ? reinterpret_cast<__nv_bfloat16*>(ws + p.dz_bytes)
-                                       : nullptr};
+  __nv_bfloat16* dz[kMaxParts] = {};
+  for (int k = 0; k < p.parts; ++k)
+    dz[k] = reinterpret_cast<__nv_bfloat16*>(ws + k * p.dz_bytes);
   float* slices = p.dx_bytes ? reinterpret_cast<float*>(ws + p.parts * p.dz_bytes) : nullptr;
   const size_t grad_size = a.grad_type == RCC_F32 ? 4 : 2;
   const bool pair = paired(a.tokens);
@@ -983,8 +992,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       GemmArgs g = grad_args(a);
       g.b_row0 = (int)v0;
       g.lse = a.lse;
-      g.dz[0] = dz[0];
-      g.dz[1] = dz[1];
+      for (int k = 0; k < p.parts; ++k) g.dz[k] = dz[k];
       g.ld_dz = p.width;
       const int bn = score_width(a.tokens, width);
       if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, box_rows(a.tokens)) ||
@@ -1008,7 +1016,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, box_rows(a.tokens))) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBK)) return cudaErrorInvalidValue;
       const int splits = (int)std::min<size_t>(p.splits, ceil_div(width, kBK));
-      e = p.parts == 2 ? launch_gemm<2, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
+      e = p.parts > 1 ? launch_gemm<kMaxParts, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
                                                               kBN, splits, kGradGroup, stream)
                        : launch_gemm<1, false, true, kEpiOut>(g, pair, a.tokens, a.dim, width,
                                                               kBN, splits, kGradGroup, stream);
@@ -1026,7 +1034,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, stage_rows(a.tokens))) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, stage_rows(a.tokens))) return cudaErrorInvalidValue;
       const bool wide = paired(width);
-      e = p.parts == 2 ? launch_gemm<2, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, kBN, 1,
+      e = p.parts > 1 ? launch_gemm<kMaxParts, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, kBN, 1,
                                                              kGradGroup, stream)
                        : launch_gemm<1, true, true, kEpiOut>(g, wide, width, a.dim, a.tokens, kBN, 1,
                                                              kGradGroup, stream);

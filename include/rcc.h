@@ -493,8 +493,8 @@ rcc_status rcc_linear_ce_forward(const void* x, size_t ld_x, const void* w, size
  * dx and dw are of grad_type and 16-byte aligned; either may be NULL (not
  * wanted).  For RCC_BF16 gradients dz, relative to the largest |dloss|, is
  * rounded to bf16 for the tensor cores; for RCC_F32 it is carried as the sum
- * of two bf16 numbers (2^-18 of its value off at most), which costs twice the
- * products.  Sums are fp32.  The logits are formed
+ * of three bf16 numbers, which hold all of fp32's 24 bits and cost three times
+ * the products.  Sums are fp32.  The logits are formed
  * again, a piece of the vocabulary at a time; the workspace holds one
  * piece's dz (512 MiB at most, and a piece is at least 256 entries). */
 rcc_status rcc_linear_ce_backward(const void* x, size_t ld_x, const void* w, size_t ld_w,

@@ -307,7 +307,7 @@ def ce_64(x, w, labels, dloss):
     edz = f.abs() * (p * (ez + elz[:, None] + (8 + 4 * far)[:, None] * U) + 2 * U * (p - one).abs())
     out = {"z": z, "lse": lse, "loss": loss, "dx": dz @ w, "dw": dz.t() @ x}
     bound = {"lse": elz, "loss": eloss}
-    for kind, step in ((F32, 2.0 ** -16), (BF16, 2.0 ** -8)):
+    for kind, step in ((F32, 2.0 ** -23), (BF16, 2.0 ** -8)):
         e = edz * (1 + step) + step * dz.abs()
         for name, left, err, right, n in (("dx", dz, e, w, vocab),
                                           ("dw", dz.t(), e.t(), x, x.shape[0])):
