@@ -233,6 +233,8 @@ enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
 
 struct GemmArgs {
   CUtensorMap a[kMaxParts], b;  // a[i]: the i-th bf16 number of A's values
+  CUtensorMap c[kMaxParts];     // C in boxes of 32 rows of 128 bytes, or dz's parts
+  int copy_out;                 // C (dz) goes out by TMA, through c
   int m, n;              // of C
   int m_tiles, n_tiles;  // of kBM * CG rows, of bn columns
   int bn;                // columns of a tile, a multiple of 16 up to kBN
@@ -257,7 +259,7 @@ struct GemmArgs {
   __nv_bfloat16* dz[kMaxParts];  // [m][ld_dz], NULL past the parts
   size_t ld_dz;
   // out
-  void* c;
+  void* out;
   size_t ld_c, split_stride;  // elements
   int c_type;
   int add;               // C += instead of C =
@@ -280,8 +282,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t at, int bk) {
 
 // Stages in shared memory: as many as fit, each a box of A (PARTS of them) and
 // one of B on boundaries of 1,024 bytes.
-constexpr int kStageMemory = 200 * 1024, kMaxStages = 8;
-constexpr int kGemmShared = kStageMemory + 1024 + 256;
+constexpr int kStageMemory = 192 * 1024, kMaxStages = 24;
+// After them the barriers, and for each warp of the epilogue 32 rows of 128
+// bytes on their way to global memory.
+constexpr int kBarBytes = 1024, kOutBytes = 32 * 128;
+constexpr int kGemmShared = 1024 + kStageMemory + kBarBytes + kEpiWarps * kOutBytes;
 
 struct Tile {
   int m, n, k0, k1, split;
@@ -351,40 +356,79 @@ __device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHa
   *part = failed ? make_float2(nan, nan) : make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
+// One box of 32 rows of 128 bytes on its way out.  Lane r holds row r as eight
+// words of 16 bytes, which lie swizzled as TMA expects them, so that no two of
+// a quarter warp share a bank.
+__device__ __forceinline__ void out_begin(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();  // the box before has been read
+}
+__device__ __forceinline__ void out_put(uint32_t at, int lane, int i, uint32_t a, uint32_t b,
+                                        uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                   at + lane * 128 + ((i ^ (lane & 7)) << 4)), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void out_send(uint32_t at, int lane, const CUtensorMap* map, int x,
+                                         int y) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+        "r"(at), "r"(x), "r"(y) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
 // dz of half a row; columns past the piece are not written.
 __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf], int row,
-                                            int col0, int left, float scale, bool failed) {
-  if (row >= g.m || left <= 0) return;
-  const int64_t label = load_id(g.labels, g.labels64, row, g.vocab);
+                                            int col0, int left, float scale, bool failed,
+                                            uint32_t box) {
+  const int lane = threadIdx.x & 31, first = row - lane;
+  if (first >= g.m || left <= 0) return;  // the whole warp
+  const bool live = row < g.m;
+  const int64_t label = live ? load_id(g.labels, g.labels64, row, g.vocab) : -1;
   const int64_t at = label - (g.b_row0 + col0);
   const float f = label >= 0 ? __fdiv_rn(g.dloss[row], scale) : 0.f;
-  const float ll = g.lse[row] * kLog2e;
+  const float ll = live ? g.lse[row] * kLog2e : 0.f;
   const size_t at_row = (size_t)row * g.ld_dz + col0;
+  const bool copy = g.copy_out && first + 32 <= g.m;
 #pragma unroll
-  for (int c = 0; c < kHalf; c += 16) {
-    // ld_dz is a multiple of 256 and the piece begins on a boundary of 256, so
-    // whole 32-byte vectors stay inside the row
-    if (c >= left) break;
+  for (int c0 = 0; c0 < kHalf; c0 += 64) {
+    if (c0 >= left) break;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p = exp2_fast(fmaf(v[c + i], kLog2e, -ll));
-      float d = label < 0 ? 0.f : f * (c + i == at ? p - 1.f : p);
-      if (failed) d = __uint_as_float(0x7FC00000u);
-      v[c + i] = d;
+    for (int i = c0; i < c0 + 64; ++i) {
+      const float p = exp2_fast(fmaf(v[i], kLog2e, -ll));
+      v[i] = label < 0 ? 0.f : f * (i == at ? p - 1.f : p);
+      if (failed) v[i] = __uint_as_float(0x7FC00000u);
     }
 #pragma unroll
     for (int part = 0; part < kMaxParts; ++part) {
       if (!g.dz[part]) break;
-      uint32_t w[8];
+      if (copy) out_begin(lane);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
-        float lo, hi;
-        widen2(w[i], lo, hi);
-        v[c + 2 * i] -= lo;  // exact
-        v[c + 2 * i + 1] -= hi;
+      for (int c = c0; c < c0 + 64; c += 16) {
+        // ld_dz is a multiple of 256 and a tile begins on a boundary of 16, so
+        // whole 32-byte vectors stay inside the tile and the row
+        if (!copy && c >= left) break;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[i] = pack2(v[c + 2 * i], v[c + 2 * i + 1]);
+          float lo, hi;
+          widen2(w[i], lo, hi);
+          v[c + 2 * i] -= lo;  // exact
+          v[c + 2 * i + 1] -= hi;
+        }
+        if (copy) {
+          out_put(box, lane, (c - c0) / 8, w[0], w[1], w[2], w[3]);
+          out_put(box, lane, (c - c0) / 8 + 1, w[4], w[5], w[6], w[7]);
+        } else if (live) {
+          store_words(g.dz[part] + at_row + c, w);
+        }
       }
-      store_words(g.dz[part] + at_row + c, w);
+      if (copy) out_send(box, lane, &g.c[part], col0 + c0, first);
     }
   }
 }
@@ -393,10 +437,36 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
 template <typename T>
 __device__ __forceinline__ void epilogue_out(const GemmArgs& g, float (&v)[kHalf], int row,
                                              int col0, int left, int split, float scale,
-                                             bool failed) {
-  if (row >= g.m) return;
+                                             bool failed, uint32_t box) {
   constexpr int kE = 16 / (int)sizeof(T);  // elements of 16 bytes
-  T* out = static_cast<T*>(g.c) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
+  const int lane = threadIdx.x & 31, first = row - lane;
+  if (g.copy_out && first + 32 <= g.m) {
+    // a slice's rows follow those of the slice before
+    const int y = split * g.m + first;
+#pragma unroll
+    for (int c0 = 0; c0 < kHalf; c0 += 8 * kE) {
+      if (c0 >= left) break;
+      out_begin(lane);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = c0 + i * kE + e * (kE / 4);
+          if constexpr (kE == 4)
+            w[e] = __float_as_uint(v[at] * scale);
+          else
+            w[e] = pack2(v[at] * scale, v[at + 1] * scale);
+          if (failed) w[e] = kE == 4 ? 0x7FC00000u : 0x7FC07FC0u;
+        }
+        out_put(box, lane, i, w[0], w[1], w[2], w[3]);
+      }
+      out_send(box, lane, &g.c[0], col0 + c0, y);
+    }
+    return;
+  }
+  if (row >= g.m) return;
+  T* out = static_cast<T*>(g.out) + (size_t)split * g.split_stride + (size_t)row * g.ld_c + col0;
 #pragma unroll
   for (int c = 0; c < kHalf; c += 2 * kE) {
     if (c >= left) break;  // left is a multiple of 8, and of 16 where wide
@@ -475,7 +545,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const uint32_t full = bars, empty = bars + 8 * kMaxStages;
   const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
   const uint32_t tmem_slot = acc_empty + 16;
-  static_assert(16 * kMaxStages + 36 <= 256, "barriers");
+  static_assert(16 * kMaxStages + 36 <= kBarBytes, "barriers");
   const int stages = g.stages;
   const uint32_t a_bytes = g.a_bytes, stage_size = g.stage_size;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -605,6 +675,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   } else if (warp >= 4) {
     const int quarter = warp & 3;  // the 32 rows of tensor memory this warp may read
     const int half = (warp - 4) >> 2;
+    const uint32_t box = bars + kBarBytes + (warp - 4) * kOutBytes;
     float scale = 1.f;
     if constexpr (EPI != kEpiStats) scale = common_factor(g, tid - 128, factor);
     int buf = 0;
@@ -640,15 +711,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       if constexpr (EPI == kEpiStats) {
         epilogue_stats(g, v, row, col0, left, 2 * tile.n + half, !ok);
       } else if constexpr (EPI == kEpiDz) {
-        epilogue_dz(g, v, row, col0, left, scale, !ok);
+        epilogue_dz(g, v, row, col0, left, scale, !ok, box);
       } else {
         if (g.c_type == RCC_F32)
-          epilogue_out<float>(g, v, row, col0, left, tile.split, scale, !ok);
+          epilogue_out<float>(g, v, row, col0, left, tile.split, scale, !ok, box);
         else
-          epilogue_out<__nv_bfloat16>(g, v, row, col0, left, tile.split, scale, !ok);
+          epilogue_out<__nv_bfloat16>(g, v, row, col0, left, tile.split, scale, !ok, box);
       }
       __syncwarp();
     }
+    if (EPI != kEpiStats && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   tmem_fence_before();
@@ -794,16 +866,18 @@ EncodeFn encode_fn() {
   return f;
 }
 
-// A bf16 matrix of `rows` rows of `cols`, read in boxes of 64 columns (128
-// bytes, swizzled) and `box_rows` rows; what lies outside reads as zero.
-bool make_map(CUtensorMap* map, const void* p, size_t cols, size_t rows, size_t ld, int box_rows) {
+// A matrix of `rows` rows of `cols` elements of `size` bytes in boxes of 128
+// bytes (swizzled) by `box_rows`; what lies outside reads as zero and is not
+// written.
+bool make_map(CUtensorMap* map, const void* p, size_t cols, size_t rows, size_t ld, int box_rows,
+              size_t size = 2) {
   const EncodeFn encode = encode_fn();
   if (!encode) return false;
-  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows}, step[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
-                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return encode(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -993,6 +1067,9 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.b_row0 = (int)v0;
       g.lse = a.lse;
       for (int k = 0; k < p.parts; ++k) g.dz[k] = dz[k];
+      g.copy_out = pair;  // tiles of whole boxes
+      for (int k = 0; k < p.parts && pair; ++k)
+        if (!make_map(&g.c[k], dz[k], width, a.tokens, p.width, 32)) return cudaErrorInvalidValue;
       g.ld_dz = p.width;
       const int bn = score_width(a.tokens, width);
       if (!make_map(&g.a[0], a.x, a.dim, a.tokens, a.ld_x, box_rows(a.tokens)) ||
@@ -1006,12 +1083,16 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
     if (a.dx) {  // dx (+)= dz W
       GemmArgs g = grad_args(a);
       g.b_row0 = (int)v0;
-      g.c = slices ? slices : a.dx;
+      g.out = slices ? slices : a.dx;
       g.c_type = slices ? RCC_F32 : a.grad_type;
       g.ld_c = a.dim;
       g.split_stride = a.tokens * a.dim;
       g.add = i > 0;
-      g.wide = wide_rows(g.c, a.dim, slices ? 4 : grad_size);
+      g.wide = wide_rows(g.out, a.dim, slices ? 4 : grad_size);
+      g.copy_out = !g.add;
+      if (g.copy_out && !make_map(&g.c[0], g.out, a.dim, a.tokens * (slices ? p.splits : 1), a.dim,
+                                  32, slices ? 4 : grad_size))
+        return cudaErrorInvalidValue;
       for (int k = 0; k < p.parts; ++k)
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, box_rows(a.tokens))) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.w, a.dim, a.vocab, a.ld_w, kBK)) return cudaErrorInvalidValue;
@@ -1025,11 +1106,14 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
     }
     if (a.dw) {  // the piece's rows of dW (+)= dz^T x
       GemmArgs g = grad_args(a);
-      g.c = static_cast<char*>(a.dw) + v0 * a.dim * grad_size;
+      g.out = static_cast<char*>(a.dw) + v0 * a.dim * grad_size;
       g.c_type = a.grad_type;
       g.ld_c = a.dim;
       g.add = a.accumulate;
-      g.wide = wide_rows(g.c, a.dim, grad_size);
+      g.wide = wide_rows(g.out, a.dim, grad_size);
+      g.copy_out = !g.add;
+      if (g.copy_out && !make_map(&g.c[0], g.out, a.dim, width, a.dim, 32, grad_size))
+        return cudaErrorInvalidValue;
       for (int k = 0; k < p.parts; ++k)
         if (!make_map(&g.a[k], dz[k], width, a.tokens, p.width, stage_rows(a.tokens))) return cudaErrorInvalidValue;
       if (!make_map(&g.b, a.x, a.dim, a.tokens, a.ld_x, stage_rows(a.tokens))) return cudaErrorInvalidValue;
