@@ -535,7 +535,7 @@ __device__ __forceinline__ float common_factor(const GemmArgs& g, int thread, fl
 // (CG = 2) per tile, every block or pair taking tiles in turn.  Warp 0 fills
 // the stages by TMA, warp 1 issues the products, the last warps take the
 // finished accumulator out of tensor memory while the next one is summed.
-template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
+template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI, bool WHOLE>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
   constexpr int kBRows = kBN / CG;  // columns of C whose B this block holds
   __shared__ float factor[kEpiWarps];
@@ -546,15 +546,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
   const uint32_t tmem_slot = acc_empty + 16;
   static_assert(16 * kMaxStages + 36 <= kBarBytes, "barriers");
-  const int stages = g.stages;
-  const uint32_t a_bytes = g.a_bytes, stage_size = g.stage_size;
+  // Whole boxes have sizes known here, which is worth 5% of a long pass to the
+  // threads that fill the stages and issue the products.
+  constexpr uint32_t kWholeA = kBM * kBK * 2, kWholeStage = PARTS * kWholeA + kBRows * kBK * 2;
+  const int stages = WHOLE ? (int)(kStageMemory / kWholeStage) : g.stages;
+  const uint32_t a_bytes = WHOLE ? kWholeA : g.a_bytes;
+  const uint32_t stage_size = WHOLE ? kWholeStage : g.stage_size;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cta_rank() : 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
   const int tiles = g.m_tiles * g.n_tiles * g.splits;
   // A short sum of both MN major takes stages of less than kBK: rows that do
   // not exist are not copied as zeros.
-  const int bk = A_MN && B_MN ? g.bk : kBK;
+  const int bk = WHOLE || !(A_MN && B_MN) ? kBK : g.bk;
 
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -581,8 +585,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       asm volatile("fence.proxy.async;" ::: "memory");
       // B's box has g.bn / CG rows.  A's may have less than kBM: the rows of
       // shared memory past it hold anything, and their sums are not used.
-      const uint32_t stage_bytes = (PARTS * (A_MN ? kBM : g.a_rows) +
-                                    (B_MN ? kBRows : g.bn / CG)) * bk * 2;
+      const uint32_t stage_bytes =
+          WHOLE ? kWholeStage : (PARTS * (A_MN ? kBM : g.a_rows) +
+                                 (B_MN ? kBRows : g.bn / CG)) * bk * 2;
+      const uint32_t full0 = CG == 2 ? peer_addr(full, 0) : full;
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         for (int k = tile.k0; k < tile.k1; ++k) {
           if (!(ok = bar_wait(empty + 8 * s, phase ^ 1))) break;
           const uint32_t at = base + s * stage_size;
-          const uint32_t bar = CG == 2 ? peer_addr(full + 8 * s, 0) : full + 8 * s;
+          const uint32_t bar = full0 + 8 * s;
           bar_expect(bar, stage_bytes);
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
@@ -635,6 +641,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
                              ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(g.bn / 8) << 17) |
                              ((uint32_t)(kBM * CG / 16) << 24);
+      // descriptors of stage 0; those of stage s are stage_size s / 16 more
+      uint64_t desc_a[PARTS];
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) desc_a[p] = smem_desc<A_MN>(base + p * a_bytes, bk);
+      const uint64_t desc_b = smem_desc<B_MN>(base + PARTS * a_bytes, bk);
       int s = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -648,14 +659,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           for (int k = k0; k < k1; ++k) {
             if (!(ok = bar_wait(full + 8 * s, phase))) break;
             tmem_fence_after();
-            const uint32_t at = base + s * stage_size;
-            const uint64_t b = smem_desc<B_MN>(at + PARTS * a_bytes, bk);
+            const uint32_t at = s * (stage_size >> 4);
+            const uint64_t b = desc_b + at;
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
-              const uint64_t a = smem_desc<A_MN>(at + p * a_bytes, bk);
+              const uint64_t a = desc_a[p] + at;
 #pragma unroll
               for (int i = 0; i < kBK / 16; ++i) {
-                if (A_MN && B_MN && i * 16 >= bk) break;
+                if (!WHOLE && A_MN && B_MN && i * 16 >= bk) break;
                 // 16 of the sum: 32 bytes along a row, or 16 rows of 128 bytes
                 mma<CG>(d, a + i * ((A_MN ? 2048 : 32) >> 4), b + i * ((B_MN ? 2048 : 32) >> 4),
                         idesc, k > k0 || p > 0 || i > 0);
@@ -883,15 +894,15 @@ bool make_map(CUtensorMap* map, const void* p, size_t cols, size_t rows, size_t 
 
 size_t ceil_div(size_t a, size_t b) { return (a + b - 1) / b; }
 
-template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI>
+template <int CG, int PARTS, bool A_MN, bool B_MN, int EPI, bool WHOLE>
 cudaError_t launch_gemm_of(GemmArgs& g, cudaStream_t stream) {
-  // a block's boxes: their bytes, and the copies' that a stage waits for
+  // a block's boxes, on boundaries of 1,024 bytes
   const int a_rows = A_MN ? kBM : g.a_rows, b_rows = B_MN ? kBN / CG : g.bn / CG;
   const auto up = [](int n) { return (n + 1023) / 1024 * 1024; };
   g.a_bytes = up(a_rows * g.bk * 2);
   g.stage_size = PARTS * g.a_bytes + up(b_rows * g.bk * 2);
   g.stages = std::min(kMaxStages, kStageMemory / g.stage_size);
-  auto kernel = gemm_kernel<CG, PARTS, A_MN, B_MN, EPI>;
+  auto kernel = gemm_kernel<CG, PARTS, A_MN, B_MN, EPI, WHOLE>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_shared(kernel, kGemmShared, allowed);
   if (e != cudaSuccess) return e;
@@ -927,8 +938,12 @@ cudaError_t launch_gemm(GemmArgs& g, bool pair, size_t m, size_t n, size_t k, in
   g.group = group;
   const int mmas = EPI == kEpiOut ? kOutMmas : pair ? kScoreMmas : kScoreMmasFew;
   g.chunk = EPI == kEpiOut && g.c_type == RCC_BF16 ? g.k_blocks : mmas / (PARTS * (kBK / 16));
-  return pair ? launch_gemm_of<2, PARTS, A_MN, B_MN, EPI>(g, stream)
-              : launch_gemm_of<1, PARTS, A_MN, B_MN, EPI>(g, stream);
+  // whole boxes: of a pair, unless the sum is short; what one block does alone
+  // is bound by memory
+  if (!pair) return launch_gemm_of<1, PARTS, A_MN, B_MN, EPI, false>(g, stream);
+  if constexpr (A_MN && B_MN)
+    if (g.bk < kBK) return launch_gemm_of<2, PARTS, A_MN, B_MN, EPI, false>(g, stream);
+  return launch_gemm_of<2, PARTS, A_MN, B_MN, EPI, true>(g, stream);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
