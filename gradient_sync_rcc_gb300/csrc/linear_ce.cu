@@ -217,12 +217,12 @@ constexpr int kTmemCols = 512;  // two accumulators of kBN columns
 // of rounding it, a loss that grows with their number (3.7e-5 of dx after
 // 4,000 of them).  So an accumulator takes a few instructions of 16 products
 // each, and the epilogue adds the accumulators up in registers, rounding to
-// nearest.  For the scores 32 (16 where a pass waits for W anyway): 64 left the
-// loss 1.3 times as far from 64 bits as plain fp32 sums, 32 half as far, and
-// 32 cost 2% of a long pass's time, 16 25%.  For fp32 gradients 48: 96 left them
-// 1.2e-6 off 64 bits, 48 7e-7, 24 4.5e-7 for 3% of the time.  A gradient that is
-// rounded to bf16 is taken whole.
-constexpr int kScoreMmas = 32, kScoreMmasFew = 16, kOutMmas = 48;
+// nearest.  Scores of 2,000 x 50,021 x 2,048, the loss's distance from 64 bits
+// (plain fp32 sums 6.5e-7): 64 instructions 8.4e-7 and 233 us, 48 5.5e-7 and
+// 238, 32 3.8e-7 and 243, 16 1.9e-7 and 290; where a pass waits for W anyway,
+// 16.  For fp32 gradients (2,048 x 32,000 x 1,024): 96 1.2e-6, 48 7e-7, 24
+// 4.5e-7 for 3% of the time.  A gradient that is rounded to bf16 is taken whole.
+constexpr int kScoreMmas = 48, kScoreMmasFew = 16, kOutMmas = 48;
 
 // bf16 numbers that make one fp32 value of dz: 24 bits, eight each.  2,048 x
 // 32,000 x 1,024: three leave dx and dW 7e-7 off 64 bits (plain fp32: 3.2e-6
