@@ -234,7 +234,7 @@ enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
 struct GemmArgs {
   CUtensorMap a[kMaxParts], b;  // a[i]: the i-th bf16 number of A's values
   CUtensorMap c[kMaxParts];     // C in boxes of 32 rows of 128 bytes, or dz's parts
-  int copy_out;                 // C (dz) goes out by TMA, through c
+  int copy_out;                 // C goes out by TMA, through c
   int m, n;              // of C
   int m_tiles, n_tiles;  // of kBM * CG rows, of bn columns
   int bn;                // columns of a tile, a multiple of 16 up to kBN
@@ -381,24 +381,28 @@ __device__ __forceinline__ void out_send(uint32_t at, int lane, const CUtensorMa
   }
 }
 
-// dz of half a row; columns past the piece are not written.
+// dz of half a row, WIDTH columns at a time; columns past the piece are not
+// written.  COPY: through `box` and TMA, which needs 32 rows that exist and
+// whole boxes of 64 columns; else 32-byte vectors.
+template <bool COPY>
 __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf], int row,
                                             int col0, int left, float scale, bool failed,
                                             uint32_t box) {
-  const int lane = threadIdx.x & 31, first = row - lane;
-  if (first >= g.m || left <= 0) return;  // the whole warp
-  const bool live = row < g.m;
-  const int64_t label = live ? load_id(g.labels, g.labels64, row, g.vocab) : -1;
+  constexpr int kWidth = COPY ? 64 : 16;
+  if (row >= g.m || left <= 0) return;  // COPY: of none or all of the warp
+  const int lane = threadIdx.x & 31;
+  const int64_t label = load_id(g.labels, g.labels64, row, g.vocab);
   const int64_t at = label - (g.b_row0 + col0);
   const float f = label >= 0 ? __fdiv_rn(g.dloss[row], scale) : 0.f;
-  const float ll = live ? g.lse[row] * kLog2e : 0.f;
+  const float ll = g.lse[row] * kLog2e;
   const size_t at_row = (size_t)row * g.ld_dz + col0;
-  const bool copy = g.copy_out && first + 32 <= g.m;
 #pragma unroll
-  for (int c0 = 0; c0 < kHalf; c0 += 64) {
+  for (int c0 = 0; c0 < kHalf; c0 += kWidth) {
+    // ld_dz is a multiple of 256 and a tile begins on a boundary of 16, so
+    // whole 32-byte vectors stay inside the tile and the row
     if (c0 >= left) break;
 #pragma unroll
-    for (int i = c0; i < c0 + 64; ++i) {
+    for (int i = c0; i < c0 + kWidth; ++i) {
       const float p = exp2_fast(fmaf(v[i], kLog2e, -ll));
       v[i] = label < 0 ? 0.f : f * (i == at ? p - 1.f : p);
       if (failed) v[i] = __uint_as_float(0x7FC00000u);
@@ -406,12 +410,9 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
 #pragma unroll
     for (int part = 0; part < kMaxParts; ++part) {
       if (!g.dz[part]) break;
-      if (copy) out_begin(lane);
+      if constexpr (COPY) out_begin(lane);
 #pragma unroll
-      for (int c = c0; c < c0 + 64; c += 16) {
-        // ld_dz is a multiple of 256 and a tile begins on a boundary of 16, so
-        // whole 32-byte vectors stay inside the tile and the row
-        if (!copy && c >= left) break;
+      for (int c = c0; c < c0 + kWidth; c += 16) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -421,14 +422,14 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
           v[c + 2 * i] -= lo;  // exact
           v[c + 2 * i + 1] -= hi;
         }
-        if (copy) {
+        if constexpr (COPY) {
           out_put(box, lane, (c - c0) / 8, w[0], w[1], w[2], w[3]);
           out_put(box, lane, (c - c0) / 8 + 1, w[4], w[5], w[6], w[7]);
-        } else if (live) {
+        } else {
           store_words(g.dz[part] + at_row + c, w);
         }
       }
-      if (copy) out_send(box, lane, &g.c[part], col0 + c0, first);
+      if constexpr (COPY) out_send(box, lane, &g.c[part], col0 + c0, row - lane);
     }
   }
 }
@@ -722,7 +723,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       if constexpr (EPI == kEpiStats) {
         epilogue_stats(g, v, row, col0, left, 2 * tile.n + half, !ok);
       } else if constexpr (EPI == kEpiDz) {
-        epilogue_dz(g, v, row, col0, left, scale, !ok, box);
+        if (CG == 2 && row - lane + 32 <= g.m)
+          epilogue_dz<CG == 2>(g, v, row, col0, left, scale, !ok, box);
+        else
+          epilogue_dz<false>(g, v, row, col0, left, scale, !ok, box);
       } else {
         if (g.c_type == RCC_F32)
           epilogue_out<float>(g, v, row, col0, left, tile.split, scale, !ok, box);
@@ -1082,8 +1086,7 @@ cudaError_t launch_linear_ce_backward(const CeArgs& a, cudaStream_t stream, uint
       g.b_row0 = (int)v0;
       g.lse = a.lse;
       for (int k = 0; k < p.parts; ++k) g.dz[k] = dz[k];
-      g.copy_out = pair;  // tiles of whole boxes
-      for (int k = 0; k < p.parts && pair; ++k)
+      for (int k = 0; k < p.parts && pair; ++k)  // tiles of whole boxes
         if (!make_map(&g.c[k], dz[k], width, a.tokens, p.width, 32)) return cudaErrorInvalidValue;
       g.ld_dz = p.width;
       const int bn = score_width(a.tokens, width);
