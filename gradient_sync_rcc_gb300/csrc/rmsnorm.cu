@@ -208,17 +208,21 @@ __device__ __forceinline__ void copies_wait() {  // all but the newest N groups
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Measured at 16,384 rows of 4,096 bf16 (fp32) columns, where 6.78 TB/s would
-// take 50 (89) us each way:
-//   forward   rows copied ahead, twice the blocks that fit    54.6 (97.6) us
-//             three rows ahead, as many blocks as fit         63.3 (106)
-//             nothing copied ahead, a block a row             66.6 (91.6)
-//   backward  768 threads an SM, 3 rows held                  67.4 (125)
-//             2 rows held                                     66.4 (136)
-//             1,024 threads, 2 rows held                      77.6 (139)
-//             512 threads, 3 rows held                        96 (125)
-//             nothing copied ahead, 1,024 threads             131 (169)
-constexpr int kForeThreads = 2048, kForeStages = 2;
+// Threads of all blocks of one SM (those waiting to start included) and rows
+// held in shared memory.  Measured at 16,384 rows of 4,096 bf16 (fp32) columns,
+// where 6.78 TB/s would take 50 (89) us each way:
+//   forward   2,048 threads, 2 rows held              54.2 (98.9) us
+//             1,024 threads, 2 rows held              58.3 (105)
+//             1,024 threads, 3 rows held              62.6 (106)
+//             4,096 threads, nothing copied ahead     63.2 (92.4)
+//             1,024 threads, nothing copied ahead     63.5 (93.4)
+//   backward  768 threads, 3 rows held                66.1 (119)
+//             768 threads, 2 rows held                65.5 (122)
+//             512 threads, 3 rows held                65.1 (119)
+//             1,024 threads, 2 rows held              82.3 (122)
+// So the forward pass copies rows of 2-byte types ahead; an fp32 row is as many
+// loads in flight by itself.
+constexpr int kForeThreads = 2048, kForeStages = 2, kForeDirect = 4096;
 constexpr int kBackThreads = 768, kBackStages = 3;
 constexpr int kSharedMost = 220 * 1024;   // of all blocks of one SM
 
@@ -236,9 +240,9 @@ struct NormFore {
   static constexpr int kParts = NV * 8 / Part<T, VEC>::kE;
   static constexpr int kStage = kThreads * kParts * 16;
   static constexpr int kFit = kSharedMost / kStage;
-  static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kForeStages ? kFit : kForeStages) : 0;
+  static constexpr int kStages = VEC && sizeof(T) == 2 && kFit >= kForeStages ? kForeStages : 0;
   static constexpr int kShared = kStages * kStage;
-  static constexpr int kPerSm = blocks_per_sm(kForeThreads, kThreads, kShared);
+  static constexpr int kPerSm = blocks_per_sm(kStages ? kForeThreads : kForeDirect, kThreads, kShared);
 };
 
 // One row for each group of G threads at a time; a thread keeps its part of

@@ -364,6 +364,27 @@ def test_linear_ce(tokens, vocab, dim, extra):
         within(added, want["dw"] + 1.0, bound["dw", kind] + 2 * U + half_ulp(want["dw"] + 1, kind))
 
 
+def test_linear_ce_vocabulary_in_pieces():
+    """More dz than the workspace holds at a time; outputs 16 bytes into a sector."""
+    tokens, vocab, dim = 1810, 150100, 72
+    x, w, labels, dloss = ce_inputs(16, tokens, vocab, dim)
+    want, bound = ce_64(x, w, labels, dloss)
+    loss, lse = rcc.linear_ce_forward(x, w, labels)
+    within(lse, want["lse"], bound["lse"])
+    within(loss, want["loss"], bound["loss"])
+    for kind, bytes_each in ((BF16, 2), (F32, 6)):
+        assert rcc.linear_ce_workspace(tokens, vocab, dim, True, kind) < tokens * vocab * bytes_each
+        pad = 16 // torch.empty(0, dtype=kind).element_size()
+        dx = torch.empty(tokens * dim + pad, dtype=kind, device=DEV)[pad:].view(tokens, dim)
+        dw = torch.empty(vocab * dim + pad, dtype=kind, device=DEV)[pad:].view(vocab, dim)
+        rcc.linear_ce_backward(x, w, labels, lse, dloss, dx=dx, dw=dw)
+        within(dx, want["dx"], bound["dx", kind])
+        within(dw, want["dw"], bound["dw", kind])
+        dw.fill_(1.0)
+        rcc.linear_ce_backward(x, w, labels, lse, dloss, dw=dw, need_dx=False, accumulate=True)
+        within(dw, want["dw"] + 1.0, bound["dw", kind] + 2 * U + half_ulp(want["dw"] + 1, kind))
+
+
 def test_linear_ce_gradient_against_differences():
     """Central differences of the loss in 64 bits."""
     x, w, labels, dloss = ce_inputs(9, 40, 300, 64)
