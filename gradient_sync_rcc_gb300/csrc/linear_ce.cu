@@ -226,7 +226,7 @@ constexpr int kScoreMmas = 48, kScoreMmasFew = 16, kOutMmas = 48;
 
 // bf16 numbers that make one fp32 value of dz: 24 bits, eight each.  2,048 x
 // 32,000 x 1,024: three leave dx and dW 7e-7 off 64 bits (plain fp32: 3.2e-6
-// and 8e-7) and take 578 us, two 2.1e-6 and 1.9e-6 and 424 us.
+// and 8e-7) and take 560 us, two 2.1e-6 and 1.9e-6 and 421 us.
 constexpr int kMaxParts = 3;
 
 enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };

@@ -3,6 +3,7 @@ successor table over several ranks, its tied gradient is the sum of both ends',
 and a non-finite gradient skips the step."""
 import importlib.util
 import os
+import re
 
 import pytest
 import torch
@@ -72,3 +73,18 @@ def test_an_infinite_weight_skips_the_step(example):
         rcc.finish(comm)
     assert report.skipped == 1 and report.nonfinite > 0 and state.step == 0
     assert state.scale == 512.0 and torch.equal(model.table, before)
+
+
+def test_the_documented_calls_run():
+    """The front page's example of the operators, as written."""
+    text = open(os.path.join(ROOT, "README.md")).read()
+    block = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "linear_ce" in b]
+    assert len(block) == 1
+    scope = {}
+    exec(compile(block[0], "README.md", "exec"), scope)
+    assert scope["dtable"].dtype == scope["dnorm"].dtype == torch.float32
+    assert all(torch.isfinite(scope[n]).all() for n in ("loss", "dtable", "dnorm"))
+    # 1,024 products of fp32: 2,048 roundings of 2^-24 of sum |y w|, near 20
+    z = scope["y"].double() @ scope["w16"].double().t()
+    want = torch.logsumexp(z, 1) - z.gather(1, scope["labels"][:, None])[:, 0]
+    assert float((scope["loss"] - want).abs().max()) < 2.5e-3
