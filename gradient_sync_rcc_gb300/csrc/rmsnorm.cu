@@ -216,14 +216,18 @@ __device__ __forceinline__ void copies_wait() {  // all but the newest N groups
 //             1,024 threads, 3 rows held              62.6 (106)
 //             4,096 threads, nothing copied ahead     63.2 (92.4)
 //             1,024 threads, nothing copied ahead     63.5 (93.4)
-//   backward  768 threads, 3 rows held                66.1 (119)
-//             768 threads, 2 rows held                65.5 (122)
-//             512 threads, 3 rows held                65.1 (119)
-//             1,024 threads, 2 rows held              82.3 (122)
+//   backward  512 threads, 3 rows held                61.4 (97.7)
+//             512 threads, 4 rows held                62.2 (96.0)
+//             768 threads, 3 rows held                62.3 (96.9)
+//             768 threads, 2 rows held                62.1 (99.7)
+//             1,024 threads, 2 rows held              73.1 (99.6)
+// and of 2,048 bf16 columns backward 35.2 with 512 threads, 36.4 with 768.  Of
+// 4,095 columns, not copied ahead: 512 threads 137 (198), 768 108 (154), 1,024
+// 111 (152).
 // So the forward pass copies rows of 2-byte types ahead; an fp32 row is as many
 // loads in flight by itself.
 constexpr int kForeThreads = 2048, kForeStages = 2, kForeDirect = 4096;
-constexpr int kBackThreads = 768, kBackStages = 3;
+constexpr int kBackThreads = 512, kBackStages = 3, kBackDirect = 768;
 constexpr int kSharedMost = 220 * 1024;   // of all blocks of one SM
 
 // blocks of `threads` that one SM takes, of `shared` bytes each, for `all` threads
@@ -233,7 +237,8 @@ constexpr int blocks_per_sm(int all, int threads, int shared) {
 }
 
 // Rows copied ahead into shared memory (aligned rows, VEC).  A thread writes
-// and reads its own parts alone, so the copies need no barrier.
+// and reads its own parts alone, so the copies need no barrier; a group's scale
+// is one lane's copy, for the lanes of its warp.
 template <typename T, int G, int NV, bool VEC>
 struct NormFore {
   static constexpr int kThreads = kBlock<G>;
@@ -376,13 +381,14 @@ template <typename T, int G, int NV, bool VEC>
 struct NormBack {
   static constexpr int kThreads = kBlock<G>;
   static constexpr int kParts = NV * 8 / Part<T, VEC>::kE;
-  static constexpr int kStage = kThreads * kParts * (16 + Part<T, VEC>::kE + 4);
+  static constexpr int kScaled = kThreads / Part<T, VEC>::kLanes;  // groups of one part
+  static constexpr int kStage = kThreads * kParts * (16 + Part<T, VEC>::kE) + kParts * kScaled * 4;
   static constexpr bool kHoldWeight = kThreads * NV * 32 + 2 * kStage <= kSharedMost;
   static constexpr int kWeight = kHoldWeight ? kThreads * NV * 32 : 0;
   static constexpr int kFit = (kSharedMost - kWeight) / kStage;
   static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kBackStages ? kFit : kBackStages) : 0;
   static constexpr int kShared = kWeight + kStages * kStage;
-  static constexpr int kPerSm = blocks_per_sm(kBackThreads, kThreads, kShared);
+  static constexpr int kPerSm = blocks_per_sm(kStages ? kBackThreads : kBackDirect, kThreads, kShared);
 };
 
 // Rows are dealt to the blocks in turn; a thread keeps the weight gradient of
@@ -428,7 +434,8 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC>::kPerSm)
   };
   auto scale_at = [&](int s, int p) {
     return reinterpret_cast<float*>(smem + B::kWeight + s * B::kStage +
-                                    kThreads * kParts * (16 + P::kE)) + p * kThreads + tid;
+                                    kThreads * kParts * (16 + P::kE)) +
+           p * B::kScaled + tid / P::kLanes;
   };
   auto weight = [&](int p, float2 (&w)[P::kPairs]) {
     if constexpr (B::kHoldWeight) {
@@ -455,7 +462,8 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC>::kPerSm)
         if (left > p * kSpan) {
           copy_async<16>(dy_at(s, p), dy + p * kSpan);
           copy_async<P::kE>(q_at(s, p), kept + p * kSpan);
-          copy_async<4>(scale_at(s, p), scales + p * (kSpan / (int)kKeepGroup));
+          if (t % P::kLanes == 0)
+            copy_async<4>(scale_at(s, p), scales + p * (kSpan / (int)kKeepGroup));
         }
       }
     }
@@ -483,6 +491,7 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC>::kPerSm)
     if constexpr (kStages > 0) {
       copy_row(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
+      __syncwarp();  // a group's scale is one lane's copy
     }
     // kept over the reduction: dy w, and dy and the bytes as they came
     uint4 raw[kParts];
@@ -681,7 +690,7 @@ cudaError_t launch_rmsnorm_forward(const NormArgs& a, cudaStream_t stream) {
 size_t rmsnorm_backward_workspace(size_t tokens, size_t dim) {
   const NormShape s = norm_shape(dim);
   const size_t ld = (dim + kKeepGroup - 1) / kKeepGroup * kKeepGroup;
-  const int most = std::max(1, kBackThreads / norm_threads(s));
+  const int most = std::max(1, std::max(kBackThreads, kBackDirect) / norm_threads(s));
   return norm_blocks(tokens, s, most) * norm_rows_per_block(s) * ld * sizeof(float);
 }
 
