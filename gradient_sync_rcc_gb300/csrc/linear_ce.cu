@@ -220,7 +220,8 @@ constexpr int kTmemCols = 512;  // two accumulators of kBN columns
 // nearest.  Scores of 2,000 x 50,021 x 2,048, the loss's distance from 64 bits
 // (plain fp32 sums 6.5e-7): 64 instructions 8.4e-7 and 233 us, 48 5.5e-7 and
 // 238, 32 3.8e-7 and 243, 16 1.9e-7 and 290; where a pass waits for W anyway,
-// 16: 100 x 50,021 x 1,024 1.9e-7 (plain 4.2e-7) and 21.6 us, 8 1.0e-7 and 23.7.  For fp32 gradients (2,048 x 32,000 x 1,024): 96 1.2e-6, 48 7e-7, 24
+// 16: 100 x 50,021 x 1,024 1.9e-7 (plain 4.2e-7) and 21.6 us, 8 1.0e-7 and
+// 23.7.  For fp32 gradients (2,048 x 32,000 x 1,024): 96 1.2e-6, 48 7e-7, 24
 // 4.5e-7 for 3% of the time.  A gradient that is rounded to bf16 is taken whole.
 constexpr int kScoreMmas = 48, kScoreMmasFew = 16, kOutMmas = 48;
 
