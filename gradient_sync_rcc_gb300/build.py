@@ -90,7 +90,7 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
         procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     binding = None
     if lib == LIB:
-        binding = BINDING + ".tmp%d" % os.getpid()
+        binding = os.path.join(objdir, "_lm.%d.so" % os.getpid())
         procs.append(("lm_binding", subprocess.Popen(
             binding_command(binding), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
