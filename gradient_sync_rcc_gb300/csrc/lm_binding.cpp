@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -135,19 +136,34 @@ Workspace workspace(PyObject* o, size_t need, at::Device dev) {
   return {t, t.data_ptr(), (size_t)t.nbytes()};
 }
 
-// The caller's stream (an address or an object with cuda_stream), or the
-// current one.  The last check of a call: nothing before it needs a GPU.
-rcc_stream_t stream_of(PyObject* o, at::Device dev) {
-  if (!dev.is_cuda()) refuse("the operators take tensors on a CUDA device");
-  if (!given(o))
-    return reinterpret_cast<rcc_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
-  PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
-  if (!v) throw python_error();
-  void* p = PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) throw python_error();
-  return static_cast<rcc_stream_t>(p);
-}
+// The stream of a call: the caller's (an address or an object with
+// cuda_stream), or the current one.  The last check of a call: nothing before
+// it needs a GPU.  While this lives the stream is the current one, so what a
+// call allocates belongs to it: a block comes without work of another stream
+// still queued on it, and a released workspace is given out again on this
+// stream alone, behind the kernels that still use it.
+class Stream {
+ public:
+  Stream(PyObject* o, at::Device dev) {
+    if (!dev.is_cuda()) refuse("the operators take tensors on a CUDA device");
+    handle_ = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    if (!given(o)) return;
+    PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+    if (!v) throw python_error();
+    auto asked = static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
+    Py_DECREF(v);
+    if (PyErr_Occurred()) throw python_error();
+    if (asked == cudaStreamLegacy) asked = nullptr;  // two names of the default stream
+    if (asked == handle_) return;
+    handle_ = asked;
+    current_.reset_stream(c10::cuda::getStreamFromExternal(asked, dev.index()));
+  }
+  rcc_stream_t handle() const { return reinterpret_cast<rcc_stream_t>(handle_); }
+
+ private:
+  cudaStream_t handle_;
+  c10::cuda::OptionalCUDAStreamGuard current_;
+};
 
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
@@ -220,11 +236,11 @@ PyObject* embedding_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = (float)number(a[2]);
     at::Tensor out;
     if (given(a[3])) out = output(a[3], "out", {tokens, m.cols}, scalar_of(out_kind), dev);
-    const rcc_stream_t stream = stream_of(a[5], dev);
+    const Stream stream(a[5], dev);
     if (!out.defined()) out = fresh({tokens, m.cols}, scalar_of(out_kind), dev);
     call(rcc_.embedding_forward, table.data_ptr(), kind, (size_t)m.ld, ids.data_ptr(), index,
          (size_t)tokens, (size_t)m.rows, (size_t)m.cols, scale, out.data_ptr(), out_kind,
-         stream);
+         stream.handle());
     return wrap(std::move(out));
   });
 }
@@ -245,12 +261,12 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const rcc_dtype kind = dtype_of(dout, "dout"), grad = dtype_of(dtable, "dtable");
     const float scale = (float)number(a[3]);
     const int accumulate = truth(a[4]);
-    const rcc_stream_t stream = stream_of(a[6], dev);
+    const Stream stream(a[6], dev);
     const Workspace ws =
         workspace(a[5], rcc_.embedding_backward_workspace(m.rows, vocab, m.cols), dev);
     call(rcc_.embedding_backward, dout.data_ptr(), kind, (size_t)m.ld, ids.data_ptr(), index,
          (size_t)m.rows, vocab, (size_t)m.cols, scale, dtable.data_ptr(), grad, accumulate, ws.p,
-         ws.bytes, stream);
+         ws.bytes, stream.handle());
     return Py_NewRef(a[2]);
   });
 }
@@ -289,13 +305,13 @@ PyObject* rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float eps = (float)number(a[2]);
     at::Tensor data;
     if (given(a[3]) && a[3] != Py_True) data = kept_arg(a[3], a[4], a[5], m.rows, m.cols, dev);
-    const rcc_stream_t stream = stream_of(a[7], dev);
+    const Stream stream(a[7], dev);
     at::Tensor y = output(a[6], "out", {m.rows, m.cols}, x.scalar_type(), dev);
     if (a[3] == Py_True)
       data = fresh({m.rows * groups_of(m.cols) * (kGroup + 4)}, at::kByte, dev);
     const Kept k = data.defined() ? kept_in(data, m.rows, m.cols) : Kept{nullptr, nullptr};
     call(rcc_.rmsnorm_forward, x.data_ptr(), kind, (size_t)m.ld, w, eps, (size_t)m.rows,
-         (size_t)m.cols, y.data_ptr(), k.values, k.scales, stream);
+         (size_t)m.cols, y.data_ptr(), k.values, k.scales, stream.handle());
     return a[3] == Py_True ? wrap(std::move(y), std::move(data)) : wrap(std::move(y));
   });
 }
@@ -313,13 +329,13 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float eps = (float)number(a[5]);
     const int accumulate = truth(a[8]);
     if (accumulate && !given(a[7])) refuse("accumulate needs the dweight to add to");
-    const rcc_stream_t stream = stream_of(a[10], dev);
+    const Stream stream(a[10], dev);
     at::Tensor dx = output(a[6], "dx", {m.rows, m.cols}, dy.scalar_type(), dev);
     at::Tensor dweight = output(a[7], "dweight", {m.cols}, at::kFloat, dev);
     const Workspace ws = workspace(a[9], rcc_.rmsnorm_backward_workspace(m.rows, m.cols), dev);
     call(rcc_.rmsnorm_backward, dy.data_ptr(), kind, (size_t)m.ld, k.values, k.scales, w, eps,
          (size_t)m.rows, (size_t)m.cols, dx.data_ptr(), static_cast<float*>(dweight.data_ptr()),
-         accumulate, ws.p, ws.bytes, stream);
+         accumulate, ws.p, ws.bytes, stream.handle());
     return wrap(std::move(dx), std::move(dweight));
   });
 }
@@ -347,7 +363,7 @@ Scores scores(PyObject* px, PyObject* pw, PyObject* pl) {
 PyObject* linear_ce_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry("linear_ce_forward", n, 7, [&] {
     const Scores s = scores(a[0], a[1], a[2]);
-    const rcc_stream_t stream = stream_of(a[6], s.dev);
+    const Stream stream(a[6], s.dev);
     at::Tensor loss = output(a[3], "loss", {s.mx.rows}, at::kFloat, s.dev);
     at::Tensor lse = output(a[4], "lse", {s.mx.rows}, at::kFloat, s.dev);
     const Workspace ws = workspace(
@@ -355,7 +371,7 @@ PyObject* linear_ce_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call(rcc_.linear_ce_forward, s.x.data_ptr(), (size_t)s.mx.ld, s.w.data_ptr(),
          (size_t)s.mw.ld, s.labels.data_ptr(), s.index, (size_t)s.mx.rows, (size_t)s.mw.rows,
          (size_t)s.mx.cols, static_cast<float*>(loss.data_ptr()),
-         static_cast<float*>(lse.data_ptr()), ws.p, ws.bytes, stream);
+         static_cast<float*>(lse.data_ptr()), ws.p, ws.bytes, stream.handle());
     return wrap(std::move(loss), std::move(lse));
   });
 }
@@ -379,7 +395,7 @@ PyObject* linear_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dx = output(a[6], "dx", {s.mx.rows, s.mx.cols}, scalar_of(grad), s.dev);
     if (need_dw && given(a[7]))
       dw = output(a[7], "dw", {s.mw.rows, s.mx.cols}, scalar_of(grad), s.dev);
-    const rcc_stream_t stream = stream_of(a[12], s.dev);
+    const Stream stream(a[12], s.dev);
     if (need_dx && !dx.defined()) dx = fresh({s.mx.rows, s.mx.cols}, scalar_of(grad), s.dev);
     if (need_dw && !dw.defined()) dw = fresh({s.mw.rows, s.mx.cols}, scalar_of(grad), s.dev);
     const Workspace ws = workspace(
@@ -387,7 +403,7 @@ PyObject* linear_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call(rcc_.linear_ce_backward, s.x.data_ptr(), (size_t)s.mx.ld, s.w.data_ptr(),
          (size_t)s.mw.ld, s.labels.data_ptr(), s.index, lse, dloss, (size_t)s.mx.rows,
          (size_t)s.mw.rows, (size_t)s.mx.cols, dx.defined() ? dx.data_ptr() : nullptr,
-         dw.defined() ? dw.data_ptr() : nullptr, grad, accumulate, ws.p, ws.bytes, stream);
+         dw.defined() ? dw.data_ptr() : nullptr, grad, accumulate, ws.p, ws.bytes, stream.handle());
     return wrap(std::move(dx), std::move(dw));
   });
 }

@@ -6,8 +6,9 @@ like the rest of the binding.
 The work of a call -- checks of what the C entry points cannot see (a type, a
 device, a shape that does not fit: ValueError), outputs and workspaces that
 the caller left out, the C call itself -- is done by the compiled module _lm.
-New tensors are allocated on the inputs' device, to be used on `stream` (the
-current one by default); tensors passed in must be safe to use there.
+New tensors are allocated on the inputs' device for `stream` (the current one
+by default), as under torch.cuda.stream; tensors passed in must be safe to use
+there.
 """
 import ctypes as C
 
