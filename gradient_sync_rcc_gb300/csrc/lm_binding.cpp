@@ -276,6 +276,8 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 constexpr int64_t kGroup = 128;
 int64_t groups_of(int64_t dim) { return (dim + kGroup - 1) / kGroup; }
 
+int64_t kept_bytes(int64_t tokens, int64_t dim) { return tokens * groups_of(dim) * (kGroup + 4); }
+
 // The 8-bit form: values, then scales, in one buffer of bytes
 struct Kept {
   int8_t* values;
@@ -289,8 +291,13 @@ Kept kept_in(const at::Tensor& data, int64_t tokens, int64_t dim) {
 const at::Tensor& kept_arg(PyObject* data, PyObject* tokens, PyObject* dim, int64_t rows,
                            int64_t cols, at::Device dev) {
   const at::Tensor& t = tensor(data, "kept");
-  if (PyLong_AsLongLong(tokens) != rows || PyLong_AsLongLong(dim) != cols || t.device() != dev)
+  const long long n = PyLong_AsLongLong(tokens), d = PyErr_Occurred() ? -1 : PyLong_AsLongLong(dim);
+  if (PyErr_Occurred()) throw python_error();
+  if (n != rows || d != cols || t.device() != dev)
     refuse("kept must hold %lld x %lld on the inputs' device", (long long)rows, (long long)cols);
+  const int64_t need = kept_bytes(rows, cols);
+  if (t.scalar_type() != at::kByte || !t.is_contiguous() || t.numel() < need)
+    refuse("kept's buffer must be %lld contiguous bytes (uint8)", (long long)need);
   return t;
 }
 
@@ -308,7 +315,7 @@ PyObject* rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Stream stream(a[7], dev);
     at::Tensor y = output(a[6], "out", {m.rows, m.cols}, x.scalar_type(), dev);
     if (a[3] == Py_True)
-      data = fresh({m.rows * groups_of(m.cols) * (kGroup + 4)}, at::kByte, dev);
+      data = fresh({kept_bytes(m.rows, m.cols)}, at::kByte, dev);
     const Kept k = data.defined() ? kept_in(data, m.rows, m.cols) : Kept{nullptr, nullptr};
     call(rcc_.rmsnorm_forward, x.data_ptr(), kind, (size_t)m.ld, w, eps, (size_t)m.rows,
          (size_t)m.cols, y.data_ptr(), k.values, k.scales, stream.handle());

@@ -77,7 +77,8 @@ class Kept:
     @property
     def scales(self):
         at = self.tokens * self.groups * KEEP_GROUP
-        return self.data[at:].view(torch.float32).view(self.tokens, self.groups)
+        n = self.tokens * self.groups * 4
+        return self.data[at:at + n].view(torch.float32).view(self.tokens, self.groups)
 
     def dequantize(self):
         """What it stands for, [tokens, dim] float32."""
