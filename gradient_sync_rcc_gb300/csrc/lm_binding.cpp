@@ -136,6 +136,13 @@ Workspace workspace(PyObject* o, size_t need, at::Device dev) {
   return {t, t.data_ptr(), (size_t)t.nbytes()};
 }
 
+// librcc launches on the current device, whose default stream goes by the same
+// handle as any other's
+void require_current(int device, int current) {
+  if (device != current)
+    refuse("current CUDA device %d is not the inputs' device %d", current, device);
+}
+
 // The stream of a call: the caller's (an address or an object with
 // cuda_stream), or the current one.  The last check of a call: nothing before
 // it needs a GPU.  While this lives the stream is the current one, so what a
@@ -146,6 +153,7 @@ class Stream {
  public:
   Stream(PyObject* o, at::Device dev) {
     if (!dev.is_cuda()) refuse("the operators take tensors on a CUDA device");
+    require_current(dev.index(), c10::cuda::current_device());
     handle_ = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     if (!given(o)) return;
     PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
@@ -435,9 +443,21 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// device, current device: ValueError unless they are the same
+PyObject* check_device(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("check_device", n, 2, [&] {
+    const long device = PyLong_AsLong(a[0]);
+    const long current = PyErr_Occurred() ? -1 : PyLong_AsLong(a[1]);
+    if (PyErr_Occurred()) throw python_error();
+    require_current((int)device, (int)current);
+    return Py_NewRef(Py_None);
+  });
+}
+
 #define RCC_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
 PyMethodDef methods[] = {
     {"bind", RCC_FAST(bind), "Takes the error callback and librcc's entry points."},
+    {"check_device", RCC_FAST(check_device), nullptr},
     {"embedding_forward", RCC_FAST(embedding_forward), nullptr},
     {"embedding_backward", RCC_FAST(embedding_backward), nullptr},
     {"rmsnorm_forward", RCC_FAST(rmsnorm_forward), nullptr},

@@ -8,7 +8,7 @@ device, a shape that does not fit: ValueError), outputs and workspaces that
 the caller left out, the C call itself -- is done by the compiled module _lm.
 New tensors are allocated on the inputs' device for `stream` (the current one
 by default), as under torch.cuda.stream; tensors passed in must be safe to use
-there.
+there.  The inputs' device must be the current one.
 """
 import ctypes as C
 

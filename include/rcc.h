@@ -417,6 +417,8 @@ rcc_status rcc_grad_stats_noalloc(const float* const* grads, int num_ranks,
  *     synchronisation, so they can be captured into a CUDA graph.  Scratch is
  *     the caller's: at least rcc_*_workspace bytes, 256-byte aligned, not used
  *     by anything else until the call's work is done, its contents arbitrary.
+ *   - The device that holds the buffers and `stream` must be the current one;
+ *     workspace sizes are the current device's.
  *   - Matrices are row major.  Inputs may have rows `ld_*` elements apart
  *     (ld >= the row's length, at most 2^30); outputs are contiguous.
  *     Outputs and scratch must not overlap each other or an input.

@@ -50,3 +50,16 @@ def test_a_kept_input_that_fits_is_not_refused(L):
         with pytest.raises(ValueError, match="CUDA device"):   # the last check
             L.rmsnorm_backward(x, kept, weight)
         assert kept.values.shape == (TOKENS, 256) and kept.scales.shape == (TOKENS, 2)
+
+
+def test_a_device_that_is_not_current_is_refused(L):
+    """What every call decides between its tensors' device and the current one."""
+    from gradient_sync_rcc_gb300 import _lm
+    for same in (0, 1, 7):
+        assert _lm.check_device(same, same) is None
+    for device, current in ((1, 0), (0, 1), (3, 2)):
+        with pytest.raises(ValueError, match="device %d is not the inputs' device %d"
+                           % (current, device)):
+            _lm.check_device(device, current)
+    with pytest.raises(TypeError):
+        _lm.check_device("0", 0)
