@@ -350,7 +350,8 @@ __device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHa
 #pragma unroll
   for (int i = 4; i < kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
   const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  const float ml = m * kLog2e;
+  // where no score is above -inf every exponential is 0, not exp(-inf + inf)
+  const float ml = (m == -INFINITY ? 0.f : m) * kLog2e;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kHalf; ++i) sum[i & 3] += exp2_fast(fmaf(v[i], kLog2e, -ml));
