@@ -350,12 +350,19 @@ __device__ __forceinline__ void epilogue_stats(const GemmArgs& g, float (&v)[kHa
 #pragma unroll
   for (int i = 4; i < kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
   const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  // where no score is above -inf every exponential is 0, not exp(-inf + inf)
-  const float ml = (m == -INFINITY ? 0.f : m) * kLog2e;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  // The difference is taken before it is scaled: the largest score gives 1
+  // exactly, and no rounding of m log2(e), which grows with m, enters the sum.
+  // Two columns an instruction.  Where no score is above -inf every
+  // exponential is 0, not exp(-inf + inf).
+  const float2 less = both(m == -INFINITY ? 0.f : -m), to2 = both(kLog2e);
+  float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
-  for (int i = 0; i < kHalf; ++i) sum[i & 3] += exp2_fast(fmaf(v[i], kLog2e, -ml));
-  *part = failed ? make_float2(nan, nan) : make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+  for (int i = 0; i < kHalf; i += 2) {
+    const float2 d = mul2(add2(make_float2(v[i], v[i + 1]), less), to2);
+    sum[i / 2 & 1] = add2(sum[i / 2 & 1], make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+  }
+  const float2 all = add2(sum[0], sum[1]);
+  *part = failed ? make_float2(nan, nan) : make_float2(m, all.x + all.y);
 }
 
 // One box of 32 rows of 128 bytes on its way out.  Lane r holds row r as eight
@@ -394,9 +401,12 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
   if (row >= g.m || left <= 0) return;  // COPY: of none or all of the warp
   const int lane = threadIdx.x & 31;
   const int64_t label = load_id(g.labels, g.labels64, row, g.vocab);
-  const int64_t at = label - (g.b_row0 + col0);
-  const float f = label >= 0 ? __fdiv_rn(g.dloss[row], scale) : 0.f;
-  const float ll = g.lse[row] * kLog2e;
+  const int64_t from = label - (g.b_row0 + col0);
+  const int at = from >= 0 && from < kHalf ? (int)from : -1;
+  const float f = __fdiv_rn(g.dloss[row], scale);
+  // two results as they go out: zeros of a padding row, whatever it holds
+  const uint32_t keep = label >= 0 ? 0xFFFFFFFFu : 0u, bad = failed ? 0x7FC07FC0u : 0u;
+  const float2 less = both(-g.lse[row]), to2 = both(kLog2e);  // scaled after, as for the scores
   const size_t at_row = (size_t)row * g.ld_dz + col0;
 #pragma unroll
   for (int c0 = 0; c0 < kHalf; c0 += kWidth) {
@@ -404,10 +414,11 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
     // whole 32-byte vectors stay inside the tile and the row
     if (c0 >= left) break;
 #pragma unroll
-    for (int i = c0; i < c0 + kWidth; ++i) {
-      const float p = exp2_fast(fmaf(v[i], kLog2e, -ll));
-      v[i] = label < 0 ? 0.f : f * (i == at ? p - 1.f : p);
-      if (failed) v[i] = __uint_as_float(0x7FC00000u);
+    for (int i = c0; i < c0 + kWidth; i += 2) {
+      const float2 d = mul2(add2(make_float2(v[i], v[i + 1]), less), to2);
+      const float2 p = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+      v[i] = f * (i == at ? p.x - 1.f : p.x);
+      v[i + 1] = f * (i + 1 == at ? p.y - 1.f : p.y);
     }
 #pragma unroll
     for (int part = 0; part < kMaxParts; ++part) {
@@ -423,6 +434,7 @@ __device__ __forceinline__ void epilogue_dz(const GemmArgs& g, float (&v)[kHalf]
           widen2(w[i], lo, hi);
           v[c + 2 * i] -= lo;  // exact
           v[c + 2 * i + 1] -= hi;
+          w[i] = (w[i] & keep) | bad;
         }
         if constexpr (COPY) {
           out_put(box, lane, (c - c0) / 8, w[0], w[1], w[2], w[3]);
