@@ -498,7 +498,8 @@ rcc_status rcc_linear_ce_forward(const void* x, size_t ld_x, const void* w, size
  * of three bf16 numbers, which hold all of fp32's 24 bits and cost three times
  * the products.  Sums are fp32.  The logits are formed
  * again, a piece of the vocabulary at a time; the workspace holds one
- * piece's dz (512 MiB at most, and a piece is at least 256 entries). */
+ * piece's dz (512 MiB at most, and a piece is at least 256 entries) and a copy
+ * of x: what rows of padding tokens hold, NaN included, reaches no gradient. */
 rcc_status rcc_linear_ce_backward(const void* x, size_t ld_x, const void* w, size_t ld_w,
                                   const void* labels, rcc_index index, const float* lse,
                                   const float* dloss, size_t tokens, size_t vocab, size_t dim,

@@ -1,5 +1,5 @@
 """The output layer's special values, against 64 bits: large scores, certain
-tokens, masked vocabulary entries."""
+tokens, masked vocabulary entries, padding tokens that hold anything."""
 import math
 
 import pytest
@@ -118,3 +118,36 @@ def test_masked_entries_do_not_count(tokens, vocab, first, last, mask):
         _, dw = rcc.linear_ce_backward(x, w, kept[at], lse, dloss, grad_dtype=kind, need_dx=False)
         assert not dw[~keep].any()
         defs.within(dw[kept], want["dw"], bound["dw", kind])
+
+
+# ---------------------------------------------------------------- padding tokens
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("tokens,vocab,dim,extra", [(3, 300, 72, 0), (100, 2049, 200, 8),
+                                                    (200, 700, 1000, 0), (640, 1500, 512, 8)])
+def test_what_padding_tokens_hold_reaches_nothing(tokens, vocab, dim, extra, bad):
+    """Padding adds to no gradient, whatever stands in its row of x and its dloss:
+    the bits are those of rows of zeros."""
+    x, w, labels, dloss = defs.ce_inputs(22, tokens, vocab, dim)
+    labels[0] = -1
+    padding = (labels < 0) | (labels >= vocab)
+    x[padding] = 0.0
+    clean = x.clone()
+    x[padding] = bad
+    dirty = dloss.clone()
+    dirty[padding] = bad
+    if extra:
+        x = defs.strided(x, extra)
+    loss0, lse0 = rcc.linear_ce_forward(clean, w, labels)
+    loss, lse = rcc.linear_ce_forward(x, w, labels)
+    assert torch.equal(loss, loss0) and torch.equal(lse[~padding], lse0[~padding])
+    for kind in (BF16, F32):
+        dx0, dw0 = rcc.linear_ce_backward(clean, w, labels, lse0, dloss, grad_dtype=kind)
+        dx, dw = rcc.linear_ce_backward(x, w, labels, lse, dirty, grad_dtype=kind)
+        assert torch.equal(dx, dx0) and torch.equal(dw, dw0)
+        base = torch.ones_like(dw)
+        only = rcc.linear_ce_backward(x, w, labels, lse, dirty, dw=base.clone(), need_dx=False,
+                                      accumulate=True)[1]
+        assert torch.equal(only, rcc.linear_ce_backward(clean, w, labels, lse0, dloss,
+                                                        dw=base.clone(), need_dx=False,
+                                                        accumulate=True)[1])
