@@ -4,10 +4,16 @@ _lm.so, the torch binding of the language-model operators.
 nvcc, one -gencode for sm_103a, the translation units compiled in parallel,
 static CUDA runtime, only the rcc_* symbols exported.  No fast-math: means use
 IEEE division and bf16 outputs round to nearest even.
+
+librcc.so needs nothing but nvcc.  Where torch is missing the binding is left
+out; where it does not compile that is said, and librcc.so is built all the same.
 """
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,18 +43,45 @@ def _inputs():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _newer_than_inputs(path: str) -> bool:
+    if not os.path.exists(path):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec else None
+
+
+def _binding_for() -> str:
+    """What _lm.so is good for: this Python, and the torch that it finds."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "?"
+    return "%s, torch %s in %s\n" % (sysconfig.get_config_var("SOABI"), version, _torch_dir())
+
+
+def _binding_up_to_date() -> bool:
+    """True also where there is no torch to build it for."""
+    if not _torch_dir():
+        return True
+    stamp = os.path.join(OBJDIR, "_lm.for")
+    if not _newer_than_inputs(BINDING) or not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == _binding_for()
+
+
+def up_to_date() -> bool:
+    return _newer_than_inputs(LIB) and _binding_up_to_date()
 
 
 def binding_command(out: str):
     """g++ on lm_binding.cpp with Python's and torch's headers and libraries."""
-    import importlib.util
-    import sysconfig
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    torch_dir = _torch_dir()
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     lib = os.path.join(torch_dir, "lib")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=1",
@@ -60,15 +93,52 @@ def binding_command(out: str):
             "-Wl,-rpath," + lib]
 
 
+def _start_binding(out: str, verbose: bool):
+    cmd = binding_command(out)
+    if verbose:
+        print(" ".join(cmd))
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_binding(proc, out: str) -> None:
+    text, _ = proc.communicate()
+    stamp = os.path.join(OBJDIR, "_lm.for")
+    if os.path.exists(stamp):
+        os.remove(stamp)
+    if proc.returncode != 0:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        print("note: _lm.so, the language-model operators' binding, did not build:\n"
+              + text.decode(errors="replace"), file=sys.stderr)
+        return
+    os.replace(out, BINDING)
+    with open(stamp, "w") as f:
+        f.write(_binding_for())
+
+
 def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB,
           objdir: str = OBJDIR) -> str:
-    """Compile librcc.so.  `defines` (e.g. ["-DRCC_WAVES=8"]) rebuild the
-    kernels with other tuning macros into `lib` / `objdir` (a comparison
-    build that RCC_LIBRARY can point the binding at)."""
+    """Compile librcc.so, and _lm.so where there is a torch.  `defines` (e.g.
+    ["-DRCC_WAVES=8"]) rebuild the kernels with other tuning macros into `lib` /
+    `objdir` (a comparison build that RCC_LIBRARY can point the binding at)."""
     defines = list(defines)
     if not force and not defines and lib == LIB and up_to_date():
         return LIB
     os.makedirs(objdir, exist_ok=True)
+    binding = None
+    if lib == LIB and _torch_dir() and (force or not _binding_up_to_date()):
+        out = os.path.join(objdir, "_lm.%d.so" % os.getpid())
+        binding = (_start_binding(out, verbose), out)
+    try:
+        if force or defines or lib != LIB or not _newer_than_inputs(LIB):
+            _build_lib(verbose, defines, lib, objdir)
+    finally:
+        if binding:
+            _finish_binding(*binding)
+    return lib
+
+
+def _build_lib(verbose: bool, defines, lib: str, objdir: str) -> None:
     jobs = []
     for dt, red, fast in PARTS:
         name = "collectives_part_%d_%d_%d" % (dt, red, fast)
@@ -88,11 +158,6 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
         if verbose:
             print(" ".join(cmd))
         procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    binding = None
-    if lib == LIB:
-        binding = os.path.join(objdir, "_lm.%d.so" % os.getpid())
-        procs.append(("lm_binding", subprocess.Popen(
-            binding_command(binding), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -110,9 +175,6 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
         print(" ".join(link))
     subprocess.run(link, check=True)
     os.replace(tmp, lib)
-    if binding:
-        os.replace(binding, BINDING)
-    return lib
 
 
 if __name__ == "__main__":

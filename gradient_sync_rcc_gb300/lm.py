@@ -15,7 +15,11 @@ import ctypes as C
 import torch
 
 from gradient_sync_rcc_gb300 import rcc as _rcc
-from gradient_sync_rcc_gb300 import _lm
+try:
+    from gradient_sync_rcc_gb300 import _lm
+except ImportError as e:
+    raise ImportError("the language-model operators' binding _lm.so does not load (%s); build it "
+                      "with gradient_sync_rcc_gb300.build.build()" % e) from e
 
 
 def _fail(status):
