@@ -218,16 +218,18 @@ constexpr int kTmemCols = 512;  // two accumulators of kBN columns
 // 4,000 of them).  So an accumulator takes a few instructions of 16 products
 // each, and the epilogue adds the accumulators up in registers, rounding to
 // nearest.  Scores of 2,000 x 50,021 x 2,048, the loss's distance from 64 bits
-// (plain fp32 sums 6.5e-7): 64 instructions 8.4e-7 and 233 us, 48 5.5e-7 and
-// 238, 32 3.8e-7 and 243, 16 1.9e-7 and 290; where a pass waits for W anyway,
-// 16: 100 x 50,021 x 1,024 1.9e-7 (plain 4.2e-7) and 21.6 us, 8 1.0e-7 and
-// 23.7.  For fp32 gradients (2,048 x 32,000 x 1,024): 96 1.2e-6, 48 7e-7, 24
-// 4.5e-7 for 3% of the time.  A gradient that is rounded to bf16 is taken whole.
+// (plain fp32 sums 6.6e-7): 64 instructions 8.2e-7 and 237 us, 48 5.3e-7 and
+// 242, 32 3.7e-7 and 244, 16 1.8e-7 and 266; where a pass waits for W anyway,
+// 16: 100 x 50,021 x 1,024 1.8e-7 (plain 4.1e-7) and 21.1 us, 8 1.1e-7 and
+// 23.5.  For fp32 gradients (2,048 x 32,000 x 1,024): 96 1.3e-6, 48 7e-7, 24
+// 4.9e-7 for 1.5% of the time.  A gradient that is rounded to bf16 is taken
+// whole, its accumulator as long as the sum: what that drops (3.7e-5 after
+// 4,000 additions) is far below the rounding of dz and of the result.
 constexpr int kScoreMmas = 48, kScoreMmasFew = 16, kOutMmas = 48;
 
 // bf16 numbers that make one fp32 value of dz: 24 bits, eight each.  2,048 x
-// 32,000 x 1,024: three leave dx and dW 7e-7 off 64 bits (plain fp32: 3.2e-6
-// and 8e-7) and take 560 us, two 2.1e-6 and 1.9e-6 and 421 us.
+// 32,000 x 1,024: three leave dx and dW 7e-7 off 64 bits (plain fp32: 3.3e-6
+// and 8e-7) and take 603 us, two 2.0e-6 and 1.7e-6 and 445 us.
 constexpr int kMaxParts = 3;
 
 enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };

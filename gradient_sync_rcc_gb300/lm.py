@@ -132,6 +132,11 @@ def linear_ce_backward(x, w, labels, lse, dloss, grad_dtype=None, dx=None, dw=No
                        stream=None):
     """rcc_linear_ce_backward: gradients of sum(dloss * loss).  Returns (dx, dw)
     of grad_dtype (a passed output's, else bfloat16); None for one that is not
-    needed.  With accumulate dw is passed and added to."""
+    needed.  With accumulate dw is passed and added to.
+
+    The type also decides how exact the gradients are: for bfloat16 dz is
+    rounded to bfloat16 too (0.0020 off 64 bits in all, where the rounding of
+    the results alone is 0.0017); for float32 it keeps 24 bits (7e-7 off) at
+    three times the gradients' products."""
     return _lm.linear_ce_backward(x, w, labels, lse, dloss, grad_dtype, dx, dw, accumulate,
                                   workspace, need_dx, need_dw, stream)
