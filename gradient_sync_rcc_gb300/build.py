@@ -27,8 +27,9 @@ NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
           "-I", INCLUDE, "-I", CSRC]
-SOURCES = ["gradsync.cu", "embedding.cu", "rmsnorm.cu", "linear_ce.cu", "rcc_host.cpp",
-           "rcc_rank.cpp", "rcc_gradsync_host.cpp", "rcc_lm_host.cpp"]
+SOURCES = ["gradsync.cu", "embedding.cu", "rmsnorm.cu", "add_rmsnorm.cu",
+           "rotary.cu", "adamw.cu", "linear_ce.cu", "rcc_host.cpp",
+           "rcc_rank.cpp", "rcc_gradsync_host.cpp", "rcc_lm_host.cpp", "rcc_adamw_host.cpp"]
 # collectives_part.cu is compiled once per (element type, reduction, tree
 # order) that the host dispatcher names: fp32 (0) and bf16 (1) x rank-order
 # sum (0), tree sum (0, fast), max (1), min (2), copy (3).

@@ -36,6 +36,11 @@ struct Entries {
   decltype(&rcc_linear_ce_forward) linear_ce_forward;
   decltype(&rcc_linear_ce_backward) linear_ce_backward;
   decltype(&rcc_linear_ce_workspace) linear_ce_workspace;
+  decltype(&rcc_add_rmsnorm_forward) add_rmsnorm_forward;
+  decltype(&rcc_add_rmsnorm_backward) add_rmsnorm_backward;
+  decltype(&rcc_rotary_forward) rotary_forward;
+  decltype(&rcc_rotary_backward) rotary_backward;
+  decltype(&rcc_adamw_step) adamw_step;
 } rcc_;
 PyObject* on_error = nullptr;  // called with a status that is not RCC_OK; raises
 
@@ -355,6 +360,201 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- RMS norm with the residual's addition, output in 8 bits ---------------------
+
+PyObject* none_or(at::Tensor t) {
+  return t.defined() ? wrap(std::move(t)) : Py_NewRef(Py_None);
+}
+
+// x, residual, weight, eps, 8-bit output, keep (None, True, or a buffer), its tokens, its dim, h,
+// out, out's scales, stream: (out, its scales, h, keep's new buffer)
+PyObject* add_rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("add_rmsnorm_forward", n, 12, [&] {
+    const at::Tensor &x = tensor(a[0], "x"), &weight = tensor(a[2], "weight");
+    const at::Device dev = x.device();
+    const Matrix m = matrix(x, "x", dev);
+    const rcc_dtype kind = dtype_of(x, "x");
+    const bool eight = truth(a[4]);
+    Matrix mr = {m.rows, m.cols, m.cols};
+    const void* residual = nullptr;
+    if (given(a[1])) {
+      const at::Tensor& r = tensor(a[1], "residual");
+      mr = matrix(r, "residual", dev);
+      if (mr.rows != m.rows || mr.cols != m.cols || r.scalar_type() != x.scalar_type())
+        refuse("residual must be of x's type and shape");
+      residual = r.data_ptr();
+    } else {
+      if (!eight) refuse("without a residual the output has to be 8-bit");
+      if (given(a[8])) refuse("h is the sum with a residual");
+    }
+    const float* w = floats(weight, "weight", dev, m.cols);
+    const float eps = (float)number(a[3]);
+    at::Tensor data, h, y, scales;
+    if (given(a[5]) && a[5] != Py_True) data = kept_arg(a[5], a[6], a[7], m.rows, m.cols, dev);
+    const auto type = eight ? at::kFloat8_e4m3fn : x.scalar_type();
+    if (given(a[8])) h = output(a[8], "h", {m.rows, m.cols}, x.scalar_type(), dev);
+    if (given(a[9])) y = output(a[9], "out", {m.rows, m.cols}, type, dev);
+    if (given(a[10])) {
+      if (!eight) refuse("out_scales come with an 8-bit output");
+      scales = output(a[10], "out_scales", {m.rows, groups_of(m.cols)}, at::kFloat, dev);
+    }
+    const Stream stream(a[11], dev);
+    if (given(a[1]) && !h.defined()) h = fresh({m.rows, m.cols}, x.scalar_type(), dev);
+    if (!y.defined()) y = fresh({m.rows, m.cols}, type, dev);
+    if (eight && !scales.defined()) scales = fresh({m.rows, groups_of(m.cols)}, at::kFloat, dev);
+    if (a[5] == Py_True) data = fresh({kept_bytes(m.rows, m.cols)}, at::kByte, dev);
+    const Kept k = data.defined() ? kept_in(data, m.rows, m.cols) : Kept{nullptr, nullptr};
+    if (m.rows)  // empty tensors have no addresses to tell apart
+      call(rcc_.add_rmsnorm_forward, x.data_ptr(), (size_t)m.ld, residual, (size_t)mr.ld, kind, w,
+           eps, (size_t)m.rows, (size_t)m.cols, h.defined() ? h.data_ptr() : nullptr, y.data_ptr(),
+           eight ? static_cast<float*>(scales.data_ptr()) : nullptr, k.values, k.scales,
+           stream.handle());
+    PyObject* r = PyTuple_New(4);
+    if (!r) throw python_error();
+    PyTuple_SET_ITEM(r, 0, wrap(std::move(y)));
+    PyTuple_SET_ITEM(r, 1, none_or(std::move(scales)));
+    PyTuple_SET_ITEM(r, 2, none_or(std::move(h)));
+    PyTuple_SET_ITEM(r, 3, none_or(a[5] == Py_True ? std::move(data) : at::Tensor()));
+    return r;
+  });
+}
+
+// dy, dh, kept's buffer, tokens and dim, weight, eps, dx, dweight, accumulate, workspace, stream
+PyObject* add_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("add_rmsnorm_backward", n, 12, [&] {
+    const at::Tensor &dy = tensor(a[0], "dy"), &weight = tensor(a[5], "weight");
+    const at::Device dev = dy.device();
+    const Matrix m = matrix(dy, "dy", dev);
+    const rcc_dtype kind = dtype_of(dy, "dy");
+    Matrix mh = {m.rows, m.cols, m.cols};
+    const void* dh = nullptr;
+    if (given(a[1])) {
+      const at::Tensor& t = tensor(a[1], "dh");
+      mh = matrix(t, "dh", dev);
+      if (mh.rows != m.rows || mh.cols != m.cols || t.scalar_type() != dy.scalar_type())
+        refuse("dh must be of dy's type and shape");
+      dh = t.data_ptr();
+    }
+    const Kept k = kept_in(kept_arg(a[2], a[3], a[4], m.rows, m.cols, dev), m.rows, m.cols);
+    const float* w = floats(weight, "weight", dev, m.cols);
+    const float eps = (float)number(a[6]);
+    const int accumulate = truth(a[9]);
+    if (accumulate && !given(a[8])) refuse("accumulate needs the dweight to add to");
+    at::Tensor dx, dweight;
+    if (given(a[7])) dx = output(a[7], "dx", {m.rows, m.cols}, dy.scalar_type(), dev);
+    if (given(a[8])) dweight = output(a[8], "dweight", {m.cols}, at::kFloat, dev);
+    const Stream stream(a[11], dev);
+    if (!dx.defined()) dx = fresh({m.rows, m.cols}, dy.scalar_type(), dev);
+    if (!dweight.defined()) dweight = fresh({m.cols}, at::kFloat, dev);
+    const Workspace ws = workspace(a[10], rcc_.rmsnorm_backward_workspace(m.rows, m.cols), dev);
+    call(rcc_.add_rmsnorm_backward, dy.data_ptr(), (size_t)m.ld, dh, (size_t)mh.ld, kind, k.values,
+         k.scales, w, eps, (size_t)m.rows, (size_t)m.cols, dx.data_ptr(),
+         static_cast<float*>(dweight.data_ptr()), accumulate, ws.p, ws.bytes, stream.handle());
+    return wrap(std::move(dx), std::move(dweight));
+  });
+}
+
+// ---- rotary positions -----------------------------------------------------------
+
+// [tokens, heads, head_dim] with neighbouring elements of a head
+struct Heads {
+  int64_t tokens, heads, head_dim;
+  size_t token, head;
+};
+Heads heads_of(const at::Tensor& t, const char* what, at::Device dev) {
+  if (t.dim() != 3 || t.device() != dev)
+    refuse("%s must be [tokens, heads, head_dim] on the inputs' device", what);
+  const Heads h = {t.size(0), t.size(1), t.size(2),
+                   (size_t)(t.size(0) < 2 ? t.size(1) * t.size(2) : t.stride(0)),
+                   (size_t)(t.size(1) < 2 ? t.size(2) : t.stride(1))};
+  if (h.head_dim > 1 && t.stride(2) != 1) refuse("the heads of %s must be contiguous", what);
+  return h;
+}
+
+// inverse, q, k, turns, positions, offset, layout, scale, q_out, k_out, stream
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("rotary", n, 11, [&] {
+    const bool inverse = truth(a[0]);
+    const char* names[2] = {"q", "k"};
+    const char* out_names[2] = {"q_out", "k_out"};
+    const at::Tensor& q = tensor(a[1], "q");
+    const at::Device dev = q.device();
+    const rcc_dtype kind = dtype_of(q, "q");
+    const int count = given(a[2]) ? 2 : 1;
+    if (count == 1 && given(a[9])) refuse("k_out without k");
+    Heads in[2];
+    at::Tensor out[2];
+    rcc_rotary_rows rows[2] = {};
+    for (int i = 0; i < count; ++i) {
+      const at::Tensor& t = tensor(a[1 + i], names[i]);
+      in[i] = heads_of(t, names[i], dev);
+      if (t.scalar_type() != q.scalar_type() || in[i].tokens != in[0].tokens ||
+          in[i].head_dim != in[0].head_dim)
+        refuse("q and k must have one type, tokens and head_dim");
+      if (given(a[8 + i])) {
+        out[i] = tensor(a[8 + i], out_names[i]);
+        if (out[i].sizes() != t.sizes() || out[i].scalar_type() != t.scalar_type())
+          refuse("%s must be of %s's type and shape", out_names[i], names[i]);
+        heads_of(out[i], out_names[i], dev);
+      }
+      rows[i].in = t.data_ptr();
+      rows[i].heads = in[i].heads;
+      rows[i].in_token = in[i].token;
+      rows[i].in_head = in[i].head;
+    }
+    const at::Tensor& turns = tensor(a[3], "turns");
+    if (turns.scalar_type() != at::kLong || turns.dim() != 1 || turns.device() != dev ||
+        !turns.is_contiguous() || 2 * turns.numel() > in[0].head_dim)
+      refuse("turns must be a contiguous vector of int64, at most half of head_dim, on the inputs' "
+             "device");
+    rcc_index index = RCC_I32;
+    const void* positions = nullptr;
+    if (given(a[4])) {
+      const at::Tensor& p = tensor(a[4], "positions");
+      index = index_of(p, "positions", dev, in[0].tokens);
+      positions = p.data_ptr();
+    }
+    const long long offset = PyLong_AsLongLong(a[5]);
+    const long layout = PyErr_Occurred() ? 0 : PyLong_AsLong(a[6]);
+    if (PyErr_Occurred()) throw python_error();
+    const float scale = (float)number(a[7]);
+    const Stream stream(a[10], dev);
+    for (int i = 0; i < count; ++i) {
+      if (!out[i].defined())
+        out[i] = fresh({in[i].tokens, in[i].heads, in[i].head_dim}, q.scalar_type(), dev);
+      const Heads h = heads_of(out[i], out_names[i], dev);
+      rows[i].out = out[i].data_ptr();
+      rows[i].out_token = h.token;
+      rows[i].out_head = h.head;
+    }
+    call(inverse ? rcc_.rotary_backward : rcc_.rotary_forward,
+         static_cast<const rcc_rotary_rows*>(&rows[0]),
+         static_cast<const rcc_rotary_rows*>(count == 2 ? &rows[1] : nullptr), kind,
+         (size_t)in[0].tokens, (size_t)in[0].head_dim,
+         static_cast<const uint64_t*>(turns.data_ptr()), (size_t)turns.numel(),
+         (rcc_rotary_layout)layout, positions, index, (int64_t)offset, scale, stream.handle());
+    return wrap(std::move(out[0]), std::move(out[1]));
+  });
+}
+
+// ---- AdamW over many tensors -----------------------------------------------------
+
+// plan, cfg's address, scale, device, stream
+PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("adamw_step", n, 5, [&] {
+    auto plan = static_cast<rcc_adamw>(PyLong_AsVoidPtr(a[0]));
+    if (PyErr_Occurred()) throw python_error();
+    auto cfg = static_cast<const rcc_adamw_cfg*>(PyLong_AsVoidPtr(a[1]));
+    if (PyErr_Occurred()) throw python_error();
+    const double scale = number(a[2]);
+    const long device = PyLong_AsLong(a[3]);
+    if (PyErr_Occurred()) throw python_error();
+    const Stream stream(a[4], at::Device(at::kCUDA, (c10::DeviceIndex)device));
+    call(rcc_.adamw_step, plan, cfg, scale, stream.handle());
+    return Py_NewRef(Py_None);
+  });
+}
+
 // ---- output layer ---------------------------------------------------------------
 
 struct Scores {
@@ -462,6 +662,10 @@ PyMethodDef methods[] = {
     {"embedding_backward", RCC_FAST(embedding_backward), nullptr},
     {"rmsnorm_forward", RCC_FAST(rmsnorm_forward), nullptr},
     {"rmsnorm_backward", RCC_FAST(rmsnorm_backward), nullptr},
+    {"add_rmsnorm_forward", RCC_FAST(add_rmsnorm_forward), nullptr},
+    {"add_rmsnorm_backward", RCC_FAST(add_rmsnorm_backward), nullptr},
+    {"rotary", RCC_FAST(rotary), nullptr},
+    {"adamw_step", RCC_FAST(adamw_step), nullptr},
     {"linear_ce_forward", RCC_FAST(linear_ce_forward), nullptr},
     {"linear_ce_backward", RCC_FAST(linear_ce_backward), nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -1,8 +1,10 @@
 // lm_internal.h -- launch interface between the host layer of the
 // language-model operators (rcc_lm_host.cpp) and their kernels
-// (embedding.cu, rmsnorm.cu, linear_ce.cu).  Not part of the public ABI.
+// (embedding.cu, rmsnorm.cu, add_rmsnorm.cu, rotary.cu, adamw.cu, linear_ce.cu).
+// Not part of the public ABI.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -59,8 +61,14 @@ struct NormArgs {
   int type;
   bool vec;
   float eps;
+  // the residual's addition and the output in 8 bits (add_rmsnorm.cu)
+  const void* residual;  // added to x, or NULL
+  void* sum;             // [tokens][dim], with a residual
+  float* y_scales;       // [tokens][groups]: y is e4m3; or NULL
+  size_t ld_residual;
 };
 cudaError_t launch_rmsnorm_forward(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_forward(const NormArgs& a, cudaStream_t stream);
 
 struct NormGradArgs {
   const void* dy;
@@ -75,10 +83,80 @@ struct NormGradArgs {
   int type;
   bool vec, accumulate;
   float eps;
+  const void* dsum;  // the sum's own gradient (add_rmsnorm.cu)
+  size_t ld_dsum;
 };
 size_t rmsnorm_backward_workspace(size_t tokens, size_t dim);
 cudaError_t launch_rmsnorm_backward(const NormGradArgs& a, cudaStream_t stream,
                                     uint64_t* launches);
+cudaError_t launch_add_rmsnorm_backward(const NormGradArgs& a, cudaStream_t stream,
+                                        uint64_t* launches);
+
+// ---- rotary positions ------------------------------------------------------------
+
+struct RotaryRows {
+  const void* in;
+  void* out;
+  size_t heads;
+  size_t in_token, in_head, out_token, out_head;  // elements apart
+};
+struct RotaryArgs {
+  RotaryRows q, k;        // k.heads may be 0
+  const uint64_t* turns;  // [pairs]
+  const void* positions;  // [tokens], or NULL: 0, 1, ...
+  int64_t offset;         // added to the positions
+  size_t tokens, head_dim, pairs;
+  int type, index64;
+  bool half, inverse;
+  bool copies;            // the columns past the pairs are written too
+  bool vec;               // every row in vectors of eight elements
+  float scale;
+  uint32_t turned_units, copied_units, chunks;  // set by the launch
+};
+constexpr size_t kMaxHeads = 65536;
+constexpr size_t kMaxHeadDim = 8192;
+cudaError_t launch_rotary(RotaryArgs a, cudaStream_t stream);
+
+// ---- AdamW over many tensors -------------------------------------------------------
+
+constexpr int kAdamWItem = 4096;            // elements of a tensor that are one item
+constexpr float kAdamWNothing = 7.88860905e-31f;  // 2^-100: a group below it is held as zeros
+
+struct AdamWTensor {
+  const void* grad;
+  float* param;
+  void *m, *v;                // fp32, or e4m3 with
+  float *m_scales, *v_scales;
+  __nv_bfloat16* copy;        // or NULL
+  uint64_t numel;
+  uint32_t bf16;              // the gradient's type
+  uint32_t vec;               // every buffer on a boundary of eight elements
+};
+struct AdamWItem {
+  uint32_t tensor, chunk;
+};
+struct AdamWRow {             // a block's part of the norm
+  double sum;
+  uint32_t bad, unused;
+};
+struct AdamWDecision {
+  uint32_t skip, step;        // step: steps taken before, its low bits
+  float coef, step_size, inv_root;
+};
+struct AdamWArgs {
+  const AdamWTensor* tensors;
+  const AdamWItem* items;
+  AdamWRow* rows;
+  rcc_adamw_status* status;
+  AdamWDecision* decision;
+  uint64_t num_items;
+  int num_rows;               // room for so many
+  uint32_t seed;
+  double scale, max_norm, lr, beta1, beta2;
+  float inv_scale, b1, one_minus_b1, b2, one_minus_b2, eps, decay;
+};
+int adamw_rows();             // rows of the current device
+cudaError_t launch_adamw(const AdamWArgs& a, bool eight, cudaStream_t stream, uint64_t* launches);
 
 // ---- output layer + softmax cross entropy ----------------------------------------
 

@@ -1,7 +1,8 @@
 """Binding of the language-model operators of librcc (include/rcc.h): token
-embedding and its gradient, the RMS norm that keeps its input in 8 bits, and
-the output layer with softmax cross entropy.  Reached as attributes of `rcc`,
-like the rest of the binding.
+embedding and its gradient, the RMS norm that keeps its input in 8 bits, alone
+and with the residual's addition, rotary positions, the output layer with
+softmax cross entropy, and AdamW over many tensors.  Reached as attributes of
+`rcc`, like the rest of the binding.
 
 The work of a call -- checks of what the C entry points cannot see (a type, a
 device, a shape that does not fit: ValueError), outputs and workspaces that
@@ -30,7 +31,9 @@ _lib = _rcc.lib()
 _lm.bind(_fail, *(C.cast(getattr(_lib, name), C.c_void_p).value for name in (
     "rcc_embedding_forward", "rcc_embedding_backward", "rcc_embedding_backward_workspace",
     "rcc_rmsnorm_forward", "rcc_rmsnorm_backward", "rcc_rmsnorm_backward_workspace",
-    "rcc_linear_ce_forward", "rcc_linear_ce_backward", "rcc_linear_ce_workspace")))
+    "rcc_linear_ce_forward", "rcc_linear_ce_backward", "rcc_linear_ce_workspace",
+    "rcc_add_rmsnorm_forward", "rcc_add_rmsnorm_backward", "rcc_rotary_forward",
+    "rcc_rotary_backward", "rcc_adamw_step")))
 
 
 # ------------------------------------------------------------- embedding
@@ -112,6 +115,220 @@ def rmsnorm_backward(dy, kept, weight, eps=1e-6, dx=None, dweight=None, accumula
     dweight is passed and added to."""
     return _lm.rmsnorm_backward(dy, kept.data, kept.tokens, kept.dim, weight, eps, dx, dweight,
                                 accumulate, workspace, stream)
+
+
+# ------------------------------------------------------------- RMS norm with the residual's addition
+
+class Scaled:
+    """A matrix in 8 bits: values [tokens, dim] float8_e4m3fn and scales
+    [tokens, ceil(dim / 128)] float32."""
+
+    __slots__ = ("values", "scales")
+
+    def __init__(self, values, scales):
+        self.values, self.scales = values, scales
+
+    def dequantize(self):
+        """What it stands for, [tokens, dim] float32."""
+        dim = self.values.shape[1]
+        return self.values.float() * self.scales.repeat_interleave(KEEP_GROUP, 1)[:, :dim]
+
+
+def add_rmsnorm_forward(x, residual, weight, eps=1e-6, out_dtype=None, keep=False, h=None,
+                        out=None, stream=None):
+    """rcc_add_rmsnorm_forward: h = x + residual and y = RMS norm of h.  Returns
+    (y, h), or (y, h, kept) with keep: True, or a Kept of these sizes to be
+    written.
+
+    y is of x's type; with out_dtype=torch.float8_e4m3fn, or a Scaled as `out`,
+    it is a Scaled.  h may be x or residual itself.  A residual of None (8-bit
+    y) adds nothing and gives an h of None."""
+    eight = out_dtype == torch.float8_e4m3fn or isinstance(out, Scaled)
+    if out_dtype not in (None, x.dtype, torch.float8_e4m3fn) or \
+            (out is not None and isinstance(out, Scaled) != eight):
+        raise ValueError("out_dtype must be x's type or torch.float8_e4m3fn, and out fit it")
+    values, scales = (out.values, out.scales) if isinstance(out, Scaled) else (out, None)
+    buffer, tokens, dim = (keep.data, keep.tokens, keep.dim) if isinstance(keep, Kept) else \
+        (True if keep else None, 0, 0)
+    y, scales, h, data = _lm.add_rmsnorm_forward(x, residual, weight, eps, eight, buffer, tokens,
+                                                 dim, h, values, scales, stream)
+    if eight:
+        y = out if isinstance(out, Scaled) else Scaled(y, scales)
+    if not keep:
+        return y, h
+    return y, h, Kept(x.shape[0], x.shape[1], data=data) if keep is True else keep
+
+
+def add_rmsnorm_backward(dy, dh, kept, weight, eps=1e-6, dx=None, dweight=None, accumulate=False,
+                         workspace=None, stream=None):
+    """rcc_add_rmsnorm_backward from a Kept of h: the gradient of x, which is also
+    residual's, for dy of y and dh of h (None: h has no other use).  Returns
+    (dx, dweight); dx may be dh itself, and with accumulate dweight is passed
+    and added to.  Workspace: rmsnorm_backward_workspace."""
+    return _lm.add_rmsnorm_backward(dy, dh, kept.data, kept.tokens, kept.dim, weight, eps, dx,
+                                    dweight, accumulate, workspace, stream)
+
+
+# ------------------------------------------------------------- rotary positions
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"linear": 1, "base": 2, "parts": 3}
+
+
+def rotary_turns(turned, base=10000.0, scaling=None, device="cuda"):
+    """rcc_rotary_turns for the first `turned` elements of a head: int64
+    [turned / 2] on `device`, once for a model.
+
+    scaling: None, ("linear", factor), ("base", factor) or ("parts", factor,
+    length trained on, low, high)."""
+    if turned < 2 or turned % 2:
+        raise ValueError("an even number of elements is turned, got %r" % (turned,))
+    arg = None
+    if scaling is not None:
+        kind, *numbers = scaling
+        if kind not in _SCALINGS or len(numbers) != (4 if kind == "parts" else 1):
+            raise ValueError("scaling %r is not one of linear, base and parts with its numbers"
+                             % (scaling,))
+        arg = _rcc.RotaryScaling(_SCALINGS[kind], *numbers)
+    turns = torch.empty(turned // 2, dtype=torch.int64)
+    _rcc._check(_lib.rcc_rotary_turns(turned // 2, base, None if arg is None else C.byref(arg),
+                                      turns.data_ptr()))
+    return turns.to(device)
+
+
+def _layout(name):
+    if name not in _LAYOUTS:
+        raise ValueError("layout must be one of %s" % ", ".join(_LAYOUTS))
+    return _LAYOUTS[name]
+
+
+def rotary_forward(q, k, turns, positions=None, offset=0, layout="half", scale=1.0, q_out=None,
+                   k_out=None, stream=None):
+    """rcc_rotary_forward: q and k [tokens, heads, head_dim] (k may be None),
+    turned by their tokens' positions: positions + offset, or 0, 1, ... + offset.
+    Returns (q, k) turned.  Any strides but the last; q_out may be q itself."""
+    return _lm.rotary(False, q, k, turns, positions, offset, _layout(layout), scale, q_out, k_out,
+                      stream)
+
+
+def rotary_backward(dq, dk, turns, positions=None, offset=0, layout="half", scale=1.0, q_out=None,
+                    k_out=None, stream=None):
+    """rcc_rotary_backward: the gradients of rotary_forward's q and k, for dq and
+    dk of its results; the other arguments as there."""
+    return _lm.rotary(True, dq, dk, turns, positions, offset, _layout(layout), scale, q_out, k_out,
+                      stream)
+
+
+# ------------------------------------------------------------- AdamW over many tensors
+
+class AdamWPlan:
+    """The tensors of rcc_adamw_step, with their states and the workspace.
+
+    tensors: dicts with param (float32), grad (float32 or bfloat16), and if
+    wanted copy (bfloat16, receives the new parameters), all contiguous and of
+    one size.  States that are left out are made, as zeros of `states`
+    (torch.float32 or torch.float8_e4m3fn): exp_avg, exp_avg_sq and, for 8 bits,
+    exp_avg_scale and exp_avg_sq_scale [ceil(n / 128)].  `.tensors` has them all;
+    saved with the report's step, and given again with that step, they resume.
+
+    The tensors' addresses are kept: a step reads the gradients where they were.
+    The plan is made on `stream`; steps on another one have to wait for it."""
+
+    def __init__(self, tensors, states=torch.float32, seed=0, step=0, betas=(0.9, 0.999),
+                 stream=None):
+        self.handle = None
+        self.tensors = [self._complete(dict(t), states) for t in tensors]
+        if not self.tensors:
+            raise ValueError("no tensors")
+        dev = self.tensors[0]["param"].device
+        arr = (_rcc.AdamWTensor * len(self.tensors))()
+        for i, t in enumerate(self.tensors):
+            if any(v.device != dev for v in t.values()):
+                raise ValueError("tensor %d: every buffer must be on one device" % i)
+            p = {k: t[k].data_ptr() if k in t else None for k in (
+                "grad", "param", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
+                "copy")}
+            arr[i] = _rcc.AdamWTensor(
+                t["param"].numel(), p["grad"],
+                _rcc.BF16 if t["grad"].dtype == torch.bfloat16 else _rcc.F32, p["param"],
+                p["exp_avg"], p["exp_avg_sq"], p["exp_avg_scale"], p["exp_avg_sq_scale"],
+                p["copy"])
+        if dev.type != "cuda":
+            raise ValueError("the operators take tensors on a CUDA device")
+        _lm.check_device(dev.index, torch.cuda.current_device())
+        self.device = dev.index
+        with _lm_stream(stream, dev):
+            need = _lib.rcc_adamw_workspace(arr, len(arr))
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            handle = C.c_void_p()
+            _rcc._check(_lib.rcc_adamw_create(
+                arr, len(arr), seed & 0xFFFFFFFF, step, betas[0], betas[1],
+                self.workspace.data_ptr(), need, torch.cuda.current_stream().cuda_stream,
+                C.byref(handle)))
+        self.handle = handle.value
+
+    @staticmethod
+    def _complete(t, states):
+        param = t["param"]
+        n = param.numel()
+        if states not in (torch.float32, torch.float8_e4m3fn):
+            raise ValueError("states must be torch.float32 or torch.float8_e4m3fn")
+        t = {k: v for k, v in t.items() if v is not None}
+        for k in ("exp_avg", "exp_avg_sq"):
+            if k not in t:
+                t[k] = torch.zeros(n, dtype=torch.uint8, device=param.device).view(states) \
+                    if states == torch.float8_e4m3fn else torch.zeros_like(param)
+            if t[k].dtype == torch.float8_e4m3fn and k + "_scale" not in t:
+                t[k + "_scale"] = torch.zeros(-(-n // 128), device=param.device)
+        eight = t["exp_avg"].dtype
+        want = {"param": (n, (torch.float32,)), "grad": (n, (torch.float32, torch.bfloat16)),
+                "exp_avg": (n, (torch.float32, torch.float8_e4m3fn)), "exp_avg_sq": (n, (eight,)),
+                "copy": (n, (torch.bfloat16,)), "exp_avg_scale": (-(-n // 128), (torch.float32,)),
+                "exp_avg_sq_scale": (-(-n // 128), (torch.float32,))}
+        for k, v in t.items():
+            if k not in want:
+                raise ValueError("%r is not a buffer of AdamW" % k)
+            count, types = want[k]
+            if v.numel() != count or v.dtype not in types or not v.is_contiguous():
+                raise ValueError("%s must be %d contiguous elements of %s"
+                                 % (k, count, " or ".join(map(str, types))))
+        if "grad" not in t or ("exp_avg_scale" in t) != (eight == torch.float8_e4m3fn) or \
+                ("exp_avg_sq_scale" in t) != (eight == torch.float8_e4m3fn):
+            raise ValueError("a tensor needs a grad, and scales for 8-bit states alone")
+        return t
+
+    @property
+    def grad_norm(self):
+        """The last step's gradient norm: float64, on the device."""
+        return self.workspace[8:16].view(torch.float64)[0]
+
+    def __del__(self):
+        if self.handle is not None:
+            _lib.rcc_adamw_destroy(self.handle)
+            self.handle = None
+
+
+def _lm_stream(stream, dev):
+    """The given stream as the current one, as the compiled calls have it."""
+    if stream is None:
+        return torch.cuda.stream(None)
+    if isinstance(stream, int):
+        stream = torch.cuda.default_stream(dev) if stream in (0, 1) else \
+            torch.cuda.ExternalStream(stream, device=dev)
+    return torch.cuda.stream(stream)
+
+
+def adamw_step(plan, cfg, scale=1.0, stream=None):
+    """rcc_adamw_step: one step over a plan's tensors, their gradients carrying
+    the loss scale `scale`.  cfg: adamw_cfg.  Nothing is read back."""
+    _lm.adamw_step(plan.handle, C.addressof(cfg), scale, plan.device, stream)
+
+
+def adamw_report(plan, stream=None):
+    """What the plan's last step did, an AdamWStatus: waits for it."""
+    with _lm_stream(stream, plan.workspace.device):
+        return _rcc.AdamWStatus.from_buffer_copy(
+            plan.workspace[:C.sizeof(_rcc.AdamWStatus)].cpu().numpy().tobytes())
 
 
 # ------------------------------------------------------------- output layer + cross entropy

@@ -50,7 +50,9 @@ SYMBOLS = ["rcc_register", "rcc_set_flags", "rcc_finish", "rcc_reset", "rcc_all_
            "rcc_last_step_times", "rcc_embedding_forward", "rcc_embedding_backward",
            "rcc_embedding_backward_workspace", "rcc_rmsnorm_forward", "rcc_rmsnorm_backward",
            "rcc_rmsnorm_backward_workspace", "rcc_linear_ce_forward", "rcc_linear_ce_backward",
-           "rcc_linear_ce_workspace"]
+           "rcc_linear_ce_workspace", "rcc_add_rmsnorm_forward", "rcc_add_rmsnorm_backward",
+           "rcc_rotary_turns", "rcc_rotary_forward", "rcc_rotary_backward", "rcc_adamw_workspace",
+           "rcc_adamw_create", "rcc_adamw_step", "rcc_adamw_destroy"]
 
 
 class ParamSet(C.Structure):
@@ -81,6 +83,30 @@ class StepReport(C.Structure):
                 ("combine_region_bytes", C.c_uint64), ("update_launches", C.c_uint64),
                 ("report_words", C.c_uint32 * 3), ("combine_levels", C.c_int32),
                 ("updates_before_readback", C.c_int32)]
+
+
+class RotaryScaling(C.Structure):
+    _fields_ = [("kind", C.c_int), ("factor", C.c_double), ("length", C.c_double),
+                ("low", C.c_double), ("high", C.c_double)]
+
+
+class RotaryRows(C.Structure):
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("heads", C.c_size_t),
+                ("in_token", C.c_size_t), ("in_head", C.c_size_t), ("out_token", C.c_size_t),
+                ("out_head", C.c_size_t)]
+
+
+class AdamWTensor(C.Structure):
+    _fields_ = [("numel", C.c_size_t), ("grad", C.c_void_p), ("grad_type", C.c_int),
+                ("param", C.c_void_p), ("exp_avg", C.c_void_p), ("exp_avg_sq", C.c_void_p),
+                ("exp_avg_scale", C.c_void_p), ("exp_avg_sq_scale", C.c_void_p),
+                ("copy", C.c_void_p)]
+
+
+class AdamWStatus(C.Structure):
+    _fields_ = [("step", C.c_int64), ("grad_norm", C.c_double), ("beta1_power", C.c_double),
+                ("beta2_power", C.c_double), ("nonfinite", C.c_uint32), ("skipped", C.c_int32),
+                ("clip_coef", C.c_float), ("unused", C.c_uint32)]
 
 
 _lib = None
@@ -133,8 +159,21 @@ def lib():
         L.rcc_embedding_backward_workspace.argtypes = [sz, sz, sz]
         L.rcc_rmsnorm_backward_workspace.argtypes = [sz, sz]
         L.rcc_linear_ce_workspace.argtypes = [sz, sz, sz, i, i]
+        rows, pt = C.POINTER(RotaryRows), C.POINTER(AdamWTensor)
+        L.rcc_add_rmsnorm_forward.argtypes = [vp, sz, vp, sz, i, vp, f, sz, sz, vp, vp, vp, vp, vp,
+                                              vp]
+        L.rcc_add_rmsnorm_backward.argtypes = [vp, sz, vp, sz, i, vp, vp, vp, f, sz, sz, vp, vp, i,
+                                               vp, sz, vp]
+        L.rcc_rotary_turns.argtypes = [sz, C.c_double, C.POINTER(RotaryScaling), vp]
+        for name in ("rcc_rotary_forward", "rcc_rotary_backward"):
+            getattr(L, name).argtypes = [rows, rows, i, sz, sz, vp, sz, i, vp, i, C.c_int64, f, vp]
+        L.rcc_adamw_workspace.argtypes = [pt, i]
+        L.rcc_adamw_create.argtypes = [pt, i, C.c_uint32, C.c_int64, C.c_double, C.c_double, vp,
+                                       sz, vp, _PP]
+        L.rcc_adamw_step.argtypes = [vp, C.POINTER(AdamWCfg), C.c_double, vp]
+        L.rcc_adamw_destroy.argtypes = [vp]
         for name in ("rcc_embedding_backward_workspace", "rcc_rmsnorm_backward_workspace",
-                     "rcc_linear_ce_workspace"):
+                     "rcc_linear_ce_workspace", "rcc_adamw_workspace"):
             getattr(L, name).restype = sz
         for name in ("rcc_register", "rcc_set_flags", "rcc_finish", "rcc_reset", "rcc_all_reduce",
                      "rcc_reduce", "rcc_broadcast", "rcc_reduce_scatter", "rcc_all_gather",
@@ -143,7 +182,10 @@ def lib():
                      "rcc_all_gather_rank", "rcc_all_to_all_single", "rcc_all_gather_list",
                      "rcc_last_step_times", "rcc_embedding_forward", "rcc_embedding_backward",
                      "rcc_rmsnorm_forward", "rcc_rmsnorm_backward", "rcc_linear_ce_forward",
-                     "rcc_linear_ce_backward"):
+                     "rcc_linear_ce_backward", "rcc_add_rmsnorm_forward",
+                     "rcc_add_rmsnorm_backward", "rcc_rotary_turns", "rcc_rotary_forward",
+                     "rcc_rotary_backward", "rcc_adamw_create", "rcc_adamw_step",
+                     "rcc_adamw_destroy"):
             getattr(L, name).restype = st
         L.rcc_last_error_message.restype = C.c_char_p
         L.rcc_last_error_message.argtypes = []
@@ -423,7 +465,9 @@ def grad_stats_noalloc(grads, loss_scale, report, mean_grad=None, stream=None):
 _LM_NAMES = ("embedding_forward", "embedding_backward", "embedding_backward_workspace",
              "KEEP_GROUP", "Kept", "rmsnorm_forward", "rmsnorm_backward",
              "rmsnorm_backward_workspace", "linear_ce_forward", "linear_ce_backward",
-             "linear_ce_workspace")
+             "linear_ce_workspace", "Scaled", "add_rmsnorm_forward", "add_rmsnorm_backward",
+             "rotary_turns", "rotary_forward", "rotary_backward", "AdamWPlan", "adamw_step",
+             "adamw_report")
 
 
 def __getattr__(name):

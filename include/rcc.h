@@ -478,6 +478,94 @@ rcc_status rcc_rmsnorm_backward(const void* dy, rcc_dtype type, size_t ld_dy, co
                                 int accumulate, void* workspace, size_t workspace_bytes,
                                 rcc_stream_t stream);
 
+/* The norm with the residual's addition before it, and with its output in 8
+ * bits:
+ *   sum = x + residual, rounded once to `type`;  y = sum r weight with r =
+ *   1 / sqrt(mean(sum^2) + eps): the same bits as rcc_rmsnorm_forward's of sum.
+ * y_scales NULL: y is of `type`.  Else y is e4m3 (1 sign, 4 exponent and 3
+ * fraction bits, largest 448): for each group of 128 columns with a = max|y|,
+ *   y = the nearest e4m3 value, ties to even, of y * (448 * (1 / a)),
+ *   y_scales [tokens][G] = a * (1 / 448),
+ * every operation rounded to fp32; a group with a < 2^-120 is zeros with a scale
+ * of 0, one with a NaN or infinity zeros with a scale of NaN.
+ * residual and sum may be NULL together (with y_scales): nothing is added.
+ * sum may be x or residual itself where that is contiguous.  kept and scales, when not
+ * NULL, receive sum in 8 bits as rcc_rmsnorm_forward's. */
+rcc_status rcc_add_rmsnorm_forward(const void* x, size_t ld_x, const void* residual,
+                                   size_t ld_residual, rcc_dtype type, const float* weight,
+                                   float eps, size_t tokens, size_t dim, void* sum, void* y,
+                                   float* y_scales, int8_t* kept, float* scales,
+                                   rcc_stream_t stream);
+
+/* The gradient of x and of residual alike, which share one buffer:
+ *   dx = dsum + (rcc_rmsnorm_backward's dx of dy), rounded once, and its dweight,
+ * with dsum the gradient that reaches sum by its other uses (NULL: none).
+ * dx may be dsum itself where that is contiguous.  Workspace:
+ * rcc_rmsnorm_backward_workspace.  An 8-bit y passes dy on as y itself would. */
+rcc_status rcc_add_rmsnorm_backward(const void* dy, size_t ld_dy, const void* dsum,
+                                    size_t ld_dsum, rcc_dtype type, const int8_t* kept,
+                                    const float* scales, const float* weight, float eps,
+                                    size_t tokens, size_t dim, void* dx, float* dweight,
+                                    int accumulate, void* workspace, size_t workspace_bytes,
+                                    rcc_stream_t stream);
+
+/* ---- rotary positions
+ *
+ * A head's first 2 P elements are P pairs: elements i and i + P (RCC_ROTARY_HALF)
+ * or 2 i and 2 i + 1 (RCC_ROTARY_INTERLEAVED).  At position p pair i, (a, b),
+ * becomes (a c - b s, a s + b c) with c, s = scale * (cos, sin)(p f_i); what is
+ * past the pairs stays as it is.  Arithmetic is fp32, results are rounded once.
+ *
+ * turns[i] is f_i / (2 pi), a fraction of a turn, times 2^64: p turns[i] modulo
+ * 2^64 is the exact part of a turn that is left, so a far position costs no
+ * accuracy but that of turns[i] itself (p 2^-53 of f_i).
+ * rcc_rotary_turns fills it on the host (no CUDA call): f_i = base^(-i / P), and
+ *   RCC_ROTARY_LINEAR  f_i / factor
+ *   RCC_ROTARY_BASE    base factor^(P / (P - 1)) instead of base: the last pair
+ *                      is slowed down by factor, the first one not
+ *   RCC_ROTARY_PARTS   by the pair's turns n = length f_i / (2 pi) within the
+ *                      length that was trained on: f_i (k + (1 - k) / factor),
+ *                      k = (n - low) / (high - low) limited to [0, 1]. */
+typedef enum { RCC_ROTARY_HALF = 0, RCC_ROTARY_INTERLEAVED = 1 } rcc_rotary_layout;
+typedef enum {
+  RCC_ROTARY_NONE = 0,
+  RCC_ROTARY_LINEAR = 1,
+  RCC_ROTARY_BASE = 2,
+  RCC_ROTARY_PARTS = 3
+} rcc_rotary_kind;
+typedef struct {
+  rcc_rotary_kind kind;
+  double factor;            /* >= 1 */
+  double length, low, high; /* RCC_ROTARY_PARTS: length > 0, 0 <= low < high */
+} rcc_rotary_scaling;
+rcc_status rcc_rotary_turns(size_t pairs, double base, const rcc_rotary_scaling* scaling,
+                            uint64_t* turns);
+
+/* One of the matrices that a call turns: [tokens][heads][head_dim] in any order
+ * of the first two, a head's elements side by side. */
+typedef struct {
+  const void* in;
+  void* out;                    /* in itself (with its strides), or apart from every input */
+  size_t heads;
+  size_t in_token, in_head;     /* elements from a token, a head to the next */
+  size_t out_token, out_head;
+} rcc_rotary_rows;
+
+/* Turns q and, unless NULL, k (a part of the same packed rows, for instance),
+ * both of `type` and head_dim.  positions [tokens], NULL: 0, 1, ...; offset is
+ * added to each.  A position below 0 is padding: its rows are only scaled.  The
+ * backward pass turns the other way: gradients of the outputs in, of the inputs
+ * out.  tokens of any number; heads up to 65,536, head_dim up to 8,192. */
+rcc_status rcc_rotary_forward(const rcc_rotary_rows* q, const rcc_rotary_rows* k, rcc_dtype type,
+                              size_t tokens, size_t head_dim, const uint64_t* turns, size_t pairs,
+                              rcc_rotary_layout layout, const void* positions, rcc_index index,
+                              int64_t offset, float scale, rcc_stream_t stream);
+rcc_status rcc_rotary_backward(const rcc_rotary_rows* dq, const rcc_rotary_rows* dk,
+                               rcc_dtype type, size_t tokens, size_t head_dim,
+                               const uint64_t* turns, size_t pairs, rcc_rotary_layout layout,
+                               const void* positions, rcc_index index, int64_t offset,
+                               float scale, rcc_stream_t stream);
+
 /* With logits z = x w^T (x [tokens][dim] and w [vocab][dim] bf16, dim a
  * multiple of 8, buffers 16-byte aligned, row strides multiples of 8):
  *   lse[t] = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][labels[t]].
@@ -505,6 +593,81 @@ rcc_status rcc_linear_ce_backward(const void* x, size_t ld_x, const void* w, siz
                                   const float* dloss, size_t tokens, size_t vocab, size_t dim,
                                   void* dx, void* dw, rcc_dtype grad_type, int accumulate,
                                   void* workspace, size_t workspace_bytes, rcc_stream_t stream);
+
+/* ---- AdamW over many tensors -------------------------------------------------
+ *
+ * The optimizer step by itself, for gradients that are already one (the mean of
+ * the ranks', from rcc_reduce or of a single rank): every tensor in one call,
+ * fp32 or bf16 gradients, states in fp32 or in 8 bits, clipping and skipping
+ * decided on the GPU, so that nothing is read back and a step can be captured
+ * into a CUDA graph.  The pages have no counterpart to these calls.
+ *
+ * A plan holds the tensors' addresses.  rcc_adamw_create checks them, writes
+ * its tables into the caller's workspace (device memory, 256-byte aligned, at
+ * least rcc_adamw_workspace bytes, the plan's alone while it lives) with a copy
+ * on `stream`, which must not be capturing.  A step may run on any stream of that
+ * device once the copy is done; steps of one plan, and the reads of its status,
+ * follow one another.  rcc_adamw_destroy ends the plan: work enqueued earlier, and
+ * graphs that captured it, need only the workspace and the tensors. */
+typedef struct {
+  size_t numel;          /* > 0, at most 2^40 */
+  const void* grad;      /* of grad_type; read only */
+  rcc_dtype grad_type;
+  float* param;          /* fp32 master parameters */
+  void* exp_avg;         /* m: fp32, or with scales e4m3 [numel] */
+  void* exp_avg_sq;      /* v: fp32, or with scales sqrt(v) as e4m3 [numel] */
+  float* exp_avg_scale;  /* [ceil(numel / 128)] each, for 8-bit states; or NULL, both of */
+  float* exp_avg_sq_scale; /* every tensor of a plan */
+  void* copy;            /* receives the new parameters in bf16 [numel]; or NULL */
+} rcc_adamw_tensor;
+
+/* The workspace begins with it; a step writes it. */
+typedef struct {
+  int64_t step;          /* steps taken (skipped ones do not count) */
+  double grad_norm;      /* L2 norm of all unscaled gradients */
+  double beta1_power;    /* beta1^step, beta2^step: products of the steps' betas */
+  double beta2_power;
+  uint32_t nonfinite;    /* gradient elements that are not finite */
+  int32_t skipped;       /* 1: the last step changed nothing */
+  float clip_coef;       /* what it multiplied the gradients by (1: not clipped) */
+  uint32_t unused;
+} rcc_adamw_status;
+
+typedef struct rcc_adamw_s* rcc_adamw;
+
+/* 0 for tensors that rcc_adamw_create refuses by their number or sizes. */
+size_t rcc_adamw_workspace(const rcc_adamw_tensor* tensors, int num_tensors);
+
+/* `step`: steps that the states have behind them, with the betas given.  `seed`:
+ * of the 8-bit states' rounding.  No buffer that a step writes (parameters,
+ * states, scales, copies, workspace) may overlap another one. */
+rcc_status rcc_adamw_create(const rcc_adamw_tensor* tensors, int num_tensors, uint32_t seed,
+                            int64_t step, double beta1, double beta2, void* workspace,
+                            size_t workspace_bytes, rcc_stream_t stream, rcc_adamw* out);
+
+/* One step over all tensors, in fp32, every operation rounded:
+ *   g = grad * fl32(1 / scale); norm = sqrt(sum g^2) (fp64); a gradient or norm
+ *   that is not finite: nothing changes but the status;
+ *   t = step + 1, g' = g * coef, coef = max_grad_norm / norm where 0 <
+ *   max_grad_norm < norm, else 1, and then rcc_grad_sync_adamw's update.
+ * Of cfg lr, beta1, beta2, eps, weight_decay and max_grad_norm count; replicas
+ * must be 1 and flags 0.
+ *
+ * 8-bit states: m and u = sqrt(v) of 128 neighbours share a scale, the smallest
+ * power of two s with max <= 448 s (0 where the max is below 2^-100, and the
+ * group is then held as zeros); they are held as |x| / s on the grid of e4m3,
+ * saturating at 448, the value above with the chance of the distance from the
+ * one below in sixteen-bit steps, which keeps small changes of a moment on
+ * average; a u > 0 is held as 2^-9 at least.  m / sqrt(v) of this step is taken
+ * before they are rounded.  The sixteen bits are, for elements 2 j and 2 j + 1
+ * of a tensor's 4,096, c-th block, the lower and upper half of
+ *   h(h(h(h(seed ^ h(step)) + tensor * 0x9E3779B9) ^ c) + j)
+ * in 32 bits with step the steps taken before and h(x): x ^= x >> 16; x *=
+ * 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^ (x >> 16). */
+rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale,
+                          rcc_stream_t stream);
+
+rcc_status rcc_adamw_destroy(rcc_adamw plan);
 
 /* ---- diagnostics ---------------------------------------------------------- */
 
