@@ -58,28 +58,121 @@ __device__ __forceinline__ float grad_at(const AdamWTensor& t, uint64_t i) {
                 : static_cast<const float*>(t.grad)[i];
 }
 
-// Simplest form: fp64 sums.
-__global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const AdamWArgs a) {
-  pdl_wait_then_release();
-  uint64_t lo, hi;
-  range_of(a.num_items, lo, hi);
+// A thread's sum of squares as a value and the error it has run up, two of each:
+// sum' = fl(sum + g^2) is one fused operation, and what it dropped is exact but
+// for u^2 of it, so n squares are good to n 2^-48, without GB300's few fp64
+// units.  Seven instructions for two elements.
+struct Squares {
+  float2 sum = both(0.f), rest = both(0.f);
+  uint32_t seen = 0;  // bits of the elements but their signs
+  __device__ __forceinline__ void add(float2 g) {
+    const float2 t = fma2(g, g, sum);
+    const float2 d = add2(t, neg(sum));  // near g^2
+    const float2 of_sum = add2(sum, neg(add2(t, neg(d))));
+    rest = add2(rest, add2(of_sum, fma2(g, g, neg(d))));
+    sum = t;
+  }
+  static __device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
+  // Neither overflown nor among the smallest numbers, where errors are lost
+  __device__ __forceinline__ bool sound() const {
+    const float s = sum.x + sum.y;
+    return seen == 0 || (s > 0x1p-60f && s < 0x1p100f);
+  }
+  __device__ __forceinline__ double value() const {
+    return ((double)sum.x + (double)rest.x) + ((double)sum.y + (double)rest.y);
+  }
+};
+
+// fp64, for gradients that Squares cannot sum; counts what is not finite
+struct WideSquares {
   double sum = 0.0;
   uint32_t bad = 0;
-  for (uint64_t item = lo; item < hi; ++item) {
-    const AdamWItem it = a.items[item];
-    const AdamWTensor t = a.tensors[it.tensor];
-    const uint64_t first = (uint64_t)it.chunk * kAdamWItem;
-    const uint64_t end = min(first + kAdamWItem, t.numel);
-    for (uint64_t i = first + threadIdx.x; i < end; i += kThreads) {
-      const float g = grad_at(t, i);
-      if (fabsf(g) < INFINITY)
-        sum += (double)g * (double)g;
-      else
-        ++bad;
-    }
+  __device__ __forceinline__ void add(float g) {
+    if (!(fabsf(g) < INFINITY))
+      ++bad;
+    else if (g != 0.f)
+      sum += (double)g * (double)g;
   }
-  __shared__ double sums[kThreads / 32];
-  __shared__ uint32_t bads[kThreads / 32];
+};
+
+// Eight gradients as they lie in memory
+struct Raw {
+  uint32_t w[8];
+};
+__device__ __forceinline__ void load_raw(const AdamWTensor& t, uint64_t i, Raw& r) {
+  if (t.bf16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.grad) + i);
+    r.w[0] = v.x;
+    r.w[1] = v.y;
+    r.w[2] = v.z;
+    r.w[3] = v.w;
+  } else {
+    float f[8];
+    load8(static_cast<const float*>(t.grad) + i, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.w[e] = __float_as_uint(f[e]);
+  }
+}
+__device__ __forceinline__ float2 pair_of(const AdamWTensor& t, const Raw& r, int i) {
+  if (!t.bf16) return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+  float2 v;
+  widen2(r.w[i], v.x, v.y);
+  return v;
+}
+
+// Elements [begin, end) of a tensor, begin on a whole item
+__device__ __forceinline__ void add_range(const AdamWTensor& t, uint64_t begin, uint64_t end,
+                                          Squares& s) {
+  constexpr int kAhead = 4;  // vectors of a thread under way
+  uint64_t from = begin;
+  if (t.vec) {
+    const uint64_t vectors = (end - begin) / kUnit;
+    for (uint64_t v = threadIdx.x; v < vectors; v += kAhead * kThreads) {
+      Raw r[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (v + k * kThreads < vectors) load_raw(t, begin + (v + k * kThreads) * kUnit, r[k]);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (v + k * kThreads >= vectors) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s.seen |= t.bf16 ? r[k].w[i] & 0x7FFF7FFFu
+                           : (r[k].w[2 * i] | r[k].w[2 * i + 1]) & 0x7FFFFFFFu;
+          s.add(pair_of(t, r[k], i));
+        }
+      }
+    }
+    from = begin + vectors * kUnit;
+  }
+  for (uint64_t i = from + threadIdx.x; i < end; i += kThreads) {
+    const float g = grad_at(t, i);
+    s.seen |= __float_as_uint(g) & 0x7FFFFFFFu;
+    s.add(make_float2(g, 0.f));
+  }
+}
+
+// The tensors' pieces within the block's items, one after the other
+template <typename F>
+__device__ __forceinline__ void for_each_range(const AdamWArgs& a, F f) {
+  uint64_t lo, hi;
+  range_of(a.num_items, lo, hi);
+  AdamWItem it = a.items[lo];
+  while (lo < hi) {
+    const AdamWTensor t = a.tensors[it.tensor];
+    const uint64_t begin = (uint64_t)it.chunk * kAdamWItem;
+    const uint64_t left = (t.numel - begin + kAdamWItem - 1) / kAdamWItem;  // items of the tensor
+    const uint64_t take = min(left, hi - lo);
+    f(t, begin, min(begin + take * kAdamWItem, t.numel));
+    lo += take;
+    it = {it.tensor + 1, 0};
+  }
+}
+
+// Sums over the block, for thread 0; `sums` and `bads` are free again after the
+// next barrier
+__device__ __forceinline__ void block_sum(double& sum, unsigned long long& bad, double* sums,
+                                          unsigned long long* bads) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -91,36 +184,16 @@ __global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const AdamWArgs a)
   }
   __syncthreads();
   if (threadIdx.x == 0) {
+#pragma unroll
     for (int w = 1; w < kThreads / 32; ++w) {
       sum += sums[w];
       bad += bads[w];
     }
-    a.rows[blockIdx.x] = {sum, bad, 0u};
   }
 }
 
-// ---- the decision ---------------------------------------------------------------
-
-// One block: the rows' sum in a fixed order, then whether and how the step is
-// taken.
-__global__ void __launch_bounds__(kThreads) adamw_decide_kernel(const AdamWArgs a, uint32_t rows) {
-  pdl_wait_then_release();
-  __shared__ double sums[kThreads];
-  __shared__ unsigned long long bads[kThreads];
-  double sum = 0.0;
-  unsigned long long bad = 0;
-  for (uint32_t r = threadIdx.x; r < rows; r += kThreads) {
-    sum += a.rows[r].sum;
-    bad += a.rows[r].bad;
-  }
-  sums[threadIdx.x] = sum;
-  bads[threadIdx.x] = bad;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int i = 1; i < kThreads; ++i) {
-    sum += sums[i];
-    bad += bads[i];
-  }
+// Whether and how the step is taken: one thread, once a step
+__device__ __forceinline__ void decide(const AdamWArgs& a, double sum, unsigned long long bad) {
   rcc_adamw_status s = *a.status;
   AdamWDecision d = {};
   const double norm = sqrt(sum) / a.scale;
@@ -140,6 +213,57 @@ __global__ void __launch_bounds__(kThreads) adamw_decide_kernel(const AdamWArgs 
   }
   *a.status = s;
   *a.decision = d;
+}
+
+// Each block leaves one row; the last one to do so adds them up, in the rows'
+// order, and decides.
+__global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const AdamWArgs a) {
+  __shared__ double sums[kThreads / 32];
+  __shared__ unsigned long long bads[kThreads / 32];
+  __shared__ bool last;
+  pdl_wait_then_release();
+  Squares s;
+  for_each_range(a, [&](const AdamWTensor& t, uint64_t begin, uint64_t end) {
+    add_range(t, begin, end, s);
+  });
+  double sum = s.value();
+  unsigned long long bad = 0;
+  if (!s.sound()) {
+    WideSquares w;
+    for_each_range(a, [&](const AdamWTensor& t, uint64_t begin, uint64_t end) {
+      // the same elements of this thread
+      uint64_t from = begin;
+      if (t.vec) {
+        const uint64_t vectors = (end - begin) / kUnit;
+        for (uint64_t v = threadIdx.x; v < vectors; v += kThreads)
+          for (int e = 0; e < kUnit; ++e) w.add(grad_at(t, begin + v * kUnit + e));
+        from = begin + vectors * kUnit;
+      }
+      for (uint64_t i = from + threadIdx.x; i < end; i += kThreads) w.add(grad_at(t, i));
+    });
+    sum = w.sum;
+    bad = w.bad;
+  }
+  block_sum(sum, bad, sums, bads);
+  if (threadIdx.x == 0) {
+    a.rows[blockIdx.x] = {sum, (uint32_t)min(bad, 0xFFFFFFFFull), 0u};
+    __threadfence();
+    last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  sum = 0.0;
+  bad = 0;
+  for (uint32_t r = threadIdx.x; r < gridDim.x; r += kThreads) {
+    sum += __ldcg(&a.rows[r].sum);
+    bad += __ldcg(&a.rows[r].bad);
+  }
+  block_sum(sum, bad, sums, bads);
+  if (threadIdx.x == 0) {
+    *a.arrived = 0;
+    decide(a, sum, bad);
+  }
 }
 
 // ---- the update -----------------------------------------------------------------
@@ -354,11 +478,9 @@ cudaError_t launch_adamw(const AdamWArgs& a, bool eight, cudaStream_t stream,
   const unsigned blocks = (unsigned)(a.num_items < fill ? a.num_items : fill);
   cudaError_t e = launch_kernel(adamw_norm_kernel, dim3(blocks), dim3(kThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(adamw_decide_kernel, dim3(1), dim3(kThreads), 0, stream, a, blocks);
-  if (e != cudaSuccess) return e;
   e = launch_kernel(eight ? adamw_update_kernel<true> : adamw_update_kernel<false>, dim3(blocks),
                     dim3(kThreads), 0, stream, a);
-  if (e == cudaSuccess) *launches = 3;
+  if (e == cudaSuccess) *launches = 2;
   return e;
 }
 

@@ -149,6 +149,7 @@ struct AdamWArgs {
   AdamWRow* rows;
   rcc_adamw_status* status;
   AdamWDecision* decision;
+  uint32_t* arrived;          // blocks whose row is written; 0 between steps
   uint64_t num_items;
   int num_rows;               // room for so many
   uint32_t seed;

@@ -3,7 +3,8 @@
 //
 // A plan is checked once, where it is made; a step checks its numbers alone and
 // launches.  The workspace holds, each on a boundary of 256 bytes: the status
-// with the decision behind it, the norm's rows, the tensors, the items.
+// with the decision and a counter behind it, the norm's rows, the tensors, the
+// items.
 #include <new>
 #include <unordered_map>
 
@@ -30,11 +31,11 @@ std::mutex g_plans_mu;
 std::unordered_map<uintptr_t, Plan> g_plans;
 uintptr_t g_next_plan = 0;
 
-constexpr size_t kDecisionAt = 64, kRowsAt = 256;
+constexpr size_t kDecisionAt = 64, kArrivedAt = 128, kRowsAt = 256;
 constexpr size_t kMaxNumel = size_t{1} << 40;
 constexpr uint64_t kMaxItems = 0x7FFFFFFF;
 static_assert(sizeof(rcc_adamw_status) <= kDecisionAt &&
-                  kDecisionAt + sizeof(AdamWDecision) <= kRowsAt,
+                  kDecisionAt + sizeof(AdamWDecision) <= kArrivedAt,
               "status and decision share the first 256 bytes");
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -243,6 +244,7 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   a.rows = reinterpret_cast<AdamWRow*>(p.workspace + kRowsAt);
   a.status = reinterpret_cast<rcc_adamw_status*>(p.workspace);
   a.decision = reinterpret_cast<AdamWDecision*>(p.workspace + kDecisionAt);
+  a.arrived = reinterpret_cast<uint32_t*>(p.workspace + kArrivedAt);
   a.num_items = p.items;
   a.num_rows = p.rows;
   a.seed = p.seed;
