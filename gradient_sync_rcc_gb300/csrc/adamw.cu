@@ -26,6 +26,12 @@ namespace rcc {
 namespace lm {
 namespace {
 
+#ifndef NORM_AHEAD
+#define NORM_AHEAD 2
+#define NORM_PER_SM 4
+#define UPD_AHEAD 1
+#define UPD_PER_SM 4
+#endif
 constexpr int kThreads = 256;
 constexpr int kUnit = 8;                             // elements of a thread at a time
 constexpr int kUnits = kAdamWItem / (kThreads * kUnit);  // of them in an item
@@ -96,53 +102,65 @@ struct WideSquares {
 };
 
 // Eight gradients as they lie in memory
+template <bool BF16>
 struct Raw {
-  uint32_t w[8];
+  static constexpr int kWords = BF16 ? 4 : 8;
+  uint32_t w[kWords];
 };
-__device__ __forceinline__ void load_raw(const AdamWTensor& t, uint64_t i, Raw& r) {
-  if (t.bf16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.grad) + i);
-    r.w[0] = v.x;
-    r.w[1] = v.y;
-    r.w[2] = v.z;
-    r.w[3] = v.w;
-  } else {
-    float f[8];
-    load8(static_cast<const float*>(t.grad) + i, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r.w[e] = __float_as_uint(f[e]);
-  }
+__device__ __forceinline__ void load_raw(const void* grad, uint64_t i, Raw<true>& r) {
+  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(grad) + i);
+  r.w[0] = v.x;
+  r.w[1] = v.y;
+  r.w[2] = v.z;
+  r.w[3] = v.w;
 }
-__device__ __forceinline__ float2 pair_of(const AdamWTensor& t, const Raw& r, int i) {
-  if (!t.bf16) return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+__device__ __forceinline__ void load_raw(const void* grad, uint64_t i, Raw<false>& r) {
+  float f[8];
+  load8(static_cast<const float*>(grad) + i, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r.w[e] = __float_as_uint(f[e]);
+}
+__device__ __forceinline__ float2 pair_of(const Raw<true>& r, int i) {
   float2 v;
   widen2(r.w[i], v.x, v.y);
   return v;
 }
+__device__ __forceinline__ float2 pair_of(const Raw<false>& r, int i) {
+  return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+}
 
 // Elements [begin, end) of a tensor, begin on a whole item
+template <bool BF16>
+__device__ __forceinline__ void add_vectors(const void* grad, uint64_t begin, uint64_t vectors,
+                                            Squares& s) {
+  constexpr int kAhead = BF16 ? 2 * NORM_AHEAD : NORM_AHEAD;  // vectors of a thread under way
+  for (uint64_t v = threadIdx.x; v < vectors; v += kAhead * kThreads) {
+    Raw<BF16> r[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+      for (int e = 0; e < Raw<BF16>::kWords; ++e) r[k].w[e] = 0u;
+      if (v + k * kThreads < vectors) load_raw(grad, begin + (v + k * kThreads) * kUnit, r[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+      for (int e = 0; e < Raw<BF16>::kWords; ++e)
+        s.seen |= r[k].w[e] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s.add(pair_of(r[k], i));
+    }
+  }
+}
 __device__ __forceinline__ void add_range(const AdamWTensor& t, uint64_t begin, uint64_t end,
                                           Squares& s) {
-  constexpr int kAhead = 4;  // vectors of a thread under way
   uint64_t from = begin;
   if (t.vec) {
     const uint64_t vectors = (end - begin) / kUnit;
-    for (uint64_t v = threadIdx.x; v < vectors; v += kAhead * kThreads) {
-      Raw r[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (v + k * kThreads < vectors) load_raw(t, begin + (v + k * kThreads) * kUnit, r[k]);
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (v + k * kThreads >= vectors) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s.seen |= t.bf16 ? r[k].w[i] & 0x7FFF7FFFu
-                           : (r[k].w[2 * i] | r[k].w[2 * i + 1]) & 0x7FFFFFFFu;
-          s.add(pair_of(t, r[k], i));
-        }
-      }
-    }
+    if (t.bf16)
+      add_vectors<true>(t.grad, begin, vectors, s);
+    else
+      add_vectors<false>(t.grad, begin, vectors, s);
     from = begin + vectors * kUnit;
   }
   for (uint64_t i = from + threadIdx.x; i < end; i += kThreads) {
@@ -208,6 +226,7 @@ __device__ __forceinline__ void decide(const AdamWArgs& a, double sum, unsigned 
     s.step += 1;
     s.beta1_power *= a.beta1;
     s.beta2_power *= a.beta2;
+    d.factor = (float)((double)d.coef / a.scale);
     d.step_size = (float)(a.lr / (1.0 - s.beta1_power));
     d.inv_root = (float)(1.0 / sqrt(1.0 - s.beta2_power));
   }
@@ -217,7 +236,7 @@ __device__ __forceinline__ void decide(const AdamWArgs& a, double sum, unsigned 
 
 // Each block leaves one row; the last one to do so adds them up, in the rows'
 // order, and decides.
-__global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, NORM_PER_SM) adamw_norm_kernel(const AdamWArgs a) {
   __shared__ double sums[kThreads / 32];
   __shared__ unsigned long long bads[kThreads / 32];
   __shared__ bool last;
@@ -268,27 +287,34 @@ __global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const AdamWArgs a)
 
 // ---- the update -----------------------------------------------------------------
 
+// Eight neighbours as they lie in memory, and their group's scales
+template <bool EIGHT, bool BF16>
 struct Unit {
-  float g[kUnit], p[kUnit], m[kUnit], v[kUnit];
+  Raw<BF16> g;
+  float p[kUnit];
+  float m[EIGHT ? 1 : kUnit], v[EIGHT ? 1 : kUnit];
+  uint2 m8, v8;
+  float ms, vs;
 };
 
-__device__ __forceinline__ void widen_e4m3(uint2 q, float (&v)[kUnit]) {
+__device__ __forceinline__ void widen_e4m3(uint2 q, float2 (&v)[4]) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t h;  // two halves: e4m3 is exact in them
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i % 2)))));
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
-        "cvt.f32.f16 %1, b;\n\t}" : "=f"(v[2 * i]), "=f"(v[2 * i + 1]) : "r"(h));
+        "cvt.f32.f16 %1, b;\n\t}" : "=f"(v[i].x), "=f"(v[i].y) : "r"(h));
   }
 }
-__device__ __forceinline__ uint2 narrow_e4m3(const float (&v)[kUnit]) {
+__device__ __forceinline__ uint2 narrow_e4m3(const float2 (&v)[4]) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * i + 1]), "f"(v[4 * i]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * i + 3]), "f"(v[4 * i + 2]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[2 * i].y), "f"(v[2 * i].x));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(hi) : "f"(v[2 * i + 1].y), "f"(v[2 * i + 1].x));
     w[i] = lo | (uint32_t)hi << 16;
   }
   return make_uint2(w[0], w[1]);
@@ -305,62 +331,73 @@ __device__ __forceinline__ float power_for(uint32_t top_bits) {
 }
 
 // y >= 0 on the grid of e4m3, up with a chance of its distance over a step:
-// `number` of 2^16.  Below 2^-6 the grid is even, as it is from 2^-6 to 2^-5.
-__device__ __forceinline__ float round_e4m3(float y, uint32_t number) {
+// `chance`, of 2^20.  Below 2^-6 the grid is even, as it is from 2^-6 to 2^-5.
+// Over 448 is left to the conversion, which saturates.
+__device__ __forceinline__ float round_e4m3(float y, uint32_t chance) {
   const float low = y < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t b = (__float_as_uint(__fadd_rn(y, low)) + (number << 4)) & 0xFFF00000u;
-  return fminf(__uint_as_float(b) - low, 448.f);
+  const uint32_t b = (__float_as_uint(__fadd_rn(y, low)) + chance) & 0xFFF00000u;
+  return __fsub_rn(__uint_as_float(b), low);
 }
 
-// The largest of the 16 threads of a group, as bits: a NaN is the largest of all
-__device__ __forceinline__ uint32_t group_max(uint32_t bits) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1)
-    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
-  return bits;
-}
-
-// Values to hold: |v| by their scale, rounded, with their sign
+// What eight values of a group are held as, and its scale
 template <bool ROOT>
-__device__ __forceinline__ float hold(float (&v)[kUnit], const uint32_t (&numbers)[kUnit]) {
+__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&chance)[kUnit],
+                                      float& scale) {
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < kUnit; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-  const float scale = power_for(group_max(top));
+  for (int i = 0; i < 4; ++i)
+    top = max(max(top, __float_as_uint(v[i].x) & 0x7FFFFFFFu), __float_as_uint(v[i].y) & 0x7FFFFFFFu);
+  // over the 16 threads of a group; a NaN's bits are the largest of all
+  top = __reduce_max_sync(threadIdx.x & 16 ? 0xFFFF0000u : 0x0000FFFFu, top);
+  scale = power_for(top);
   const float inv = scale > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(scale)) : 0.f;
+  float2 w[4];
 #pragma unroll
-  for (int e = 0; e < kUnit; ++e) {
-    const float y = fabsf(v[e]) * inv;
-    float w = round_e4m3(y, numbers[e]);
-    if (ROOT) w = y > 0.f ? fmaxf(w, 0x1p-9f) : 0.f;
-    v[e] = copysignf(w, v[e]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = mul2(v[i], both(inv));
+    w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), chance[2 * i]);
+    w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), chance[2 * i + 1]);
+    if (ROOT) {
+      if (y.x > 0.f) w[i].x = fmaxf(w[i].x, 0x1p-9f);
+      if (y.y > 0.f) w[i].y = fmaxf(w[i].y, 0x1p-9f);
+    } else {
+      w[i] = make_float2(copysignf(w[i].x, y.x), copysignf(w[i].y, y.y));
+    }
   }
-  return scale;
+  return narrow_e4m3(w);
 }
 
 // Up to eight elements from the i-th on; zeros past the tensor
-template <bool EIGHT>
-__device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i, bool whole, Unit& u) {
-  if (whole) {
-    if (t.bf16)
-      load8(static_cast<const __nv_bfloat16*>(t.grad) + i, u.g);
-    else
-      load8(static_cast<const float*>(t.grad) + i, u.g);
+template <bool EIGHT, bool BF16>
+__device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i,
+                                          Unit<EIGHT, BF16>& u) {
+  if constexpr (EIGHT) {
+    const bool live = i < t.numel;
+    u.ms = live ? t.m_scales[i / kGroup] : 0.f;
+    u.vs = live ? t.v_scales[i / kGroup] : 0.f;
+  }
+  if (t.vec && i + kUnit <= t.numel) {
+    load_raw(t.grad, i, u.g);
     load8(t.param + i, u.p);
     if constexpr (EIGHT) {
-      widen_e4m3(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i), u.m);
-      widen_e4m3(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i), u.v);
+      u.m8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
+      u.v8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
     } else {
       load8(static_cast<const float*>(t.m) + i, u.m);
       load8(static_cast<const float*>(t.v) + i, u.v);
     }
     return;
   }
+#pragma unroll
+  for (int e = 0; e < Raw<BF16>::kWords; ++e) u.g.w[e] = 0u;
   uint32_t q[2][2] = {};
 #pragma unroll
   for (int e = 0; e < kUnit; ++e) {
     const bool live = i + e < t.numel;
-    u.g[e] = live ? grad_at(t, i + e) : 0.f;
+    if constexpr (BF16)
+      u.g.w[e / 2] |= (live ? static_cast<const uint16_t*>(t.grad)[i + e] : 0u) << (16 * (e % 2));
+    else
+      u.g.w[e] = live ? static_cast<const uint32_t*>(t.grad)[i + e] : 0u;
     u.p[e] = live ? t.param[i + e] : 0.f;
     if constexpr (EIGHT) {
       q[0][e / 4] |= (live ? static_cast<const uint8_t*>(t.m)[i + e] : 0u) << (8 * (e % 4));
@@ -371,25 +408,26 @@ __device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i, bool
     }
   }
   if constexpr (EIGHT) {
-    widen_e4m3(make_uint2(q[0][0], q[0][1]), u.m);
-    widen_e4m3(make_uint2(q[1][0], q[1][1]), u.v);
+    u.m8 = make_uint2(q[0][0], q[0][1]);
+    u.v8 = make_uint2(q[1][0], q[1][1]);
   }
 }
 
-template <bool EIGHT>
-__device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i, bool whole,
-                                           const Unit& u) {
-  uint2 m8 = {}, v8 = {};
+template <bool EIGHT, bool BF16>
+__device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i,
+                                           const Unit<EIGHT, BF16>& u) {
   if constexpr (EIGHT) {
-    m8 = narrow_e4m3(u.m);
-    v8 = narrow_e4m3(u.v);
+    if (threadIdx.x % kLanes == 0 && i < t.numel) {
+      t.m_scales[i / kGroup] = u.ms;
+      t.v_scales[i / kGroup] = u.vs;
+    }
   }
-  if (whole) {
+  if (t.vec && i + kUnit <= t.numel) {
     store8(t.param + i, u.p);
     if (t.copy) store8(t.copy + i, u.p);
     if constexpr (EIGHT) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = m8;
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = v8;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = u.m8;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = u.v8;
     } else {
       store8(static_cast<float*>(t.m) + i, u.m);
       store8(static_cast<float*>(t.v) + i, u.v);
@@ -402,8 +440,8 @@ __device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i, boo
     t.param[i + e] = u.p[e];
     if (t.copy) from_f32(u.p[e], t.copy[i + e]);
     if constexpr (EIGHT) {
-      static_cast<uint8_t*>(t.m)[i + e] = (uint8_t)((e < 4 ? m8.x : m8.y) >> (8 * (e % 4)));
-      static_cast<uint8_t*>(t.v)[i + e] = (uint8_t)((e < 4 ? v8.x : v8.y) >> (8 * (e % 4)));
+      static_cast<uint8_t*>(t.m)[i + e] = (uint8_t)((e < 4 ? u.m8.x : u.m8.y) >> (8 * (e % 4)));
+      static_cast<uint8_t*>(t.v)[i + e] = (uint8_t)((e < 4 ? u.v8.x : u.v8.y) >> (8 * (e % 4)));
     } else {
       static_cast<float*>(t.m)[i + e] = u.m[e];
       static_cast<float*>(t.v)[i + e] = u.v[e];
@@ -411,62 +449,108 @@ __device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i, boo
   }
 }
 
+// fp32 states: every operation rounded, as rcc_grad_sync_adamw's update
+template <bool BF16>
+__device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecision& d,
+                                            uint32_t, Unit<false, BF16>& u) {
+#pragma unroll
+  for (int e = 0; e < kUnit; ++e) {
+    const float2 two = pair_of(u.g, e / 2);
+    const float g = __fmul_rn(__fmul_rn(e % 2 ? two.y : two.x, a.inv_scale), d.coef);
+    const float m = __fadd_rn(__fmul_rn(a.b1, u.m[e]), __fmul_rn(a.one_minus_b1, g));
+    const float v = __fadd_rn(__fmul_rn(a.b2, u.v[e]), __fmul_rn(a.one_minus_b2, __fmul_rn(g, g)));
+    const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v), d.inv_root), a.eps);
+    u.p[e] = __fsub_rn(__fmul_rn(u.p[e], a.decay), __fmul_rn(d.step_size, __fdiv_rn(m, denom)));
+    u.m[e] = m;
+    u.v[e] = v;
+  }
+}
+
+__device__ __forceinline__ float root_of(float v) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float inverse_of(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// 8-bit states: two elements an operation, products fused into sums, root and
+// quotient to 2^-22: what is held keeps four bits of it.
+template <bool BF16>
+__device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecision& d,
+                                            uint32_t first, Unit<true, BF16>& u) {
+  float2 m[4], v[4];
+  widen_e4m3(u.m8, m);
+  widen_e4m3(u.v8, v);
+  uint32_t chance[kUnit];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 g = mul2(pair_of(u.g, i), both(d.factor));
+    m[i] = fma2(m[i], both(u.ms * a.b1), mul2(g, both(a.one_minus_b1)));
+    const float2 root = mul2(v[i], both(u.vs));
+    v[i] = fma2(mul2(root, root), both(a.b2), mul2(mul2(g, g), both(a.one_minus_b2)));
+    v[i] = make_float2(root_of(v[i].x), root_of(v[i].y));
+    const float2 denom = fma2(v[i], both(d.inv_root), both(a.eps));
+    const float2 change = mul2(m[i], make_float2(inverse_of(denom.x), inverse_of(denom.y)));
+    const float2 p = fma2(change, both(-d.step_size),
+                          mul2(make_float2(u.p[2 * i], u.p[2 * i + 1]), both(a.decay)));
+    u.p[2 * i] = p.x;
+    u.p[2 * i + 1] = p.y;
+    const uint32_t h = mix(first + i);
+    chance[2 * i] = (h & 0xFFFFu) << 4;
+    chance[2 * i + 1] = h >> 16 << 4;
+  }
+  u.m8 = hold<false>(m, chance, u.ms);
+  u.v8 = hold<true>(v, chance, u.vs);
+}
+
+template <bool EIGHT, bool BF16>
+__device__ __forceinline__ void update_item(const AdamWArgs& a, const AdamWDecision& d,
+                                            const AdamWTensor& t, uint32_t chunk, uint32_t key) {
+  const uint64_t i = (uint64_t)chunk * kAdamWItem + threadIdx.x * kUnit;
+#pragma unroll 1
+  for (int k0 = 0; k0 < kUnits; k0 += UPD_AHEAD) {
+    Unit<EIGHT, BF16> u[UPD_AHEAD];
+#pragma unroll
+    for (int k = 0; k < UPD_AHEAD; ++k) load_unit(t, i + (k0 + k) * kThreads * kUnit, u[k]);
+#pragma unroll
+    for (int k = 0; k < UPD_AHEAD; ++k) {
+      update_unit(a, d, key + ((k0 + k) * kThreads + threadIdx.x) * (kUnit / 2), u[k]);
+      store_unit(t, i + (k0 + k) * kThreads * kUnit, u[k]);
+    }
+  }
+}
+
 template <bool EIGHT>
-__global__ void __launch_bounds__(kThreads) adamw_update_kernel(const AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, UPD_PER_SM) adamw_update_kernel(const AdamWArgs a) {
+  __shared__ AdamWTensor t;
   pdl_wait_then_release();
   const AdamWDecision d = *a.decision;
   if (d.skip) return;
   uint64_t lo, hi;
   range_of(a.num_items, lo, hi);
-  const uint32_t key = mix(a.seed ^ mix(d.step));
+  const uint32_t step_key = mix(a.seed ^ mix(d.step));
+  AdamWItem next = a.items[hi - 1];
+  uint32_t tensor = ~0u;
   for (uint64_t item = hi; item-- > lo;) {
-    const AdamWItem it = a.items[item];
-    const AdamWTensor t = a.tensors[it.tensor];
-    const uint32_t block_key = mix(mix(key + it.tensor * kGolden) ^ it.chunk);
-    for (int k = 0; k < kUnits; ++k) {
-      const uint32_t inside = (k * kThreads + threadIdx.x) * kUnit;
-      const uint64_t i = (uint64_t)it.chunk * kAdamWItem + inside;
-      const bool whole = t.vec && i + kUnit <= t.numel;
-      Unit u;
-      load_unit<EIGHT>(t, i, whole, u);
-      if constexpr (EIGHT) {
-        const bool live = i < t.numel;
-        const float ms = live ? t.m_scales[i / kGroup] : 0.f;
-        const float vs = live ? t.v_scales[i / kGroup] : 0.f;
-#pragma unroll
-        for (int e = 0; e < kUnit; ++e) {
-          u.m[e] = __fmul_rn(u.m[e], ms);
-          u.v[e] = __fmul_rn(u.v[e], vs);
-          u.v[e] = __fmul_rn(u.v[e], u.v[e]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < kUnit; ++e) {
-        const float g = __fmul_rn(__fmul_rn(u.g[e], a.inv_scale), d.coef);
-        u.m[e] = __fadd_rn(__fmul_rn(a.b1, u.m[e]), __fmul_rn(a.one_minus_b1, g));
-        u.v[e] = __fadd_rn(__fmul_rn(a.b2, u.v[e]), __fmul_rn(a.one_minus_b2, __fmul_rn(g, g)));
-        const float root = __fsqrt_rn(u.v[e]);
-        const float denom = __fadd_rn(__fmul_rn(root, d.inv_root), a.eps);
-        u.p[e] = __fsub_rn(__fmul_rn(u.p[e], a.decay),
-                           __fmul_rn(d.step_size, __fdiv_rn(u.m[e], denom)));
-        if (EIGHT) u.v[e] = root;
-      }
-      if constexpr (EIGHT) {
-        uint32_t numbers[kUnit];
-#pragma unroll
-        for (int e = 0; e < kUnit; e += 2) {
-          const uint32_t h = mix(block_key + (inside + e) / 2);
-          numbers[e] = h & 0xFFFFu;
-          numbers[e + 1] = h >> 16;
-        }
-        const float ms = hold<false>(u.m, numbers), vs = hold<true>(u.v, numbers);
-        if (threadIdx.x % kLanes == 0 && i < t.numel) {
-          t.m_scales[i / kGroup] = ms;
-          t.v_scales[i / kGroup] = vs;
-        }
-      }
-      store_unit<EIGHT>(t, i, whole, u);
+    const AdamWItem it = next;
+    if (item > lo) next = a.items[item - 1];
+    if (it.tensor != tensor) {
+      __syncthreads();
+      tensor = it.tensor;
+      if (threadIdx.x < sizeof(AdamWTensor) / 8)
+        reinterpret_cast<uint64_t*>(&t)[threadIdx.x] =
+            reinterpret_cast<const uint64_t*>(a.tensors + tensor)[threadIdx.x];
+      __syncthreads();
     }
+    const uint32_t key = mix(mix(step_key + tensor * kGolden) ^ it.chunk);
+    if (t.bf16)
+      update_item<EIGHT, true>(a, d, t, it.chunk, key);
+    else
+      update_item<EIGHT, false>(a, d, t, it.chunk, key);
   }
 }
 
@@ -474,17 +558,21 @@ __global__ void __launch_bounds__(kThreads) adamw_update_kernel(const AdamWArgs 
 
 cudaError_t launch_adamw(const AdamWArgs& a, bool eight, cudaStream_t stream,
                          uint64_t* launches) {
-  const uint64_t fill = (uint64_t)a.num_rows;
-  const unsigned blocks = (unsigned)(a.num_items < fill ? a.num_items : fill);
-  cudaError_t e = launch_kernel(adamw_norm_kernel, dim3(blocks), dim3(kThreads), 0, stream, a);
+  // every SM full once, ranges of items as long as that makes them
+  auto blocks_for = [&](int per_sm) {
+    const uint64_t fill = (uint64_t)a.sms * per_sm;
+    return dim3((unsigned)(a.num_items < fill ? a.num_items : fill));
+  };
+  cudaError_t e = launch_kernel(adamw_norm_kernel, blocks_for(NORM_PER_SM), dim3(kThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(eight ? adamw_update_kernel<true> : adamw_update_kernel<false>, dim3(blocks),
-                    dim3(kThreads), 0, stream, a);
+  e = launch_kernel(eight ? adamw_update_kernel<true> : adamw_update_kernel<false>,
+                    blocks_for(UPD_PER_SM), dim3(kThreads), 0, stream, a);
   if (e == cudaSuccess) *launches = 2;
   return e;
 }
 
-int adamw_rows() { return sm_count() * 8; }
+int adamw_sms() { return sm_count(); }
+int adamw_rows(int sms) { return sms * NORM_PER_SM; }
 
 }  // namespace lm
 }  // namespace rcc

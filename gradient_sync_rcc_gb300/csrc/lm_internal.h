@@ -141,7 +141,7 @@ struct AdamWRow {             // a block's part of the norm
 };
 struct AdamWDecision {
   uint32_t skip, step;        // step: steps taken before, its low bits
-  float coef, step_size, inv_root;
+  float coef, factor, step_size, inv_root;  // factor: coef / scale
 };
 struct AdamWArgs {
   const AdamWTensor* tensors;
@@ -151,12 +151,13 @@ struct AdamWArgs {
   AdamWDecision* decision;
   uint32_t* arrived;          // blocks whose row is written; 0 between steps
   uint64_t num_items;
-  int num_rows;               // room for so many
+  int sms;                    // that the rows have room for
   uint32_t seed;
   double scale, max_norm, lr, beta1, beta2;
   float inv_scale, b1, one_minus_b1, b2, one_minus_b2, eps, decay;
 };
-int adamw_rows();             // rows of the current device
+int adamw_sms();              // of the current device
+int adamw_rows(int sms);
 cudaError_t launch_adamw(const AdamWArgs& a, bool eight, cudaStream_t stream, uint64_t* launches);
 
 // ---- output layer + softmax cross entropy ----------------------------------------

@@ -22,7 +22,7 @@ struct Plan {
   char* workspace = nullptr;
   size_t tensors_at = 0, items_at = 0;
   uint64_t items = 0;
-  int rows = 0, device = 0;
+  int sms = 0, device = 0;
   uint32_t seed = 0;
   bool eight = false;
 };
@@ -107,8 +107,8 @@ rcc_status create(const rcc_adamw_tensor* tensors, int n, uint32_t seed, int64_t
   }
   if (!workspace || !on(workspace, 256))
     return fail(bad, "workspace must be given, 256-byte aligned");
-  const int rows = adamw_rows();
-  const Layout l = layout_of(n, items, rows);
+  const int sms = adamw_sms();
+  const Layout l = layout_of(n, items, adamw_rows(sms));
   if (workspace_bytes < l.bytes)
     return fail(RCC_ERR_SHAPE_MISMATCH, "the workspace has %zu bytes, %zu are needed",
                 workspace_bytes, l.bytes);
@@ -164,7 +164,7 @@ rcc_status create(const rcc_adamw_tensor* tensors, int n, uint32_t seed, int64_t
   p.tensors_at = l.tensors_at;
   p.items_at = l.items_at;
   p.items = items;
-  p.rows = rows;
+  p.sms = sms;
   p.seed = seed;
   p.eight = eight;
   cudaError_t e = cudaGetDevice(&p.device);
@@ -196,7 +196,7 @@ extern "C" {
 
 size_t rcc_adamw_workspace(const rcc_adamw_tensor* tensors, int num_tensors) {
   const uint64_t items = count_items(tensors, num_tensors);
-  return items ? layout_of(num_tensors, items, adamw_rows()).bytes : 0;
+  return items ? layout_of(num_tensors, items, adamw_rows(adamw_sms())).bytes : 0;
 }
 
 rcc_status rcc_adamw_create(const rcc_adamw_tensor* tensors, int num_tensors, uint32_t seed,
@@ -231,8 +231,8 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   if (!finite_pos(cfg->lr) && cfg->lr != 0.0) return fail(bad, "lr must be finite and >= 0");
   if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0 && cfg->beta2 >= 0.0 && cfg->beta2 < 1.0))
     return fail(bad, "betas must lie in [0, 1)");
-  if (!finite_pos(cfg->eps) || (float)cfg->eps == 0.f || std::isinf((float)cfg->eps))
-    return fail(bad, "eps must be finite and > 0, in fp32 too");
+  if (!(cfg->eps > 0.0) || !std::isnormal((float)cfg->eps))
+    return fail(bad, "eps must be > 0 and a normal fp32 number");
   if (!std::isfinite(cfg->weight_decay) || !std::isfinite(cfg->max_grad_norm))
     return fail(bad, "weight_decay and max_grad_norm must be finite");
   if (!finite_pos(scale)) return fail(bad, "scale must be finite and > 0");
@@ -246,7 +246,7 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   a.decision = reinterpret_cast<AdamWDecision*>(p.workspace + kDecisionAt);
   a.arrived = reinterpret_cast<uint32_t*>(p.workspace + kArrivedAt);
   a.num_items = p.items;
-  a.num_rows = p.rows;
+  a.sms = p.sms;
   a.seed = p.seed;
   a.scale = scale;
   a.max_norm = cfg->max_grad_norm;

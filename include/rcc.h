@@ -645,13 +645,16 @@ rcc_status rcc_adamw_create(const rcc_adamw_tensor* tensors, int num_tensors, ui
                             int64_t step, double beta1, double beta2, void* workspace,
                             size_t workspace_bytes, rcc_stream_t stream, rcc_adamw* out);
 
-/* One step over all tensors, in fp32, every operation rounded:
- *   g = grad * fl32(1 / scale); norm = sqrt(sum g^2) (fp64); a gradient or norm
- *   that is not finite: nothing changes but the status;
- *   t = step + 1, g' = g * coef, coef = max_grad_norm / norm where 0 <
- *   max_grad_norm < norm, else 1, and then rcc_grad_sync_adamw's update.
+/* One step over all tensors:
+ *   norm = |grad| / scale (good to 2^-40); a gradient or norm that is not finite:
+ *   nothing changes but the status;
+ *   t = step + 1, g = grad / scale * coef, coef = max_grad_norm / norm where 0 <
+ *   max_grad_norm < norm, else 1, and then rcc_grad_sync_adamw's update in fp32.
+ * With fp32 states that is fl32(fl32(grad * fl32(1 / scale)) * coef) and the same
+ * bits as there; with 8-bit states the gradient has one factor, products are fused
+ * into sums, and root and quotient are good to 2^-22.
  * Of cfg lr, beta1, beta2, eps, weight_decay and max_grad_norm count; replicas
- * must be 1 and flags 0.
+ * must be 1 and flags 0; eps must be a normal fp32 number.
  *
  * 8-bit states: m and u = sqrt(v) of 128 neighbours share a scale, the smallest
  * power of two s with max <= 448 s (0 where the max is below 2^-100, and the
