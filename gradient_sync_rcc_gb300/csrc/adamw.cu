@@ -17,7 +17,7 @@
 // bound.
 //
 // One pass over the gradients for their norm, one that updates.  Both are bound
-// by memory: a block takes a range of neighbouring items (4,096 elements of a
+// by memory: a block takes a range of neighbouring items (2,048 elements of a
 // tensor), the update from its end, where the gradients are still in L2.
 #include "lm_common.cuh"
 #include "lm_internal.h"
@@ -26,21 +26,27 @@ namespace rcc {
 namespace lm {
 namespace {
 
-#ifndef NORM_AHEAD
-#define NORM_AHEAD 2
-#define NORM_PER_SM 4
-#define UPD_AHEAD 1
-#define UPD_PER_SM 4
-#endif
 constexpr int kThreads = 256;
-constexpr int kUnit = 8;                             // elements of a thread at a time
-constexpr int kUnits = kAdamWItem / (kThreads * kUnit);  // of them in an item
-constexpr int kGroup = 128;                          // elements that share a scale
-constexpr int kLanes = kGroup / kUnit;               // threads that share one
+constexpr int kUnit = 8;                 // elements of a thread in an item
+constexpr int kGroup = 128;              // elements that share a scale
+constexpr int kLanes = kGroup / kUnit;   // threads that share one
+constexpr int kNumbered = 4096;          // elements whose rounding numbers share a key
 constexpr uint32_t kGolden = 0x9E3779B9u;            // the golden ratio's fraction
 constexpr uint32_t kRootTwo = 0x6A09E667u, kRootThree = 0xBB67AE85u;  // the roots' fractions
+constexpr uint32_t kNothingBits = 27u << 23;  // 2^-100: a group below it is held as zeros
 
-static_assert(kAdamWItem % (kThreads * kUnit) == 0 && kLanes == 16, "whole units and groups");
+// Blocks that an SM holds, of each kernel, vectors of eight fp32 gradients that a
+// thread of the norm has under way (bf16: twice as many), stages of the 8-bit
+// update.  Measured on 544 M elements of 1,024 tensors: the norm of bf16 182 us
+// (6.0 TB/s); 208 with eight blocks of 32 registers, 184 with three.  The
+// 8-bit update with three blocks and two stages 1.39 ms (6.3 TB/s), three stages
+// 1.49, four blocks 1.47, two blocks (of three stages) 1.40; loaded by its threads
+// instead of copied ahead 1.58, with a block barrier for each stage 1.68.
+constexpr int kNormPerSm = 4, kNormAhead = 2, kUpdatePerSm = 4;
+constexpr int kEightPerSm = 3, kStages = 2;
+
+static_assert(kAdamWItem == kThreads * kUnit && kNumbered % kAdamWItem == 0 && kLanes == 16,
+              "whole units and groups");
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
@@ -107,12 +113,23 @@ struct Raw {
   static constexpr int kWords = BF16 ? 4 : 8;
   uint32_t w[kWords];
 };
+template <bool BF16>
+__device__ __forceinline__ void set_words(Raw<BF16>& r, int at, const uint4& v) {
+  r.w[at] = v.x;
+  r.w[at + 1] = v.y;
+  r.w[at + 2] = v.z;
+  r.w[at + 3] = v.w;
+}
+__device__ __forceinline__ void set_wide(Raw<false>& r, const uint4& v) {  // of bf16
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.w[2 * i] = w[i] << 16;
+    r.w[2 * i + 1] = w[i] & 0xFFFF0000u;
+  }
+}
 __device__ __forceinline__ void load_raw(const void* grad, uint64_t i, Raw<true>& r) {
-  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(grad) + i);
-  r.w[0] = v.x;
-  r.w[1] = v.y;
-  r.w[2] = v.z;
-  r.w[3] = v.w;
+  set_words(r, 0, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(grad) + i));
 }
 __device__ __forceinline__ void load_raw(const void* grad, uint64_t i, Raw<false>& r) {
   float f[8];
@@ -133,7 +150,7 @@ __device__ __forceinline__ float2 pair_of(const Raw<false>& r, int i) {
 template <bool BF16>
 __device__ __forceinline__ void add_vectors(const void* grad, uint64_t begin, uint64_t vectors,
                                             Squares& s) {
-  constexpr int kAhead = BF16 ? 2 * NORM_AHEAD : NORM_AHEAD;  // vectors of a thread under way
+  constexpr int kAhead = BF16 ? 2 * kNormAhead : kNormAhead;  // vectors of a thread under way
   for (uint64_t v = threadIdx.x; v < vectors; v += kAhead * kThreads) {
     Raw<BF16> r[kAhead];
 #pragma unroll
@@ -210,35 +227,51 @@ __device__ __forceinline__ void block_sum(double& sum, unsigned long long& bad, 
   }
 }
 
-// Whether and how the step is taken: one thread, once a step
-__device__ __forceinline__ void decide(const AdamWArgs& a, double sum, unsigned long long bad) {
-  rcc_adamw_status s = *a.status;
-  AdamWDecision d = {};
-  const double norm = sqrt(sum) / a.scale;
+// What the step would be, from the status before it: one thread, once a step
+struct Powers {
+  double beta1, beta2;
+  float step_size, inv_root;
+  int64_t step;
+};
+__device__ __forceinline__ Powers powers_of(const AdamWArgs& a) {
+  Powers p;
+  p.step = a.status->step;
+  p.beta1 = a.status->beta1_power * a.beta1;
+  p.beta2 = a.status->beta2_power * a.beta2;
+  p.step_size = (float)(a.lr / (1.0 - p.beta1));
+  p.inv_root = (float)(1.0 / sqrt(1.0 - p.beta2));
+  return p;
+}
+
+// Whether and how it is taken
+__device__ __forceinline__ void decide(const AdamWArgs& a, const Powers& p, double sum,
+                                       unsigned long long bad) {
+  const double norm = sqrt(sum) * a.inv_scale64;
+  AdamWDecision d;
   d.skip = bad > 0 || !(norm < INFINITY);
-  d.coef = !d.skip && a.max_norm > 0.0 && norm > a.max_norm ? (float)(a.max_norm / norm) : 1.f;
-  d.step = (uint32_t)s.step;
-  s.grad_norm = norm;
-  s.nonfinite = bad > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)bad;
-  s.skipped = d.skip;
-  s.clip_coef = d.coef;
-  if (!d.skip) {
-    s.step += 1;
-    s.beta1_power *= a.beta1;
-    s.beta2_power *= a.beta2;
-    d.factor = (float)((double)d.coef / a.scale);
-    d.step_size = (float)(a.lr / (1.0 - s.beta1_power));
-    d.inv_root = (float)(1.0 / sqrt(1.0 - s.beta2_power));
-  }
-  *a.status = s;
+  const double coef = !d.skip && a.max_norm > 0.0 && norm > a.max_norm ? a.max_norm / norm : 1.0;
+  d.coef = (float)coef;
+  d.factor = (float)((double)d.coef * a.inv_scale64);
+  d.step = (uint32_t)p.step;
+  d.step_size = p.step_size;
+  d.inv_root = p.inv_root;
   *a.decision = d;
+  a.status->grad_norm = norm;
+  a.status->nonfinite = bad > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)bad;
+  a.status->skipped = d.skip;
+  a.status->clip_coef = d.coef;
+  if (d.skip) return;
+  a.status->step = p.step + 1;
+  a.status->beta1_power = p.beta1;
+  a.status->beta2_power = p.beta2;
 }
 
 // Each block leaves one row; the last one to do so adds them up, in the rows'
 // order, and decides.
-__global__ void __launch_bounds__(kThreads, NORM_PER_SM) adamw_norm_kernel(const AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const AdamWArgs a) {
   __shared__ double sums[kThreads / 32];
   __shared__ unsigned long long bads[kThreads / 32];
+  __shared__ Powers powers;
   __shared__ bool last;
   pdl_wait_then_release();
   Squares s;
@@ -272,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, NORM_PER_SM) adamw_norm_kernel(const
   __syncthreads();
   if (!last) return;
   __threadfence();
+  if (threadIdx.x == kThreads - 1) powers = powers_of(a);  // beside the sum
   sum = 0.0;
   bad = 0;
   for (uint32_t r = threadIdx.x; r < gridDim.x; r += kThreads) {
@@ -281,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, NORM_PER_SM) adamw_norm_kernel(const
   block_sum(sum, bad, sums, bads);
   if (threadIdx.x == 0) {
     *a.arrived = 0;
-    decide(a, sum, bad);
+    decide(a, powers, sum, bad);
   }
 }
 
@@ -320,46 +354,45 @@ __device__ __forceinline__ uint2 narrow_e4m3(const float2 (&v)[4]) {
   return make_uint2(w[0], w[1]);
 }
 
-// The smallest power of two s with top <= 448 s: 448 is 1.75 2^8, so a fraction
-// above 0.75 carries into the exponent.  0 for next to nothing, NaN for a NaN.
-__device__ __forceinline__ float power_for(uint32_t top_bits) {
-  const float top = __uint_as_float(top_bits);
-  if (top < kAdamWNothing) return 0.f;
-  if (!(top <= INFINITY)) return top;
-  const uint32_t b = min(top_bits, 0x7F7FFFFFu);
-  return __uint_as_float(((b + 0x1FFFFFu) & 0x7F800000u) - (8u << 23));
-}
-
 // y >= 0 on the grid of e4m3, up with a chance of its distance over a step:
-// `chance`, of 2^20.  Below 2^-6 the grid is even, as it is from 2^-6 to 2^-5.
+// `number` of 2^16.  Below 2^-6 the grid is even, as it is from 2^-6 to 2^-5.
 // Over 448 is left to the conversion, which saturates.
-__device__ __forceinline__ float round_e4m3(float y, uint32_t chance) {
+__device__ __forceinline__ float round_e4m3(float y, uint32_t number) {
   const float low = y < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t b = (__float_as_uint(__fadd_rn(y, low)) + chance) & 0xFFF00000u;
+  const uint32_t b = (__float_as_uint(__fadd_rn(y, low)) + (number << 4)) & 0xFFF00000u;
   return __fsub_rn(__uint_as_float(b), low);
 }
 
-// What eight values of a group are held as, and its scale
+// What eight values of a group are held as, and its scale s: the smallest power
+// of two with max <= 448 s.  448 is 1.75 2^8, so a fraction above 0.75 carries
+// into the exponent.  0 for next to nothing, NaN for a NaN.
 template <bool ROOT>
-__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&chance)[kUnit],
+__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&number)[kUnit],
                                       float& scale) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    top = max(max(top, __float_as_uint(v[i].x) & 0x7FFFFFFFu), __float_as_uint(v[i].y) & 0x7FFFFFFFu);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = __float_as_uint(v[i].x), y = __float_as_uint(v[i].y);
+    top = ROOT ? max(max(top, x), y) : max(max(top, x << 1), y << 1);  // but their signs
+  }
   // over the 16 threads of a group; a NaN's bits are the largest of all
   top = __reduce_max_sync(threadIdx.x & 16 ? 0xFFFF0000u : 0x0000FFFFu, top);
-  scale = power_for(top);
-  const float inv = scale > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(scale)) : 0.f;
+  if (!ROOT) top >>= 1;
+  const uint32_t s = ((min(top, 0x7F7FFFFFu) + 0x1FFFFFu) & 0x7F800000u) - (8u << 23);
+  const bool some = top >= kNothingBits;
+  scale = some ? __uint_as_float(top > 0x7F800000u ? top : s) : 0.f;
+  const float inv = some ? __uint_as_float((254u << 23) - s) : 0.f;
   float2 w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = mul2(v[i], both(inv));
-    w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), chance[2 * i]);
-    w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), chance[2 * i + 1]);
+    w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), number[2 * i]);
+    w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), number[2 * i + 1]);
     if (ROOT) {
-      if (y.x > 0.f) w[i].x = fmaxf(w[i].x, 0x1p-9f);
-      if (y.y > 0.f) w[i].y = fmaxf(w[i].y, 0x1p-9f);
+      // the smallest step, but for zeros: times 2^126 all else is above it
+      const float2 f = mul2(y, both(0x1p126f));
+      w[i].x = fmaxf(w[i].x, fminf(f.x, 0x1p-9f));
+      w[i].y = fmaxf(w[i].y, fminf(f.y, 0x1p-9f));
     } else {
       w[i] = make_float2(copysignf(w[i].x, y.x), copysignf(w[i].y, y.y));
     }
@@ -377,7 +410,14 @@ __device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i,
     u.vs = live ? t.v_scales[i / kGroup] : 0.f;
   }
   if (t.vec && i + kUnit <= t.numel) {
-    load_raw(t.grad, i, u.g);
+    if constexpr (BF16) {
+      load_raw(t.grad, i, u.g);
+    } else if (t.bf16) {
+      set_wide(u.g, *reinterpret_cast<const uint4*>(
+                        static_cast<const __nv_bfloat16*>(t.grad) + i));
+    } else {
+      load_raw(t.grad, i, u.g);
+    }
     load8(t.param + i, u.p);
     if constexpr (EIGHT) {
       u.m8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
@@ -397,7 +437,7 @@ __device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i,
     if constexpr (BF16)
       u.g.w[e / 2] |= (live ? static_cast<const uint16_t*>(t.grad)[i + e] : 0u) << (16 * (e % 2));
     else
-      u.g.w[e] = live ? static_cast<const uint32_t*>(t.grad)[i + e] : 0u;
+      u.g.w[e] = live ? __float_as_uint(grad_at(t, i + e)) : 0u;
     u.p[e] = live ? t.param[i + e] : 0.f;
     if constexpr (EIGHT) {
       q[0][e / 4] |= (live ? static_cast<const uint8_t*>(t.m)[i + e] : 0u) << (8 * (e % 4));
@@ -485,7 +525,7 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
   float2 m[4], v[4];
   widen_e4m3(u.m8, m);
   widen_e4m3(u.v8, v);
-  uint32_t chance[kUnit];
+  uint32_t number[kUnit];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 g = mul2(pair_of(u.g, i), both(d.factor));
@@ -500,79 +540,270 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
     u.p[2 * i] = p.x;
     u.p[2 * i + 1] = p.y;
     const uint32_t h = mix(first + i);
-    chance[2 * i] = (h & 0xFFFFu) << 4;
-    chance[2 * i + 1] = h >> 16 << 4;
+    number[2 * i] = h & 0xFFFFu;
+    number[2 * i + 1] = h >> 16;
   }
-  u.m8 = hold<false>(m, chance, u.ms);
-  u.v8 = hold<true>(v, chance, u.vs);
+  u.m8 = hold<false>(m, number, u.ms);
+  u.v8 = hold<true>(v, number, u.vs);
 }
 
-template <bool EIGHT, bool BF16>
+// fp32 states: a thread's loads are bytes enough by themselves.  The tables do
+// not change between steps, so they are read before the norm is there.
+template <bool BF16>
 __device__ __forceinline__ void update_item(const AdamWArgs& a, const AdamWDecision& d,
-                                            const AdamWTensor& t, uint32_t chunk, uint32_t key) {
+                                            const AdamWTensor& t, uint32_t chunk) {
   const uint64_t i = (uint64_t)chunk * kAdamWItem + threadIdx.x * kUnit;
-#pragma unroll 1
-  for (int k0 = 0; k0 < kUnits; k0 += UPD_AHEAD) {
-    Unit<EIGHT, BF16> u[UPD_AHEAD];
-#pragma unroll
-    for (int k = 0; k < UPD_AHEAD; ++k) load_unit(t, i + (k0 + k) * kThreads * kUnit, u[k]);
-#pragma unroll
-    for (int k = 0; k < UPD_AHEAD; ++k) {
-      update_unit(a, d, key + ((k0 + k) * kThreads + threadIdx.x) * (kUnit / 2), u[k]);
-      store_unit(t, i + (k0 + k) * kThreads * kUnit, u[k]);
-    }
-  }
+  Unit<false, BF16> u;
+  load_unit(t, i, u);
+  update_unit(a, d, 0, u);
+  store_unit(t, i, u);
 }
-
-template <bool EIGHT>
-__global__ void __launch_bounds__(kThreads, UPD_PER_SM) adamw_update_kernel(const AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, kUpdatePerSm) adamw_update_kernel(const AdamWArgs a) {
   __shared__ AdamWTensor t;
+  uint64_t lo, hi;
+  range_of(a.num_items, lo, hi);
+  AdamWItem next = a.items[hi - 1];
+  uint32_t tensor = next.tensor;
+  auto load_tensor = [&] {
+    if (threadIdx.x < sizeof(AdamWTensor) / 8)
+      reinterpret_cast<uint64_t*>(&t)[threadIdx.x] =
+          reinterpret_cast<const uint64_t*>(a.tensors + tensor)[threadIdx.x];
+    __syncthreads();
+  };
+  load_tensor();
   pdl_wait_then_release();
   const AdamWDecision d = *a.decision;
   if (d.skip) return;
-  uint64_t lo, hi;
-  range_of(a.num_items, lo, hi);
-  const uint32_t step_key = mix(a.seed ^ mix(d.step));
-  AdamWItem next = a.items[hi - 1];
-  uint32_t tensor = ~0u;
   for (uint64_t item = hi; item-- > lo;) {
     const AdamWItem it = next;
     if (item > lo) next = a.items[item - 1];
     if (it.tensor != tensor) {
       __syncthreads();
       tensor = it.tensor;
-      if (threadIdx.x < sizeof(AdamWTensor) / 8)
-        reinterpret_cast<uint64_t*>(&t)[threadIdx.x] =
-            reinterpret_cast<const uint64_t*>(a.tensors + tensor)[threadIdx.x];
-      __syncthreads();
+      load_tensor();
     }
-    const uint32_t key = mix(mix(step_key + tensor * kGolden) ^ it.chunk);
     if (t.bf16)
-      update_item<EIGHT, true>(a, d, t, it.chunk, key);
+      update_item<true>(a, d, t, it.chunk);
     else
-      update_item<EIGHT, false>(a, d, t, it.chunk, key);
+      update_item<false>(a, d, t, it.chunk);
   }
+}
+
+// 8-bit states: half the bytes for the same threads, so what a block reads is
+// copied into shared memory ahead, item by item.  One more warp does that; an
+// item's stage is full when its bytes are there and empty when all other warps are
+// through, which no block barrier holds together.
+constexpr int kEightThreads = kThreads + 32;
+
+struct Entry {  // an item and its tensor
+  AdamWTensor t;
+  AdamWItem item;
+};
+constexpr int kEntryWords = sizeof(Entry) / 8;
+
+// A stage: parameters, gradients, the two states, their scales, the entry
+template <bool BF16>
+struct Stage {
+  static constexpr int kGrad = kAdamWItem * 4, kM = kGrad + kAdamWItem * (BF16 ? 2 : 4);
+  static constexpr int kV = kM + kAdamWItem, kMs = kV + kAdamWItem, kVs = kMs + kAdamWItem / kGroup * 4;
+  static constexpr int kEntry = kVs + kAdamWItem / kGroup * 4;
+  static constexpr int kBytes = (kEntry + (int)sizeof(Entry) + 127) / 128 * 128;
+};
+
+// `bytes` (a multiple of 16, from a boundary of 16) into shared memory
+__device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          to), "l"(from), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Whether the item at `first` is whole and on boundaries that bulk copies take
+__device__ __forceinline__ bool whole_item(const AdamWTensor& t, uint64_t first) {
+  return t.bulk && first + kAdamWItem <= t.numel;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void copy_item(const AdamWTensor& t, uint64_t first, uint32_t to,
+                                           uint32_t bar) {
+  using S = Stage<BF16>;
+  const uint32_t size = BF16 || t.bf16 ? 2 : 4;
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+               "r"(kAdamWItem * (4 + size + 2)) : "memory");
+  copy_bulk(to, t.param + first, kAdamWItem * 4, bar);
+  copy_bulk(to + S::kGrad, static_cast<const char*>(t.grad) + first * size, kAdamWItem * size, bar);
+  copy_bulk(to + S::kM, static_cast<const char*>(t.m) + first, kAdamWItem, bar);
+  copy_bulk(to + S::kV, static_cast<const char*>(t.v) + first, kAdamWItem, bar);
+}
+// The scales, which may lie anywhere: one a lane, whose arrival follows its copy
+template <bool BF16>
+__device__ __forceinline__ void copy_scale(const AdamWTensor& t, uint64_t first,
+                                           unsigned char* stage, int lane, uint32_t bar) {
+  static_assert(kAdamWItem / kGroup == 16, "a half warp each");
+  const float* from = (lane < 16 ? t.m_scales : t.v_scales) + first / kGroup + lane % 16;
+  copy_async<4>(stage + Stage<BF16>::kMs + lane * 4, from);
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A thread's unit out of a stage
+template <bool BF16>
+__device__ __forceinline__ void take_unit(const unsigned char* stage, bool bf16,
+                                          Unit<true, BF16>& u) {
+  using S = Stage<BF16>;
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 q = reinterpret_cast<const uint4*>(stage)[2 * tid + h];
+    u.p[4 * h] = __uint_as_float(q.x);
+    u.p[4 * h + 1] = __uint_as_float(q.y);
+    u.p[4 * h + 2] = __uint_as_float(q.z);
+    u.p[4 * h + 3] = __uint_as_float(q.w);
+  }
+  const uint4* g = reinterpret_cast<const uint4*>(stage + S::kGrad);
+  if constexpr (BF16) {
+    set_words(u.g, 0, g[tid]);
+  } else if (bf16) {
+    set_wide(u.g, g[tid]);
+  } else {
+    set_words(u.g, 0, g[2 * tid]);
+    set_words(u.g, 4, g[2 * tid + 1]);
+  }
+  u.m8 = reinterpret_cast<const uint2*>(stage + S::kM)[tid];
+  u.v8 = reinterpret_cast<const uint2*>(stage + S::kV)[tid];
+  u.ms = reinterpret_cast<const float*>(stage + S::kMs)[tid / kLanes];
+  u.vs = reinterpret_cast<const float*>(stage + S::kVs)[tid / kLanes];
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <bool BF16>  // every gradient of the plan is; else they may be mixed
+__global__ void __launch_bounds__(kEightThreads, kEightPerSm)
+    adamw_update_eight_kernel(const AdamWArgs a) {
+  using S = Stage<BF16>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[2][kStages];
+  const int tid = threadIdx.x;
+  const uint32_t full = (uint32_t)__cvta_generic_to_shared(bars[0]), empty = full + 8 * kStages;
+  const uint32_t stages = (uint32_t)__cvta_generic_to_shared(smem);
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(full + 8 * s, 33);  // the bulk copies', and each lane's
+      bar_init(empty + 8 * s, kThreads / 32);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  uint64_t lo, hi;
+  range_of(a.num_items, lo, hi);
+  const uint64_t items = hi - lo;  // the n-th is the one at hi - 1 - n
+  int s = 0;
+  uint32_t parity = 0;
+  auto next = [&] {
+    if (++s == kStages) {
+      s = 0;
+      parity ^= 1;
+    }
+  };
+  if (tid >= kThreads) {
+    const int lane = tid - kThreads;
+    auto item_at = [&](uint64_t n) { return a.items[hi - 1 - min(n, items - 1)]; };
+    auto entry_word = [&](const AdamWItem& it) {  // of the first kEntryWords lanes
+      if (lane >= kEntryWords) return uint64_t{0};
+      if (lane == kEntryWords - 1) return (uint64_t)it.chunk << 32 | it.tensor;
+      return reinterpret_cast<const uint64_t*>(a.tensors + it.tensor)[lane];
+    };
+    // words of the next item, and the one after that (tables that do not change)
+    uint64_t word = entry_word(item_at(0));
+    AdamWItem far = item_at(1);
+    pdl_wait_then_release();
+    if (a.decision->skip) return;
+    uint64_t n = 0;
+    for (; n < items; ++n, next()) {
+      const uint64_t word_next = entry_word(far);
+      far = item_at(n + 2);
+      if (n >= kStages && !bar_wait(empty + 8 * s, parity ^ 1)) break;
+      unsigned char* stage = smem + s * S::kBytes;
+      const Entry& e = *reinterpret_cast<const Entry*>(stage + S::kEntry);
+      if (lane < kEntryWords) reinterpret_cast<uint64_t*>(stage + S::kEntry)[lane] = word;
+      __syncwarp();
+      const uint64_t first = (uint64_t)e.item.chunk * kAdamWItem;
+      if (whole_item(e.t, first)) {
+        copy_scale<BF16>(e.t, first, stage, lane, full + 8 * s);
+        if (lane == 0) copy_item<BF16>(e.t, first, stages + s * S::kBytes, full + 8 * s);
+      } else {
+        arrive(full + 8 * s);
+        if (lane == 0) arrive(full + 8 * s);
+      }
+      word = word_next;
+    }
+    if (n < items) {  // a wait ran out: the copies under way end before the block does
+      if (lane == 0) a.status->skipped = -1;
+      for (uint64_t m = n >= kStages ? n - kStages : 0; m < n; ++m)
+        bar_wait(full + 8 * (int)(m % kStages), (uint32_t)(m / kStages) & 1);
+    }
+    return;
+  }
+  pdl_wait_then_release();
+  const AdamWDecision d = *a.decision;
+  if (d.skip) return;
+  const uint32_t step_key = mix(a.seed ^ mix(d.step));
+  for (uint64_t n = 0; n < items; ++n, next()) {
+    if (!bar_wait(full + 8 * s, parity)) {
+      a.status->skipped = -1;
+      return;
+    }
+    const unsigned char* stage = smem + s * S::kBytes;
+    const Entry& e = *reinterpret_cast<const Entry*>(stage + S::kEntry);
+    const uint64_t first = (uint64_t)e.item.chunk * kAdamWItem, i = first + tid * kUnit;
+    Unit<true, BF16> u;
+    if (whole_item(e.t, first))
+      take_unit<BF16>(stage, e.t.bf16, u);
+    else
+      load_unit(e.t, i, u);
+    const uint32_t key = mix(mix(step_key + e.item.tensor * kGolden) ^ (uint32_t)(i / kNumbered));
+    update_unit(a, d, key + (uint32_t)(i % kNumbered) / 2, u);
+    store_unit(e.t, i, u);
+    __syncwarp();
+    if (tid % 32 == 0) arrive(empty + 8 * s);
+  }
+}
+
+// Every SM full once, ranges of items as long as that makes them
+dim3 blocks_for(const AdamWArgs& a, int per_sm) {
+  const uint64_t fill = (uint64_t)a.sms * per_sm;
+  return dim3((unsigned)(a.num_items < fill ? a.num_items : fill));
+}
+
+template <bool BF16>
+cudaError_t launch_eight(const AdamWArgs& a, cudaStream_t stream) {
+  constexpr int kShared = kStages * Stage<BF16>::kBytes;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(adamw_update_eight_kernel<BF16>, kShared, allowed);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(adamw_update_eight_kernel<BF16>, blocks_for(a, kEightPerSm),
+                       dim3(kEightThreads), kShared, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_adamw(const AdamWArgs& a, bool eight, cudaStream_t stream,
                          uint64_t* launches) {
-  // every SM full once, ranges of items as long as that makes them
-  auto blocks_for = [&](int per_sm) {
-    const uint64_t fill = (uint64_t)a.sms * per_sm;
-    return dim3((unsigned)(a.num_items < fill ? a.num_items : fill));
-  };
-  cudaError_t e = launch_kernel(adamw_norm_kernel, blocks_for(NORM_PER_SM), dim3(kThreads), 0, stream, a);
+  cudaError_t e =
+      launch_kernel(adamw_norm_kernel, blocks_for(a, kNormPerSm), dim3(kThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(eight ? adamw_update_kernel<true> : adamw_update_kernel<false>,
-                    blocks_for(UPD_PER_SM), dim3(kThreads), 0, stream, a);
+  if (eight) {
+    e = a.all_bf16 ? launch_eight<true>(a, stream) : launch_eight<false>(a, stream);
+  } else {
+    e = launch_kernel(adamw_update_kernel, blocks_for(a, kUpdatePerSm), dim3(kThreads), 0, stream, a);
+  }
   if (e == cudaSuccess) *launches = 2;
   return e;
 }
 
 int adamw_sms() { return sm_count(); }
-int adamw_rows(int sms) { return sms * NORM_PER_SM; }
+int adamw_rows(int sms) { return sms * kNormPerSm; }
 
 }  // namespace lm
 }  // namespace rcc

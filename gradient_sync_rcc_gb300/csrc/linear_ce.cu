@@ -50,9 +50,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
 // `bar` is an address of any block of the cluster.  Relaxed: the arrival
 // publishes nothing of this thread's, only the bytes the copies will bring.
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
@@ -65,26 +62,6 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-// Waits for a phase, at most about two seconds; false when that ran out.
-constexpr long long kWaitCycles = 4000000000ll;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  if (bar_try(bar, parity)) return true;
-  const long long t0 = clock64();
-  do {
-    if (bar_try(bar, parity)) return true;
-  } while (clock64() - t0 < kWaitCycles);
-  return false;
-}
-
 // One box of a two-dimensional tensor map into this block's shared memory;
 // the bytes count on `bar`, which with CG = 2 is the pair's first block's.
 template <int CG>

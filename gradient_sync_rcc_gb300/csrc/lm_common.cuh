@@ -110,11 +110,53 @@ __device__ __forceinline__ void store_slab(T* row, size_t base, int t, size_t di
   }
 }
 
+// `n` (4, 8 or 16) bytes of global memory into shared memory, asynchronously
+template <int N>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(N)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the newest N groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A token id or label; one outside [0, vocab) comes back as -1 (padding).
 __device__ __forceinline__ int64_t load_id(const void* ids, int ids64, size_t t, size_t vocab) {
   const int64_t id = ids64 ? static_cast<const int64_t*>(ids)[t]
                            : static_cast<const int32_t*>(ids)[t];
   return id >= 0 && id < static_cast<int64_t>(vocab) ? id : -1;
+}
+
+// Barriers in shared memory, by their shared address
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Waits for a phase, at most about two seconds; false when that ran out.
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
+    if (bar_try(bar, parity)) return true;
+  } while (clock64() - t0 < kWaitCycles);
+  return false;
 }
 
 // launch_kernel for a grid of clusters of `cluster` blocks.

@@ -109,9 +109,9 @@ struct RotaryArgs {
   int type, index64;
   bool half, inverse;
   bool copies;            // the columns past the pairs are written too
-  bool vec;               // every row in vectors of eight elements
+  int wide;               // elements of a vector: 8, 4, 2 or 1, as every row allows
   float scale;
-  uint32_t turned_units, copied_units, chunks;  // set by the launch
+  int units, block_tokens, block_heads;  // set by the launch
 };
 constexpr size_t kMaxHeads = 65536;
 constexpr size_t kMaxHeadDim = 8192;
@@ -119,8 +119,7 @@ cudaError_t launch_rotary(RotaryArgs a, cudaStream_t stream);
 
 // ---- AdamW over many tensors -------------------------------------------------------
 
-constexpr int kAdamWItem = 4096;            // elements of a tensor that are one item
-constexpr float kAdamWNothing = 7.88860905e-31f;  // 2^-100: a group below it is held as zeros
+constexpr int kAdamWItem = 2048;  // elements of a tensor that are one item
 
 struct AdamWTensor {
   const void* grad;
@@ -129,8 +128,9 @@ struct AdamWTensor {
   float *m_scales, *v_scales;
   __nv_bfloat16* copy;        // or NULL
   uint64_t numel;
-  uint32_t bf16;              // the gradient's type
-  uint32_t vec;               // every buffer on a boundary of eight elements
+  uint16_t bf16;              // the gradient's type
+  uint8_t vec;                // every buffer on a boundary of eight elements
+  uint8_t bulk;               // and the 8-bit states on one of 16 bytes
 };
 struct AdamWItem {
   uint32_t tensor, chunk;
@@ -152,8 +152,9 @@ struct AdamWArgs {
   uint32_t* arrived;          // blocks whose row is written; 0 between steps
   uint64_t num_items;
   int sms;                    // that the rows have room for
+  bool all_bf16;              // every gradient
   uint32_t seed;
-  double scale, max_norm, lr, beta1, beta2;
+  double inv_scale64, max_norm, lr, beta1, beta2;
   float inv_scale, b1, one_minus_b1, b2, one_minus_b2, eps, decay;
 };
 int adamw_sms();              // of the current device

@@ -24,7 +24,7 @@ struct Plan {
   uint64_t items = 0;
   int sms = 0, device = 0;
   uint32_t seed = 0;
-  bool eight = false;
+  bool eight = false, all_bf16 = true;
 };
 
 std::mutex g_plans_mu;
@@ -140,6 +140,8 @@ rcc_status create(const rcc_adamw_tensor* tensors, int n, uint32_t seed, int64_t
   status->beta1_power = std::pow(beta1, (double)step);
   status->beta2_power = std::pow(beta2, (double)step);
   status->clip_coef = 1.f;
+  bool all_bf16 = true;
+  for (int i = 0; i < n; ++i) all_bf16 = all_bf16 && tensors[i].grad_type == RCC_BF16;
   auto* table = reinterpret_cast<AdamWTensor*>(tables.data());
   auto* item = reinterpret_cast<AdamWItem*>(tables.data() + (l.items_at - l.tensors_at));
   for (int i = 0; i < n; ++i) {
@@ -155,6 +157,7 @@ rcc_status create(const rcc_adamw_tensor* tensors, int n, uint32_t seed, int64_t
     d.numel = t.numel;
     d.bf16 = t.grad_type == RCC_BF16;
     d.vec = vectors_of(t, eight);
+    d.bulk = d.vec && on(t.exp_avg, 16) && on(t.exp_avg_sq, 16);
     const size_t chunks = (t.numel + kAdamWItem - 1) / kAdamWItem;
     for (size_t c = 0; c < chunks; ++c) *item++ = {(uint32_t)i, (uint32_t)c};
   }
@@ -167,6 +170,7 @@ rcc_status create(const rcc_adamw_tensor* tensors, int n, uint32_t seed, int64_t
   p.sms = sms;
   p.seed = seed;
   p.eight = eight;
+  p.all_bf16 = all_bf16;
   cudaError_t e = cudaGetDevice(&p.device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -247,8 +251,9 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   a.arrived = reinterpret_cast<uint32_t*>(p.workspace + kArrivedAt);
   a.num_items = p.items;
   a.sms = p.sms;
+  a.all_bf16 = p.all_bf16;
   a.seed = p.seed;
-  a.scale = scale;
+  a.inv_scale64 = 1.0 / scale;
   a.max_norm = cfg->max_grad_norm;
   a.lr = cfg->lr;
   a.beta1 = cfg->beta1;

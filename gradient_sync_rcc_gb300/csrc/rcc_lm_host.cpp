@@ -179,8 +179,9 @@ rcc_status check_heads(const Heads& r, size_t tokens, size_t head_dim, size_t si
   return RCC_OK;
 }
 
-bool head_vectors(const Heads& r, size_t size) {
-  return reinterpret_cast<uintptr_t>(r.p) % (8 * size) == 0 && r.token % 8 == 0 && r.head % 8 == 0;
+// Every head in vectors of n elements, each on a boundary of its size
+bool head_vectors(const Heads& r, size_t size, size_t n) {
+  return reinterpret_cast<uintptr_t>(r.p) % (n * size) == 0 && r.token % n == 0 && r.head % n == 0;
 }
 
 rcc_status rotary(const char* what, const rcc_rotary_rows* q, const rcc_rotary_rows* k,
@@ -243,9 +244,15 @@ rcc_status rotary(const char* what, const rcc_rotary_rows* q, const rcc_rotary_r
     return fail(RCC_ERR_INVALID_ARGUMENT, "%zu tokens of %zu heads of %zu: too many for one call",
                 tokens, heads, head_dim);
   RotaryArgs a = {};
-  a.vec = pairs % 8 == 0 && head_dim % 8 == 0;
+  // the widest vectors: of both halves of the pairs, or of neighbours
+  auto fits = [&](size_t w) {
+    bool ok = head_dim % w == 0 && (layout == RCC_ROTARY_INTERLEAVED || pairs % w == 0);
+    for (int i = 0; i < n; ++i)
+      ok = ok && head_vectors(in[i], s, w) && head_vectors(out[i], s, w);
+    return ok;
+  };
+  a.wide = fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
   for (int i = 0; i < n; ++i) {
-    a.vec = a.vec && head_vectors(in[i], s) && head_vectors(out[i], s);
     RotaryRows& r = in[i].name[0] == 'q' ? a.q : a.k;
     r = {in[i].p, const_cast<void*>(out[i].p), in[i].heads, in[i].token, in[i].head, out[i].token,
          out[i].head};

@@ -206,24 +206,6 @@ __device__ __forceinline__ void store_bytes(int8_t* p, int left, const uint32_t 
   }
 }
 
-// `n` (4, 8 or 16) bytes of global memory into shared memory, asynchronously
-template <int N>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
-  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(N)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {  // all but the newest N groups
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Threads of all blocks of one SM (those waiting to start included) and rows
 // held in shared memory.  Measured at 16,384 rows of 4,096 bf16 (fp32) columns,
 // where 6.78 TB/s would take 50 (89) us each way:

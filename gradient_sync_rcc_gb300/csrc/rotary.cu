@@ -9,9 +9,12 @@
 // the argument of the sine and cosine (2^-25 of half a turn off as a float).
 //
 // Memory bound: queries and keys are read and written once, in one launch.  A
-// thread makes the sines and cosines of eight pairs of a token and turns those
-// pairs in kHeads heads, so that 16 (32) bytes a pair of accesses stand against
-// an eighth of the sines; its loads are all under way before the first is used.
+// block takes a few tokens with all their heads (or, where there are few tokens,
+// some heads of one), makes their sines and cosines once, in shared memory, while
+// its first loads are under way, and turns unit after unit: W pairs, two vectors
+// of W elements.
+#include <algorithm>
+
 #include "lm_common.cuh"
 #include "lm_internal.h"
 
@@ -20,23 +23,70 @@ namespace lm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // heads of one token that a thread turns
+// Blocks an SM, units of a block for each thread, units that a thread has under
+// way (32-byte vectors: half).  16,384 tokens of 40 heads of 128 in bf16, forward
+// and backward (671 MB): 104.9 us (6.4 TB/s); with four units under way and three
+// blocks 106.8, four units a block 104.4, two 131.  Sines made by each thread for four heads instead: 177.
+constexpr int kPerSm = 4, kShare = 8, kUnderWay = 2;
+constexpr int kTableBytes = 32 * 1024;  // of sines and cosines, at most
 
-struct Rows {
-  const char* in;
-  char* out;
+// W elements as they lie in memory
+template <typename T, int W>
+struct Vector {
+  static constexpr int kBytes = W * (int)sizeof(T);
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes == 32) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                     "=r"(w[6]), "=r"(w[7]) : "l"(p) : "memory");
+    } else if constexpr (kBytes == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kBytes == 32)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                   "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+    else if constexpr (kBytes == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 8)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (kBytes == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[W]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (W == 1) {
+      w[0] = pack2(v[0], 0.f) & 0xFFFFu;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 2) w[i / 2] = pack2(v[i], v[i + 1]);
+    }
+  }
 };
-
-// The head `h` of a token among the queries' and then the keys'
-__device__ __forceinline__ Rows head_rows(const RotaryArgs& a, size_t token, int h, int size) {
-  const bool key = h >= (int)a.q.heads;
-  const RotaryRows& r = key ? a.k : a.q;
-  const size_t head = key ? h - (int)a.q.heads : h;
-  Rows s;
-  s.in = static_cast<const char*>(r.in) + (token * r.in_token + head * r.in_head) * size;
-  s.out = static_cast<char*>(r.out) + (token * r.out_token + head * r.out_head) * size;
-  return s;
-}
 
 __device__ __forceinline__ uint64_t position_of(const RotaryArgs& a, size_t token) {
   int64_t p = (int64_t)token;
@@ -46,119 +96,193 @@ __device__ __forceinline__ uint64_t position_of(const RotaryArgs& a, size_t toke
   return p < 0 ? 0 : (uint64_t)p + (uint64_t)a.offset;
 }
 
-__device__ __forceinline__ void sine_cosine(uint64_t position, uint64_t turns, float scale,
-                                            float& s, float& c) {
-  // half turns in [-1, 1)
-  const float half = (float)(int32_t)((position * turns) >> 32) * 0x1p-31f;
-  sincospif(half, &s, &c);
-  s *= scale;
-  c *= scale;
+// Cosine and sine of a token's pairs, with the scale.  The pairs of a unit lie
+// a column of `units` float4 (of two pairs) apart, so that neighbouring units'
+// reads fall on neighbouring banks; W of 1 has one pair in a float2.
+template <int W>
+__device__ __forceinline__ int table_at(int pair, int units) {
+  if constexpr (W == 1) return pair;
+  return ((pair % W) / 2 * units + pair / W) * 2 + pair % 2;
 }
 
-// A unit of VEC: eight pairs (16 elements), or eight elements that are only
-// copied; else one pair or one element.
-template <typename T, bool VEC, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
+// A unit of a head, at two columns; `turned` of its pairs turn
+template <typename T, int W>
+struct Unit {
+  Vector<T, W> x, y;
+  T* out;
+  int first, second;  // columns; -1: none
+  int table;          // of its token and unit
+  int turned;
+};
+
+template <typename T, int W, bool HALF>
+__global__ void __launch_bounds__(kThreads, kPerSm) rotary_kernel(const RotaryArgs a) {
+  extern __shared__ __align__(16) float2 table[];
+  constexpr int kAhead = W * sizeof(T) >= 32 ? kUnderWay / 2 : kUnderWay;  // units of a thread under way
   pdl_wait_then_release();
-  constexpr int kWide = VEC ? 8 : 1;
-  const uint64_t at = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  const uint32_t units = a.turned_units + a.copied_units;
-  const uint32_t each = units * a.chunks;  // threads of a token
-  const uint64_t token = at / each;
-  if (token >= a.tokens) return;
-  const uint32_t rest = (uint32_t)(at - token * each);
-  const uint32_t chunk = rest / units, unit = rest - chunk * units;
-  const int h0 = (int)chunk * kHeads;
-  const int live = min(kHeads, (int)(a.q.heads + a.k.heads) - h0);
-  if (unit >= a.turned_units) {
-    const uint32_t col = 2 * a.pairs + (unit - a.turned_units) * kWide;
-    for (int i = 0; i < live; ++i) {
-      const Rows r = head_rows(a, token, h0 + i, sizeof(T));
-      const T* in = reinterpret_cast<const T*>(r.in) + col;
-      T* out = reinterpret_cast<T*>(r.out) + col;
-      if constexpr (VEC) {
-        float v[8];
-        load8(in, v);
-        store8(out, v);
-      } else {
-        *out = *in;
-      }
+  const int units = a.units, pairs = (int)a.pairs, dim = (int)a.head_dim;
+  const int turned_units = (pairs + W - 1) / W, held = turned_units * W;  // pairs in the table
+  // tokens [t0, t0 + tokens), heads [h0, h0 + heads) of the queries' and then the keys'
+  const size_t t0 = (size_t)blockIdx.x * a.block_tokens;
+  const int tokens = (int)min((size_t)a.block_tokens, a.tokens - t0);
+  const int h0 = blockIdx.y * a.block_heads;
+  const int heads = min(a.block_heads, (int)(a.q.heads + a.k.heads) - h0);
+  const int all = tokens * heads * units;
+
+  // the thread's unit, and the step to its next one
+  int u = threadIdx.x % units, h = threadIdx.x / units, t = h / heads;
+  h -= t * heads;
+  const int du = kThreads % units, dh = kThreads / units % heads,
+            dt = kThreads / units / heads;
+  auto advance = [&] {
+    u += du;
+    h += dh;
+    t += dt;
+    if (u >= units) {
+      u -= units;
+      ++h;
     }
-    return;
-  }
-  // first and second elements of the unit's pairs
-  const uint32_t first = HALF ? unit * kWide : 2 * unit * kWide;
-  const uint32_t second = HALF ? first + a.pairs : first + kWide;
-  float x[kHeads][kWide], y[kHeads][kWide];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (i < live) {
-      const T* in = reinterpret_cast<const T*>(head_rows(a, token, h0 + i, sizeof(T)).in);
-      if constexpr (VEC) {
-        load8(in + first, x[i]);
-        load8(in + second, y[i]);
-      } else {
-        x[i][0] = to_f32(in[first]);
-        y[i][0] = to_f32(in[second]);
-      }
+    if (h >= heads) {
+      h -= heads;
+      ++t;
     }
-  }
-  float s[kWide], c[kWide];
-  const uint64_t position = position_of(a, token);
+  };
+  auto begin = [&](Unit<T, W>& w) {
+    const int head = h0 + h;
+    const bool key = head >= (int)a.q.heads;
+    const RotaryRows& r = key ? a.k : a.q;
+    const size_t at = key ? head - (int)a.q.heads : head;
+    const T* in = static_cast<const T*>(r.in) + (t0 + t) * r.in_token + at * r.in_head;
+    w.out = static_cast<T*>(r.out) + (t0 + t) * r.out_token + at * r.out_head;
+    w.turned = min(W, pairs - u * W);
+    w.table = t * held + (W == 1 ? u : 2 * u);
+    if (HALF) {
+      w.first = w.turned > 0 ? u * W : 2 * pairs + (u - turned_units) * 2 * W;
+      w.second = w.turned > 0 ? w.first + pairs : w.first + W;
+    } else {
+      w.first = u * 2 * W;
+      w.second = w.first + W;
+    }
+    w.x.load(in + w.first);
+    if (w.second < dim) w.y.load(in + w.second);
+  };
+  auto finish = [&](Unit<T, W>& w) {
+    if (w.turned > 0) {
+      float c[W], s[W];
+      if constexpr (W == 1) {
+        c[0] = table[w.table].x;
+        s[0] = table[w.table].y;
+      } else {
 #pragma unroll
-  for (int e = 0; e < kWide; ++e)
-    sine_cosine(position, a.turns[unit * kWide + e], a.scale, s[e], c[e]);
-  if (a.inverse)
-#pragma unroll
-    for (int e = 0; e < kWide; ++e) s[e] = -s[e];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (i < live) {
-      T* out = reinterpret_cast<T*>(head_rows(a, token, h0 + i, sizeof(T)).out);
-      float u[kWide], v[kWide];
-      if constexpr (HALF || !VEC) {
-#pragma unroll
-        for (int e = 0; e < kWide; ++e) {
-          u[e] = x[i][e] * c[e] - y[i][e] * s[e];
-          v[e] = x[i][e] * s[e] + y[i][e] * c[e];
-        }
-      } else {  // neighbours: x holds the first four pairs, y the others
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          u[2 * e] = x[i][2 * e] * c[e] - x[i][2 * e + 1] * s[e];
-          u[2 * e + 1] = x[i][2 * e] * s[e] + x[i][2 * e + 1] * c[e];
-          v[2 * e] = y[i][2 * e] * c[4 + e] - y[i][2 * e + 1] * s[4 + e];
-          v[2 * e + 1] = y[i][2 * e] * s[4 + e] + y[i][2 * e + 1] * c[4 + e];
+        for (int e = 0; e < W; e += 2) {
+          const float4 f = *reinterpret_cast<const float4*>(&table[w.table + e * turned_units]);
+          c[e] = f.x;
+          s[e] = f.y;
+          c[e + 1] = f.z;
+          s[e + 1] = f.w;
         }
       }
-      if constexpr (VEC) {
-        store8(out + first, u);
-        store8(out + second, v);
-      } else {
-        from_f32(u[0], out[first]);
-        from_f32(v[0], out[second]);
+      float x[W], y[W];
+      if constexpr (HALF) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float p = w.x.get(e), q = w.y.get(e);
+          x[e] = p * c[e] - q * s[e];
+          y[e] = p * s[e] + q * c[e];
+        }
+      } else {  // x and y are neighbours; their pairs past the last stay
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int i = 2 * e % W, j = (2 * e + 1) % W;
+          const bool lower = 2 * e < W, low_j = 2 * e + 1 < W;
+          const float p = lower ? w.x.get(i) : w.y.get(i), q = low_j ? w.x.get(j) : w.y.get(j);
+          const float up = e < w.turned ? p * c[e] - q * s[e] : p;
+          const float uq = e < w.turned ? p * s[e] + q * c[e] : q;
+          if (lower) x[i] = up;
+          else y[i] = up;
+          if (low_j) x[j] = uq;
+          else y[j] = uq;
+        }
       }
+      w.x.set(x);
+      w.y.set(y);
     }
+    w.x.store(w.out + w.first);
+    if (w.second < dim) w.y.store(w.out + w.second);
+  };
+
+  bool made = false;
+  for (int n = threadIdx.x; n - (int)threadIdx.x < all; n += kAhead * kThreads) {
+    Unit<T, W> w[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (n + k * kThreads < all) begin(w[k]);
+      advance();
+    }
+    if (!made) {
+      for (int i = threadIdx.x; i < tokens * held; i += kThreads) {
+        const int token = i / held, pair = i - token * held;
+        float s = 0.f, c = 1.f;
+        if (pair < pairs) {
+          // half turns in [-1, 1)
+          const uint64_t left = position_of(a, t0 + token) * a.turns[pair];
+          sincospif((float)(int32_t)(left >> 32) * 0x1p-31f, &s, &c);
+        }
+        table[token * held + table_at<W>(pair, turned_units)] =
+            make_float2(a.scale * c, a.inverse ? -a.scale * s : a.scale * s);
+      }
+      __syncthreads();
+      made = true;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (n + k * kThreads < all) finish(w[k]);
   }
 }
 
-template <typename T>
+// A block has one unit for each thread where that is what fills the card, up to
+// kShare where there are enough.
+template <typename T, int W, bool HALF>
 cudaError_t launch_of(RotaryArgs& a, cudaStream_t stream) {
-  const size_t wide = a.vec ? 8 : 1;
-  a.turned_units = (uint32_t)(a.pairs / wide);
-  a.copied_units = a.copies ? (uint32_t)((a.head_dim - 2 * a.pairs) / wide) : 0;
-  a.chunks = (uint32_t)((a.q.heads + a.k.heads + kHeads - 1) / kHeads);
-  const size_t threads = a.tokens * (a.turned_units + a.copied_units) * a.chunks;
-  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
-  auto kernel = a.vec ? a.half ? rotary_kernel<T, true, true> : rotary_kernel<T, true, false>
-                      : a.half ? rotary_kernel<T, false, true> : rotary_kernel<T, false, false>;
-  return launch_kernel(kernel, grid, dim3(kThreads), 0, stream, a);
+  const size_t heads = a.q.heads + a.k.heads, pairs = a.pairs;
+  const size_t turned = (pairs + W - 1) / W, rest = a.head_dim - 2 * pairs;
+  a.units = (int)(!a.copies ? turned
+                  : HALF    ? turned + (rest + 2 * W - 1) / (2 * W)
+                            : (a.head_dim + 2 * W - 1) / (2 * W));
+  const size_t per_token = heads * a.units;
+  const size_t want = std::min<size_t>(
+      kShare * kThreads, std::max<size_t>(kThreads, a.tokens * per_token / (sm_count() * 6)));
+  size_t most = std::max<size_t>(1, kTableBytes / (turned * W * sizeof(float2)));
+  a.block_tokens = (int)std::min(most, std::max<size_t>(1, want / per_token));
+  a.block_heads = (int)heads;
+  size_t splits = 1;
+  if (per_token > want) {
+    splits = std::min<size_t>(65535, std::min(heads, (per_token + want - 1) / want));
+    a.block_heads = (int)((heads + splits - 1) / splits);
+    splits = (heads + a.block_heads - 1) / a.block_heads;
+  }
+  const dim3 grid((unsigned)((a.tokens + a.block_tokens - 1) / a.block_tokens), (unsigned)splits);
+  const size_t shared = a.block_tokens * turned * W * sizeof(float2);
+  return launch_kernel(rotary_kernel<T, W, HALF>, grid, dim3(kThreads), shared, stream, a);
+}
+template <typename T, int W>
+cudaError_t launch_wide(RotaryArgs& a, cudaStream_t stream) {
+  return a.half ? launch_of<T, W, true>(a, stream) : launch_of<T, W, false>(a, stream);
+}
+template <typename T>
+cudaError_t launch_type(RotaryArgs& a, cudaStream_t stream) {
+  switch (a.wide) {
+    case 8: return launch_wide<T, 8>(a, stream);
+    case 4: return launch_wide<T, 4>(a, stream);
+    case 2: return launch_wide<T, 2>(a, stream);
+  }
+  return launch_wide<T, 1>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(RotaryArgs a, cudaStream_t stream) {
-  return a.type == RCC_F32 ? launch_of<float>(a, stream) : launch_of<__nv_bfloat16>(a, stream);
+  return a.type == RCC_F32 ? launch_type<float>(a, stream) : launch_type<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace lm

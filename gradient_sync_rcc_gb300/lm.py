@@ -266,6 +266,8 @@ class AdamWPlan:
                 self.workspace.data_ptr(), need, torch.cuda.current_stream().cuda_stream,
                 C.byref(handle)))
         self.handle = handle.value
+        # the last step's gradient norm: float64, on the device, written by each step
+        self.grad_norm = self.workspace[8:16].view(torch.float64)[0]
 
     @staticmethod
     def _complete(t, states):
@@ -296,11 +298,6 @@ class AdamWPlan:
                 ("exp_avg_sq_scale" in t) != (eight == torch.float8_e4m3fn):
             raise ValueError("a tensor needs a grad, and scales for 8-bit states alone")
         return t
-
-    @property
-    def grad_norm(self):
-        """The last step's gradient norm: float64, on the device."""
-        return self.workspace[8:16].view(torch.float64)[0]
 
     def __del__(self):
         if self.handle is not None:

@@ -350,6 +350,23 @@ def test_guards():
                 assert torch.equal(t["grad"], grad)
 
 
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("kinds", [(F32, BF16, BF16), (BF16, BF16, BF16), (F32, F32, F32)])
+def test_many_pieces(eight, kinds):
+    """Blocks take whole pieces and edges of several tensors, of one or both types."""
+    g = defs.gen(91)
+    sizes = [2048 * 700, 5, 2048, 4096 * 300 + 17, 100, 2049, 6144, 4096, 2047] * 2
+    tensors = [make(g, n, kinds[i % 3], eight, i % 2 == 1, offset=2 if i == 6 else 0)
+               for i, n in enumerate(sizes)]
+    plan = rcc.AdamWPlan(tensors, seed=3, step=1)
+    powers = Powers(CFG["betas"], 1)
+    for k in range(2):
+        now = powers.next()
+        want = [expected(t, i, CFG, 1.0, 1 + k, 3, 1.0, now) for i, t in enumerate(tensors)]
+        rcc.adamw_step(plan, rcc.adamw_cfg(max_grad_norm=0.0, **CFG))
+        same(tensors, want)
+
+
 def test_thousands_of_tensors():
     g = defs.gen(87)
     sizes = [1 + (i * i * 31) % 700 for i in range(2500)]
