@@ -90,7 +90,7 @@ def binding_command(out: str):
             "-isystem", os.path.join(torch_dir, "include"),
             "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
             "-isystem", cuda, os.path.join(CSRC, "lm_binding.cpp"), "-o", out,
-            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cuda", "-ltorch_cpu", "-ltorch_python",
             "-Wl,-rpath," + lib]
 
 

@@ -187,20 +187,36 @@ __device__ __forceinline__ void add_range(const AdamWTensor& t, uint64_t begin, 
   }
 }
 
-// The tensors' pieces within the block's items, one after the other
-template <typename F>
-__device__ __forceinline__ void for_each_range(const AdamWArgs& a, F f) {
+// Where a block's items begin.  The tables do not change between steps, so they
+// are read before the kernel ahead is through.
+struct Start {
+  uint64_t items;
+  AdamWItem item;
+  AdamWTensor tensor;
+};
+__device__ __forceinline__ Start start_of(const AdamWArgs& a) {
+  Start s;
   uint64_t lo, hi;
   range_of(a.num_items, lo, hi);
-  AdamWItem it = a.items[lo];
-  while (lo < hi) {
-    const AdamWTensor t = a.tensors[it.tensor];
+  s.items = hi - lo;
+  s.item = a.items[lo];
+  s.tensor = a.tensors[s.item.tensor];
+  return s;
+}
+// The tensors' pieces within the block's items, one after the other
+template <typename F>
+__device__ __forceinline__ void for_each_range(const AdamWArgs& a, const Start& s, F f) {
+  AdamWItem it = s.item;
+  AdamWTensor t = s.tensor;
+  for (uint64_t items = s.items;;) {
     const uint64_t begin = (uint64_t)it.chunk * kAdamWItem;
     const uint64_t left = (t.numel - begin + kAdamWItem - 1) / kAdamWItem;  // items of the tensor
-    const uint64_t take = min(left, hi - lo);
+    const uint64_t take = min(left, items);
     f(t, begin, min(begin + take * kAdamWItem, t.numel));
-    lo += take;
+    items -= take;
+    if (items == 0) return;
     it = {it.tensor + 1, 0};
+    t = a.tensors[it.tensor];
   }
 }
 
@@ -273,16 +289,17 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const 
   __shared__ unsigned long long bads[kThreads / 32];
   __shared__ Powers powers;
   __shared__ bool last;
+  const Start start = start_of(a);
   pdl_wait_then_release();
   Squares s;
-  for_each_range(a, [&](const AdamWTensor& t, uint64_t begin, uint64_t end) {
+  for_each_range(a, start, [&](const AdamWTensor& t, uint64_t begin, uint64_t end) {
     add_range(t, begin, end, s);
   });
   double sum = s.value();
   unsigned long long bad = 0;
   if (!s.sound()) {
     WideSquares w;
-    for_each_range(a, [&](const AdamWTensor& t, uint64_t begin, uint64_t end) {
+    for_each_range(a, start_of(a), [&](const AdamWTensor& t, uint64_t begin, uint64_t end) {
       // the same elements of this thread
       uint64_t from = begin;
       if (t.vec) {
@@ -547,8 +564,7 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
   u.v8 = hold<true>(v, number, u.vs);
 }
 
-// fp32 states: a thread's loads are bytes enough by themselves.  The tables do
-// not change between steps, so they are read before the norm is there.
+// fp32 states: a thread's loads are bytes enough by themselves.
 template <bool BF16>
 __device__ __forceinline__ void update_item(const AdamWArgs& a, const AdamWDecision& d,
                                             const AdamWTensor& t, uint32_t chunk) {

@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -112,8 +112,10 @@ float* floats(const at::Tensor& t, const char* what, at::Device dev, int64_t n) 
   return static_cast<float*>(t.data_ptr());
 }
 
+// What at::empty comes to, without the 0.5 to 1 us of its way there (three new
+// tensors, forward with a kept input: 6.0 us of host time a call instead of 7.5)
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 // The caller's output, checked, or a new one
 at::Tensor output(PyObject* o, const char* what, at::IntArrayRef shape, at::ScalarType type,

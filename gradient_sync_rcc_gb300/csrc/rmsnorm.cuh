@@ -448,6 +448,8 @@ struct NormBack {
   static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kBackStages ? kFit : kBackStages) : 0;
   static constexpr int kShared = kWeight + kStages * kStage;
   static constexpr int kPerSm = blocks_per_sm(kStages ? kBackThreads : kBackDirect, kThreads, kShared);
+  // a block's rows of partial sums are added up where the weight was
+  static constexpr bool kJoin = (MORE & kAdd) != 0 && kThreads > G && kHoldWeight;
 };
 
 // Rows are dealt to the blocks in turn; a thread keeps the weight gradient of
@@ -633,9 +635,29 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
     stage = stage + 1 >= kStages ? 0 : stage + 1;
     flip ^= 1;
   }
-  // one row of partial sums for each group of threads
+  // one row of partial sums for each group of threads; with kAdd for each block,
+  // whose groups' sums are added first (1,023 rows of 1,000 fp32 columns: 256 rows
+  // left to norm_dweight_kernel instead of 1,024)
   const int ld = groups * (int)kKeepGroup;
   float* part = static_cast<float*>(a.workspace) + ((size_t)blockIdx.x * kRows + tid / G) * ld + col;
+  if constexpr (B::kJoin) {
+    __syncthreads();  // the weight is read no more
+    auto held = [&](int group, int p, int e) {
+      return reinterpret_cast<float2*>(smem) + ((group * kParts + p) * P::kPairs + e) * G + t;
+    };
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int e = 0; e < P::kPairs; ++e) *held(tid / G, p, e) = acc[p][e];
+    __syncthreads();
+    if (tid >= G) return;
+    for (int r = 1; r < kRows; ++r)
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int e = 0; e < P::kPairs; ++e) acc[p][e] = add2(acc[p][e], *held(r, p, e));
+    part = static_cast<float*>(a.workspace) + (size_t)blockIdx.x * ld + col;
+  }
 #pragma unroll
   for (int p = 0; p < kParts; ++p) {
     if (left <= p * kSpan) continue;
@@ -735,9 +757,9 @@ cudaError_t forward_of(const NormArgs& a, cudaStream_t stream) {
   });
 }
 
-// *blocks: blocks launched, each of which leaves its rows of partial sums
+// *rows: rows of partial sums that the blocks leave
 template <typename T, bool VEC, int MORE>
-cudaError_t backward_of(const NormGradArgs& a, cudaStream_t stream, size_t* blocks) {
+cudaError_t backward_of(const NormGradArgs& a, cudaStream_t stream, size_t* rows) {
   const NormShape s = norm_shape(a.dim);
   return with_shape(s, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value;
@@ -748,8 +770,9 @@ cudaError_t backward_of(const NormGradArgs& a, cudaStream_t stream, size_t* bloc
       const cudaError_t e = allow_shared(kernel, B::kShared, allowed);
       if (e != cudaSuccess) return e;
     }
-    *blocks = norm_blocks(a.tokens, s, B::kPerSm);
-    return launch_kernel(kernel, dim3((unsigned)*blocks), dim3(B::kThreads), B::kShared, stream, a);
+    const size_t blocks = norm_blocks(a.tokens, s, B::kPerSm);
+    *rows = B::kJoin ? blocks : blocks * norm_rows_per_block(s);
+    return launch_kernel(kernel, dim3((unsigned)blocks), dim3(B::kThreads), B::kShared, stream, a);
   });
 }
 
@@ -767,21 +790,19 @@ cudaError_t forward_with(const NormArgs& a, cudaStream_t stream) {
 template <int MORE>
 cudaError_t backward_with(const NormGradArgs& a, cudaStream_t stream, uint64_t* launches) {
   cudaError_t e;
-  size_t blocks = 0;
+  size_t rows = 0;
   if (a.type == RCC_F32)
-    e = a.vec ? backward_of<float, true, MORE>(a, stream, &blocks)
-              : backward_of<float, false, MORE>(a, stream, &blocks);
+    e = a.vec ? backward_of<float, true, MORE>(a, stream, &rows)
+              : backward_of<float, false, MORE>(a, stream, &rows);
   else
-    e = a.vec ? backward_of<__nv_bfloat16, true, MORE>(a, stream, &blocks)
-              : backward_of<__nv_bfloat16, false, MORE>(a, stream, &blocks);
+    e = a.vec ? backward_of<__nv_bfloat16, true, MORE>(a, stream, &rows)
+              : backward_of<__nv_bfloat16, false, MORE>(a, stream, &rows);
   if (e != cudaSuccess) return e;
-  const NormShape s = norm_shape(a.dim);
   const size_t ld = (a.dim + kKeepGroup - 1) / kKeepGroup * kKeepGroup;
   e = launch_kernel(norm_dweight_kernel, dim3((unsigned)((a.dim + kSumCols - 1) / kSumCols)),
                     dim3(kSumCols * kSumRows), 0, stream,
-                    static_cast<const float*>(a.workspace),
-                    blocks * norm_rows_per_block(s), ld,
-                    a.dweight, a.dim, a.accumulate);
+                    static_cast<const float*>(a.workspace), rows, ld, a.dweight, a.dim,
+                    a.accumulate);
   if (e == cudaSuccess) *launches = 2;
   return e;
 }
