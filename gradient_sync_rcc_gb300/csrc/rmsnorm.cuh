@@ -223,7 +223,11 @@ __device__ __forceinline__ void store_bytes(int8_t* p, int left, const uint32_t 
 // 4,095 columns, not copied ahead: 512 threads 137 (198), 768 108 (154), 1,024
 // 111 (152).
 // So the forward pass copies rows of 2-byte types ahead; an fp32 row is as many
-// loads in flight by itself.
+// loads in flight by itself.  With an output in 8 bits there is more to do between
+// a row's loads and its last store, and fp32 rows are copied ahead too: with the
+// residual 150 us (5.8 TB/s; 143 of 8,192 columns) instead of 182 (234).  The
+// residual alone, kept in 8 bits: 180 us as they are (6.3 TB/s), 186 copied ahead;
+// bf16 97 us (6.3 TB/s), and 76 with the output in 8 bits.
 constexpr int kForeThreads = 2048, kForeStages = 2, kForeDirect = 4096;
 constexpr int kBackThreads = 512, kBackStages = 3, kBackDirect = 768;
 constexpr int kSharedMost = 220 * 1024;   // of all blocks of one SM
@@ -244,7 +248,8 @@ struct NormFore {
   static constexpr int kRow = kThreads * kParts * 16;  // of one input
   static constexpr int kStage = MORE & kAdd ? 2 * kRow : kRow;
   static constexpr int kFit = kSharedMost / kStage;
-  static constexpr int kStages = VEC && sizeof(T) == 2 && kFit >= kForeStages ? kForeStages : 0;
+  static constexpr int kStages =
+      VEC && (sizeof(T) == 2 || (MORE & kEight)) && kFit >= kForeStages ? kForeStages : 0;
   static constexpr int kShared = kStages * kStage;
   static constexpr int kPerSm = blocks_per_sm(kStages ? kForeThreads : kForeDirect, kThreads, kShared);
 };
