@@ -107,6 +107,31 @@ struct WideSquares {
   }
 };
 
+// Eight fp32 values, on a boundary of 32 bytes (wide) or 16
+__device__ __forceinline__ void load_eight(const float* p, bool wide, float (&v)[kUnit]) {
+  if (wide) {
+    load8(p, v);
+    return;
+  }
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = a.z;
+  v[3] = a.w;
+  v[4] = b.x;
+  v[5] = b.y;
+  v[6] = b.z;
+  v[7] = b.w;
+}
+__device__ __forceinline__ void store_eight(float* p, bool wide, const float (&v)[kUnit]) {
+  if (wide) {
+    store8(p, v);
+    return;
+  }
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 // Eight gradients as they lie in memory
 template <bool BF16>
 struct Raw {
@@ -128,12 +153,12 @@ __device__ __forceinline__ void set_wide(Raw<false>& r, const uint4& v) {  // of
     r.w[2 * i + 1] = w[i] & 0xFFFF0000u;
   }
 }
-__device__ __forceinline__ void load_raw(const void* grad, uint64_t i, Raw<true>& r) {
+__device__ __forceinline__ void load_raw(const void* grad, uint64_t i, bool, Raw<true>& r) {
   set_words(r, 0, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(grad) + i));
 }
-__device__ __forceinline__ void load_raw(const void* grad, uint64_t i, Raw<false>& r) {
+__device__ __forceinline__ void load_raw(const void* grad, uint64_t i, bool wide, Raw<false>& r) {
   float f[8];
-  load8(static_cast<const float*>(grad) + i, f);
+  load_eight(static_cast<const float*>(grad) + i, wide, f);
 #pragma unroll
   for (int e = 0; e < 8; ++e) r.w[e] = __float_as_uint(f[e]);
 }
@@ -148,8 +173,8 @@ __device__ __forceinline__ float2 pair_of(const Raw<false>& r, int i) {
 
 // Elements [begin, end) of a tensor, begin on a whole item
 template <bool BF16>
-__device__ __forceinline__ void add_vectors(const void* grad, uint64_t begin, uint64_t vectors,
-                                            Squares& s) {
+__device__ __forceinline__ void add_vectors(const void* grad, bool wide, uint64_t begin,
+                                            uint64_t vectors, Squares& s) {
   constexpr int kAhead = BF16 ? 2 * kNormAhead : kNormAhead;  // vectors of a thread under way
   for (uint64_t v = threadIdx.x; v < vectors; v += kAhead * kThreads) {
     Raw<BF16> r[kAhead];
@@ -157,7 +182,7 @@ __device__ __forceinline__ void add_vectors(const void* grad, uint64_t begin, ui
     for (int k = 0; k < kAhead; ++k) {
 #pragma unroll
       for (int e = 0; e < Raw<BF16>::kWords; ++e) r[k].w[e] = 0u;
-      if (v + k * kThreads < vectors) load_raw(grad, begin + (v + k * kThreads) * kUnit, r[k]);
+      if (v + k * kThreads < vectors) load_raw(grad, begin + (v + k * kThreads) * kUnit, wide, r[k]);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -175,9 +200,9 @@ __device__ __forceinline__ void add_range(const AdamWTensor& t, uint64_t begin, 
   if (t.vec) {
     const uint64_t vectors = (end - begin) / kUnit;
     if (t.bf16)
-      add_vectors<true>(t.grad, begin, vectors, s);
+      add_vectors<true>(t.grad, true, begin, vectors, s);
     else
-      add_vectors<false>(t.grad, begin, vectors, s);
+      add_vectors<false>(t.grad, t.wide, begin, vectors, s);
     from = begin + vectors * kUnit;
   }
   for (uint64_t i = from + threadIdx.x; i < end; i += kThreads) {
@@ -428,20 +453,20 @@ __device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i,
   }
   if (t.vec && i + kUnit <= t.numel) {
     if constexpr (BF16) {
-      load_raw(t.grad, i, u.g);
+      load_raw(t.grad, i, t.wide, u.g);
     } else if (t.bf16) {
       set_wide(u.g, *reinterpret_cast<const uint4*>(
                         static_cast<const __nv_bfloat16*>(t.grad) + i));
     } else {
-      load_raw(t.grad, i, u.g);
+      load_raw(t.grad, i, t.wide, u.g);
     }
-    load8(t.param + i, u.p);
+    load_eight(t.param + i, t.wide, u.p);
     if constexpr (EIGHT) {
       u.m8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
       u.v8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
     } else {
-      load8(static_cast<const float*>(t.m) + i, u.m);
-      load8(static_cast<const float*>(t.v) + i, u.v);
+      load_eight(static_cast<const float*>(t.m) + i, t.wide, u.m);
+      load_eight(static_cast<const float*>(t.v) + i, t.wide, u.v);
     }
     return;
   }
@@ -480,14 +505,14 @@ __device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i,
     }
   }
   if (t.vec && i + kUnit <= t.numel) {
-    store8(t.param + i, u.p);
+    store_eight(t.param + i, t.wide, u.p);
     if (t.copy) store8(t.copy + i, u.p);
     if constexpr (EIGHT) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = u.m8;
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = u.v8;
     } else {
-      store8(static_cast<float*>(t.m) + i, u.m);
-      store8(static_cast<float*>(t.v) + i, u.v);
+      store_eight(static_cast<float*>(t.m) + i, t.wide, u.m);
+      store_eight(static_cast<float*>(t.v) + i, t.wide, u.v);
     }
     return;
   }

@@ -128,9 +128,10 @@ struct AdamWTensor {
   float *m_scales, *v_scales;
   __nv_bfloat16* copy;        // or NULL
   uint64_t numel;
-  uint16_t bf16;              // the gradient's type
-  uint8_t vec;                // every buffer on a boundary of eight elements
-  uint8_t bulk;               // and the 8-bit states on one of 16 bytes
+  uint8_t bf16;               // the gradient's type
+  uint8_t vec;                // every buffer on a boundary of 16 bytes (8-bit states of 8)
+  uint8_t wide;               // and the fp32 ones of 32
+  uint8_t bulk;               // vec, and the 8-bit states on one of 16 bytes
 };
 struct AdamWItem {
   uint32_t tensor, chunk;

@@ -80,9 +80,10 @@ rcc_status check_tensor(const rcc_adamw_tensor& t, int i, bool eight) {
   return RCC_OK;
 }
 
-bool vectors_of(const rcc_adamw_tensor& t, bool eight) {
-  const size_t state = eight ? 8 : 32;
-  return on(t.grad, t.grad_type == RCC_BF16 ? 16 : 32) && on(t.param, 32) &&
+// Vectors of eight elements: fp32 ones on boundaries of `fp32` bytes
+bool vectors_of(const rcc_adamw_tensor& t, bool eight, size_t fp32) {
+  const size_t state = eight ? 8 : fp32;
+  return on(t.grad, t.grad_type == RCC_BF16 ? 16 : fp32) && on(t.param, fp32) &&
          on(t.exp_avg, state) && on(t.exp_avg_sq, state) && on(t.copy, 16);
 }
 
@@ -156,7 +157,8 @@ rcc_status create(const rcc_adamw_tensor* tensors, int n, uint32_t seed, int64_t
     d.copy = static_cast<__nv_bfloat16*>(t.copy);
     d.numel = t.numel;
     d.bf16 = t.grad_type == RCC_BF16;
-    d.vec = vectors_of(t, eight);
+    d.vec = vectors_of(t, eight, 16);
+    d.wide = vectors_of(t, eight, 32);
     d.bulk = d.vec && on(t.exp_avg, 16) && on(t.exp_avg_sq, 16);
     const size_t chunks = (t.numel + kAdamWItem - 1) / kAdamWItem;
     for (size_t c = 0; c < chunks; ++c) *item++ = {(uint32_t)i, (uint32_t)c};

@@ -232,32 +232,28 @@ class AdamWPlan:
     saved with the report's step, and given again with that step, they resume.
 
     The tensors' addresses are kept: a step reads the gradients where they were.
-    The plan is made on `stream`; steps on another one have to wait for it."""
+    The plan and the states it makes belong to `stream`; steps on another one have
+    to wait for it.  One step after the other: a plan's steps, and graphs of them,
+    share its workspace."""
 
     def __init__(self, tensors, states=torch.float32, seed=0, step=0, betas=(0.9, 0.999),
                  stream=None):
         self.handle = None
-        self.tensors = [self._complete(dict(t), states) for t in tensors]
-        if not self.tensors:
+        if states not in (torch.float32, torch.float8_e4m3fn):
+            raise ValueError("states must be torch.float32 or torch.float8_e4m3fn")
+        tensors = [self._checked(i, t, states) for i, t in enumerate(tensors)]
+        if not tensors:
             raise ValueError("no tensors")
-        dev = self.tensors[0]["param"].device
-        arr = (_rcc.AdamWTensor * len(self.tensors))()
-        for i, t in enumerate(self.tensors):
-            if any(v.device != dev for v in t.values()):
-                raise ValueError("tensor %d: every buffer must be on one device" % i)
-            p = {k: t[k].data_ptr() if k in t else None for k in (
-                "grad", "param", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
-                "copy")}
-            arr[i] = _rcc.AdamWTensor(
-                t["param"].numel(), p["grad"],
-                _rcc.BF16 if t["grad"].dtype == torch.bfloat16 else _rcc.F32, p["param"],
-                p["exp_avg"], p["exp_avg_sq"], p["exp_avg_scale"], p["exp_avg_sq_scale"],
-                p["copy"])
+        dev = tensors[0]["param"].device
+        if any(v.device != dev for t in tensors for v in t.values()):
+            raise ValueError("every buffer must be on one device")
         if dev.type != "cuda":
             raise ValueError("the operators take tensors on a CUDA device")
         _lm.check_device(dev.index, torch.cuda.current_device())
         self.device = dev.index
         with _lm_stream(stream, dev):
+            self.tensors = [self._with_states(t, states) for t in tensors]
+            arr = (_rcc.AdamWTensor * len(self.tensors))(*map(self._entry, self.tensors))
             need = _lib.rcc_adamw_workspace(arr, len(arr))
             self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             handle = C.c_void_p()
@@ -270,37 +266,56 @@ class AdamWPlan:
         self.grad_norm = self.workspace[8:16].view(torch.float64)[0]
 
     @staticmethod
-    def _complete(t, states):
-        param = t["param"]
-        n = param.numel()
-        if states not in (torch.float32, torch.float8_e4m3fn):
-            raise ValueError("states must be torch.float32 or torch.float8_e4m3fn")
-        t = {k: v for k, v in t.items() if v is not None}
-        for k in ("exp_avg", "exp_avg_sq"):
-            if k not in t:
-                t[k] = torch.zeros(n, dtype=torch.uint8, device=param.device).view(states) \
-                    if states == torch.float8_e4m3fn else torch.zeros_like(param)
-            if t[k].dtype == torch.float8_e4m3fn and k + "_scale" not in t:
-                t[k + "_scale"] = torch.zeros(-(-n // 128), device=param.device)
-        eight = t["exp_avg"].dtype
-        want = {"param": (n, (torch.float32,)), "grad": (n, (torch.float32, torch.bfloat16)),
-                "exp_avg": (n, (torch.float32, torch.float8_e4m3fn)), "exp_avg_sq": (n, (eight,)),
-                "copy": (n, (torch.bfloat16,)), "exp_avg_scale": (-(-n // 128), (torch.float32,)),
-                "exp_avg_sq_scale": (-(-n // 128), (torch.float32,))}
+    def _checked(i, given, states):
+        t = {k: v for k, v in given.items() if v is not None}
+        if "param" not in t or "grad" not in t:
+            raise ValueError("tensor %d lacks a param or grad" % i)
+        n = t["param"].numel()
+        kind = t["exp_avg"].dtype if "exp_avg" in t else states
+        f32, scales = (torch.float32,), -(-n // 128)
+        want = {"param": (n, f32), "grad": (n, (torch.float32, torch.bfloat16)),
+                "copy": (n, (torch.bfloat16,)),
+                "exp_avg": (n, (torch.float32, torch.float8_e4m3fn)), "exp_avg_sq": (n, (kind,))}
+        if kind == torch.float8_e4m3fn:
+            want |= {"exp_avg_scale": (scales, f32), "exp_avg_sq_scale": (scales, f32)}
+            # values without the scales that they were held with mean nothing
+            if any((k in t) != (k + "_scale" in t) for k in ("exp_avg", "exp_avg_sq")):
+                raise ValueError("tensor %d: 8-bit states come with their scales" % i)
         for k, v in t.items():
             if k not in want:
-                raise ValueError("%r is not a buffer of AdamW" % k)
+                raise ValueError("tensor %d: %r is not a buffer of AdamW, or not of its states"
+                                 % (i, k))
             count, types = want[k]
             if v.numel() != count or v.dtype not in types or not v.is_contiguous():
-                raise ValueError("%s must be %d contiguous elements of %s"
-                                 % (k, count, " or ".join(map(str, types))))
-        if "grad" not in t or ("exp_avg_scale" in t) != (eight == torch.float8_e4m3fn) or \
-                ("exp_avg_sq_scale" in t) != (eight == torch.float8_e4m3fn):
-            raise ValueError("a tensor needs a grad, and scales for 8-bit states alone")
+                raise ValueError("tensor %d: %s must be %d contiguous elements of %s"
+                                 % (i, k, count, " or ".join(map(str, types))))
         return t
 
+    @staticmethod
+    def _with_states(t, states):
+        param = t["param"].detach()
+        kind = t["exp_avg"].dtype if "exp_avg" in t else states
+        for k in ("exp_avg", "exp_avg_sq"):
+            if k in t:
+                continue
+            if kind == torch.float32:
+                t[k] = torch.zeros_like(param)
+            else:
+                t[k] = torch.zeros_like(param, dtype=torch.uint8).view(kind)
+                t[k + "_scale"] = torch.zeros(-(-param.numel() // 128), device=param.device)
+        return t
+
+    @staticmethod
+    def _entry(t):
+        p = {k: v.data_ptr() for k, v in t.items()}
+        return _rcc.AdamWTensor(
+            t["param"].numel(), p["grad"],
+            _rcc.BF16 if t["grad"].dtype == torch.bfloat16 else _rcc.F32, p["param"],
+            p["exp_avg"], p["exp_avg_sq"], p.get("exp_avg_scale"), p.get("exp_avg_sq_scale"),
+            p.get("copy"))
+
     def __del__(self):
-        if self.handle is not None:
+        if self.handle is not None and _lib is not None:   # None: the interpreter ends
             _lib.rcc_adamw_destroy(self.handle)
             self.handle = None
 
@@ -318,6 +333,8 @@ def _lm_stream(stream, dev):
 def adamw_step(plan, cfg, scale=1.0, stream=None):
     """rcc_adamw_step: one step over a plan's tensors, their gradients carrying
     the loss scale `scale`.  cfg: adamw_cfg.  Nothing is read back."""
+    if not isinstance(cfg, _rcc.AdamWCfg):
+        raise ValueError("cfg must be one of adamw_cfg's")
     _lm.adamw_step(plan.handle, C.addressof(cfg), scale, plan.device, stream)
 
 

@@ -40,9 +40,9 @@ def stir(x):
     return x ^ (x >> 16)
 
 
-def numbers_of(n, tensor, seed, step):
-    """The 16 bits of each element of tensor `tensor`."""
-    i = torch.arange(n, device=DEV)
+def numbers_of(n, tensor, seed, step, start=0):
+    """The 16 bits of the elements [start, start + n) of tensor `tensor`."""
+    i = torch.arange(start, start + n, device=DEV)
     key = stir(torch.tensor(seed, device=DEV) ^ stir(torch.tensor(step & WORD, device=DEV)))
     key = stir((key + tensor * 0x9E3779B9) & WORD)
     h = stir((stir(key ^ (i // 4096)) + i % 4096 // 2) & WORD)
@@ -87,9 +87,10 @@ def const(v):
     return float(torch.tensor(v, dtype=F32))
 
 
-def expected(t, tensor, cfg, scale, step, seed, coef, powers):
-    """New param, states and scales of one tensor.  fp32 states: the documented
-    operations.  8 bits: each as what is the least and the most it may be."""
+def expected(t, tensor, cfg, scale, step, seed, coef, powers, start=0):
+    """New param, states and scales of one tensor (or a part of it, from element
+    `start` on).  fp32 states: the documented operations.  8 bits: each as what is
+    the least and the most it may be."""
     b1, b2 = cfg["betas"]
     f = lambda v: torch.tensor(v, dtype=F32, device=DEV)  # noqa: E731
     n = t["param"].numel()
@@ -118,7 +119,7 @@ def expected(t, tensor, cfg, scale, step, seed, coef, powers):
     dp = size * (dm / denom + 14 * U * m.abs() / denom) * (1 + 16 * U)
     p = t["param"].double() * decay - size * m / denom
     dp = dp + 2 * U * (t["param"].double().abs() + p.abs()) + 2.0 ** -140
-    numbers = numbers_of(n, tensor, seed, step)
+    numbers = numbers_of(n, tensor, seed, step, start)
     out = {"param": (p - dp, p + dp)}
     if "copy" in t:
         out["copy"] = ((p - dp).float().to(BF16).double(), (p + dp).float().to(BF16).double())
@@ -207,7 +208,7 @@ def clone(tensors):
 @pytest.mark.parametrize("grad_type", [F32, BF16])
 @pytest.mark.parametrize("eight", [False, True])
 @pytest.mark.parametrize("copy", [False, True])
-@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("offset", [0, 1, 4, 8, 16])
 def test_steps(grad_type, eight, copy, offset):
     g = defs.gen(81)
     tensors = [make(g, n, grad_type, eight, copy, offset=offset) for n in SIZES]

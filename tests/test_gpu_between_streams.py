@@ -1,0 +1,131 @@
+"""The `stream` argument of the residual norm, rotary positions and AdamW: calls on
+a stream that is not the current one, with outputs and workspaces left out."""
+import pytest
+import torch
+
+import test_gpu_lm as defs
+from gradient_sync_rcc_gb300 import rcc
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+BF16, E4M3 = defs.BF16, torch.float8_e4m3fn
+TOKENS, DIM, HEADS = 900, 520, 5
+DELAY = 20000000   # cycles, about 10 ms: everything queued behind it is still to come
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gradient_sync_rcc_gb300 import build
+    build.build()
+    assert torch.cuda.is_available()
+
+
+class Step:
+    """All calls; `after` runs behind each of them."""
+
+    def __init__(self, seed):
+        g = defs.gen(seed)
+        self.x, self.r = (defs.randn(g, TOKENS, DIM, dtype=BF16) for _ in range(2))
+        self.weight = 1.0 + defs.randn(g, DIM, scale=0.1)
+        self.turns = rcc.rotary_turns(104, device=DEV)
+        self.param, self.start = (torch.empty(DIM, device=DEV) for _ in range(2))
+        self.start.copy_(defs.randn(g, DIM))
+        self.grad = torch.zeros(DIM, device=DEV)
+        torch.cuda.synchronize()
+
+    def run(self, stream=None, after=lambda: None):
+        y, h, kept = rcc.add_rmsnorm_forward(self.x, self.r, self.weight, keep=True, stream=stream)
+        after()
+        y8, _ = rcc.add_rmsnorm_forward(self.x, self.r, self.weight, out_dtype=E4M3, stream=stream)
+        after()
+        q, k = y.view(TOKENS, HEADS, DIM // HEADS), h.view(TOKENS, HEADS, DIM // HEADS)
+        q, k = rcc.rotary_forward(q, k, self.turns, stream=stream)
+        after()
+        dq, dk = rcc.rotary_backward(q, k, self.turns, stream=stream)
+        after()
+        dx, dweight = rcc.add_rmsnorm_backward(dq.view(TOKENS, DIM), dk.view(TOKENS, DIM), kept,
+                                               self.weight, dweight=self.grad, stream=stream)
+        after()
+        return y, h, kept.data, y8.values.view(torch.uint8), y8.scales, q, k, dq, dk, dx, dweight
+
+
+SIZES = [TOKENS * DIM * 2, TOKENS * DIM, TOKENS * 5 * 132, TOKENS * 5 * 4, DIM * 4,
+         rcc.rmsnorm_backward_workspace(TOKENS, DIM)]
+
+
+def overwrite():
+    held = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for n in SIZES * 2]
+    del held
+
+
+@pytest.mark.parametrize("form", ["object", "address"])
+def test_released_blocks_are_not_given_out_while_in_use(form):
+    step = Step(121)
+    want = [t.clone() for t in step.run()]
+    step.grad.fill_(-1.0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(DELAY)
+    got = step.run(side if form == "object" else side.cuda_stream, after=overwrite)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_outputs_are_not_blocks_that_the_current_stream_still_writes():
+    step = Step(122)
+    want = [t.clone() for t in step.run()]
+    step.grad.fill_(-1.0)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(DELAY)
+    overwrite()
+    side = torch.cuda.Stream()
+    got = step.run(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("name", [0, 1])
+def test_adamw_on_a_stream(name):
+    """A plan made and stepped on a side stream, and one on the default stream by
+    its names while another is current: the same bits."""
+    g = defs.gen(123)
+    param, grad = defs.randn(g, 70001), defs.randn(g, 70001, dtype=BF16)
+    cfg = rcc.adamw_cfg(max_grad_norm=1.0)
+    plans = []
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream, current in ((None, None), (side, None), (side.cuda_stream, None), (name, side)):
+        p = param.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            plan = rcc.AdamWPlan([dict(param=p, grad=grad)], states=E4M3, stream=stream)
+            for _ in range(3):
+                rcc.adamw_step(plan, cfg, stream=stream)
+            assert rcc.adamw_report(plan, stream=stream).step == 3
+            assert torch.cuda.current_stream() == (current or torch.cuda.default_stream())
+        plans.append((plan, p))
+    torch.cuda.synchronize()
+    first, p0 = plans[0]
+    for plan, p in plans[1:]:
+        assert torch.equal(p, p0)
+        for k in ("exp_avg", "exp_avg_sq"):
+            assert torch.equal(plan.tensors[0][k].view(torch.uint8),
+                               first.tensors[0][k].view(torch.uint8))
+
+
+def test_a_plan_is_not_made_while_capturing():
+    p, g = torch.zeros(300, device=DEV), torch.zeros(300, device=DEV)
+    plan = rcc.AdamWPlan([dict(param=p, grad=g)])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        with pytest.raises(rcc.RccError, match="capturing"):
+            rcc.AdamWPlan([dict(param=p, grad=g, exp_avg=torch.empty_like(p),
+                                exp_avg_sq=torch.empty_like(p))])
+        rcc.adamw_step(plan, rcc.adamw_cfg())
+    graph.replay()
+    assert rcc.adamw_report(plan).step == 1

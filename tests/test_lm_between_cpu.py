@@ -296,7 +296,10 @@ def test_the_plan_of_the_binding_refuses(L):
               dict(param=p, grad=g.half()), dict(param=p, grad=g, copy=g),
               dict(param=p, grad=g, exp_avg=p.clone(), exp_avg_sq=p.to(E4M3)),
               dict(param=p, grad=g, other=p), dict(param=torch.zeros(20)[::2], grad=g),
-              dict(param=p, grad=g, exp_avg_scale=torch.zeros(1))):
+              dict(param=p, grad=g, exp_avg_scale=torch.zeros(1)), dict(grad=g),
+              dict(param=p, grad=g, exp_avg=p.to(E4M3)),
+              dict(param=p, grad=g, exp_avg=p.to(E4M3), exp_avg_sq=p.to(E4M3),
+                   exp_avg_scale=torch.zeros(1), exp_avg_sq_scale=torch.zeros(2))):
         with pytest.raises(ValueError):
             L.AdamWPlan([t])
     with pytest.raises(ValueError):
@@ -305,3 +308,5 @@ def test_the_plan_of_the_binding_refuses(L):
         L.AdamWPlan([])
     with pytest.raises(ValueError, match="CUDA device"):
         L.AdamWPlan([dict(param=p, grad=g)], states=E4M3)
+    with pytest.raises(ValueError, match="adamw_cfg"):
+        L.adamw_step(None, dict(lr=1.0))
