@@ -409,8 +409,9 @@ rcc_status rcc_grad_stats_noalloc(const float* const* grads, int num_ranks,
  * The ends of a language model, whose gradients are the largest that the
  * gradient sync sees, and the norm between them: the token embedding and its
  * gradient, an RMS norm that keeps its input in 8 bits for the backward pass,
- * and the output layer with softmax cross entropy, which never keeps the
- * logits.  The pages have no counterpart to these calls.
+ * alone and with the residual's addition, rotary positions, and the output layer
+ * with softmax cross entropy, which never keeps the logits.  The pages have no
+ * counterpart to these calls.
  *
  * Shared by all of them:
  *   - Asynchronous on `stream`; no session, no allocation, no
@@ -628,7 +629,8 @@ typedef struct {
   double beta1_power;    /* beta1^step, beta2^step: products of the steps' betas */
   double beta2_power;
   uint32_t nonfinite;    /* gradient elements that are not finite */
-  int32_t skipped;       /* 1: the last step changed nothing */
+  int32_t skipped;       /* 1: the last step changed nothing; -1: a wait inside it ran
+                            out, what it left is not to be used */
   float clip_coef;       /* what it multiplied the gradients by (1: not clipped) */
   uint32_t unused;
 } rcc_adamw_status;

@@ -6,6 +6,8 @@ Its matrix products, attention and activation are torch's.  Against automatic
 differentiation of the same model in 64 bits.
 """
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -222,3 +224,19 @@ def test_one_token_at_a_time():
         ei, _ = rcc.add_rmsnorm_forward(x[i:i + 1], r[i:i + 1], weight, out_dtype=E4M3)
         assert torch.equal(ei.values.view(torch.uint8), y8.values[i:i + 1].view(torch.uint8))
         assert torch.equal(ei.scales, y8.scales[i:i + 1])
+
+
+def test_the_documented_calls_run(capsys):
+    """The front page's example of these operators, as written."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    block = [b for b in re.findall(r"```python\n(.*?)```", open(path).read(), re.S)
+             if "adamw_step" in b]
+    assert len(block) == 1
+    scope = {}
+    exec(compile(block[0], "README.md", "exec"), scope)
+    total = scope["dnorm"].double().square().sum() + \
+        scope["plan"].tensors[0]["grad"].double().square().sum()
+    # printed with 16 digits; the norm is good to 2^-40
+    assert abs(float(capsys.readouterr().out) - math.sqrt(float(total))) < 1e-11 * math.sqrt(float(total))
+    assert torch.equal(scope["w16"], scope["weight"].to(BF16))
+    assert torch.isfinite(scope["dx"]).all() and torch.isfinite(scope["dq"]).all()
