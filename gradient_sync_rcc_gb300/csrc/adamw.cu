@@ -3,7 +3,8 @@
 //   g = grad (1/scale) coef,  coef = max_grad_norm / |g| where that is less than 1
 //   m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2
 //   p = p (1 - lr wd) - lr/(1-b1^t) m / (sqrt(v) / sqrt(1-b2^t) + eps)
-// every operation rounded to fp32 in this order, as rcc_grad_sync_adamw's.
+// With fp32 states every operation is rounded, in the order of
+// rcc_grad_sync_adamw's, whose bits these are.
 //
 // States in 8 bits: m and sqrt(v) (half the range of v, and what is divided by)
 // as e4m3 with one scale for 128 elements, the smallest power of two that holds
@@ -259,11 +260,13 @@ __device__ __forceinline__ void block_sum(double& sum, unsigned long long& bad, 
     bads[threadIdx.x / 32] = bad;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < kThreads / 32) {
+    sum = sums[threadIdx.x];
+    bad = bads[threadIdx.x];
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) {
-      sum += sums[w];
-      bad += bads[w];
+    for (int o = kThreads / 64; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync((1u << kThreads / 32) - 1, sum, o);
+      bad += __shfl_xor_sync((1u << kThreads / 32) - 1, bad, o);
     }
   }
 }
@@ -307,6 +310,15 @@ __device__ __forceinline__ void decide(const AdamWArgs& a, const Powers& p, doub
   a.status->beta2_power = p.beta2;
 }
 
+// Whether the block is the last to arrive: its writes before are there for the
+// last one to read
+__device__ __forceinline__ bool arrive_last(uint32_t* arrived) {
+  uint32_t before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(arrived)
+               : "memory");
+  return before == gridDim.x - 1;
+}
+
 // Each block leaves one row; the last one to do so adds them up, in the rows'
 // order, and decides.
 __global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const AdamWArgs a) {
@@ -341,12 +353,10 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const 
   block_sum(sum, bad, sums, bads);
   if (threadIdx.x == 0) {
     a.rows[blockIdx.x] = {sum, (uint32_t)min(bad, 0xFFFFFFFFull), 0u};
-    __threadfence();
-    last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+    last = arrive_last(a.arrived);
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
   if (threadIdx.x == kThreads - 1) powers = powers_of(a);  // beside the sum
   sum = 0.0;
   bad = 0;

@@ -406,11 +406,10 @@ PyObject* add_rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (eight && !scales.defined()) scales = fresh({m.rows, groups_of(m.cols)}, at::kFloat, dev);
     if (a[5] == Py_True) data = fresh({kept_bytes(m.rows, m.cols)}, at::kByte, dev);
     const Kept k = data.defined() ? kept_in(data, m.rows, m.cols) : Kept{nullptr, nullptr};
-    if (m.rows)  // empty tensors have no addresses to tell apart
-      call(rcc_.add_rmsnorm_forward, x.data_ptr(), (size_t)m.ld, residual, (size_t)mr.ld, kind, w,
-           eps, (size_t)m.rows, (size_t)m.cols, h.defined() ? h.data_ptr() : nullptr, y.data_ptr(),
-           eight ? static_cast<float*>(scales.data_ptr()) : nullptr, k.values, k.scales,
-           stream.handle());
+    call(rcc_.add_rmsnorm_forward, x.data_ptr(), (size_t)m.ld, residual, (size_t)mr.ld, kind, w,
+         eps, (size_t)m.rows, (size_t)m.cols, h.defined() ? h.data_ptr() : nullptr, y.data_ptr(),
+         eight ? static_cast<float*>(scales.data_ptr()) : nullptr, k.values, k.scales,
+         stream.handle());
     PyObject* r = PyTuple_New(4);
     if (!r) throw python_error();
     PyTuple_SET_ITEM(r, 0, wrap(std::move(y)));

@@ -242,6 +242,8 @@ def test_no_tokens():
     x = torch.empty(0, 40, device=DEV)
     y, h, kept = rcc.add_rmsnorm_forward(x, x, weight, keep=True)
     assert y.shape == h.shape == (0, 40)
+    with pytest.raises(rcc.RccError):
+        rcc.add_rmsnorm_forward(x, x, weight, eps=-1.0)
     y8, _ = rcc.add_rmsnorm_forward(x, None, weight, out_dtype=E4M3)
     assert y8.values.shape == (0, 40) and y8.scales.shape == (0, 1)
     base = torch.ones(40, device=DEV)
