@@ -206,6 +206,41 @@ __device__ __forceinline__ void store_bytes(int8_t* p, int left, const uint32_t 
   }
 }
 
+// A row of `dim` elements, and what else is in its first and last 16 bytes, into
+// shared memory by the G threads that share it (t of them); nothing outside of
+// [lo, hi), which holds all rows, is read.  The row then begins at `to` plus its
+// address modulo 16.
+template <int G, typename T>
+__device__ __forceinline__ void copy_window(unsigned char* to, const T* row, int dim, const T* lo,
+                                            const T* hi, int t) {
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(row);
+  const uintptr_t end = begin + dim * sizeof(T), from = begin & ~uintptr_t{15};
+  const int n = (int)((end - from + 15) / 16);
+  for (int c = t; c < n; c += G) {
+    const uintptr_t at = from + 16 * c;
+    if (at >= reinterpret_cast<uintptr_t>(lo) && at + 16 <= reinterpret_cast<uintptr_t>(hi)) {
+      copy_async<16>(to + 16 * c, reinterpret_cast<const void*>(at));
+    } else {
+      for (int e = 0; e < 16; e += (int)sizeof(T))
+        if (at + e >= begin && at + e < end)
+          *reinterpret_cast<T*>(to + 16 * c + e) = *reinterpret_cast<const T*>(at + e);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ const T* in_window(const unsigned char* to, const T* row) {
+  return reinterpret_cast<const T*>(to + (reinterpret_cast<uintptr_t>(row) & 15));
+}
+// What the threads of a row wrote is there for all of them.  G > 32: every
+// thread of the block.
+template <int G>
+__device__ __forceinline__ void sync_row() {
+  if constexpr (G > 32)
+    __syncthreads();
+  else
+    __syncwarp();
+}
+
 // Threads of all blocks of one SM (those waiting to start included) and rows
 // held in shared memory.  Measured at 16,384 rows of 4,096 bf16 (fp32) columns,
 // where 6.78 TB/s would take 50 (89) us each way:
@@ -238,18 +273,21 @@ constexpr int blocks_per_sm(int all, int threads, int shared) {
                                                         : (all / threads > 0 ? all / threads : 1);
 }
 
-// Rows copied ahead into shared memory (aligned rows, VEC).  A thread writes
-// and reads its own parts alone, so the copies need no barrier; a group's scale
-// is one lane's copy, for the lanes of its warp.
+// Rows copied ahead into shared memory.  Aligned rows (VEC): a thread writes and
+// reads its own parts alone, so the copies need no barrier; a group's scale is one
+// lane's copy, for the lanes of its warp.  Others: in whole 16 bytes that reach
+// into the neighbouring rows, read back element by element behind a barrier.
+constexpr int kWindow = 32;  // bytes that a row's copy may be longer than the row
 template <typename T, int G, int NV, bool VEC, int MORE>
 struct NormFore {
   static constexpr int kThreads = kBlock<G>;
   static constexpr int kParts = NV * 8 / Part<T, VEC>::kE;
-  static constexpr int kRow = kThreads * kParts * 16;  // of one input
+  static constexpr int kOne = NV * 8 * G * (int)sizeof(T) + (VEC ? 0 : kWindow);  // a row
+  static constexpr int kRow = kThreads / G * kOne;  // the rows of one input
   static constexpr int kStage = MORE & kAdd ? 2 * kRow : kRow;
   static constexpr int kFit = kSharedMost / kStage;
   static constexpr int kStages =
-      VEC && (sizeof(T) == 2 || (MORE & kEight)) && kFit >= kForeStages ? kForeStages : 0;
+      (!VEC || sizeof(T) == 2 || (MORE & kEight)) && kFit >= kForeStages ? kForeStages : 0;
   static constexpr int kShared = kStages * kStage;
   static constexpr int kPerSm = blocks_per_sm(kStages ? kForeThreads : kForeDirect, kThreads, kShared);
 };
@@ -287,15 +325,29 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
   auto x_at = [&](int s, int p) {
     return reinterpret_cast<uint4*>(smem + s * F::kStage) + p * kThreads + tid;
   };
+  // rows that are not aligned: where the group's lies in a stage
+  [[maybe_unused]] auto window = [&](int s) {
+    return smem + s * F::kStage + tid / G * F::kOne;
+  };
   auto copy_row = [&](int s) {
     if (ahead_row < a.tokens) {
-#pragma unroll
-      for (int p = 0; p < kParts; ++p)
-        if (left > p * kSpan) {
-          copy_async<16>(x_at(s, p), ahead + p * kSpan);
-          if constexpr ((MORE & kAdd) != 0)
-            copy_async<16>(x_at(s, p) + F::kRow / 16, other + p * kSpan);
+      if constexpr (!VEC) {
+        const T* x = static_cast<const T*>(a.x);
+        copy_window<G>(window(s), ahead - col, dim, x, x + (a.tokens - 1) * a.ld_x + dim, t);
+        if constexpr ((MORE & kAdd) != 0) {
+          const T* r = static_cast<const T*>(a.residual);
+          copy_window<G>(window(s) + F::kRow, other - col, dim, r,
+                         r + (a.tokens - 1) * a.ld_residual + dim, t);
         }
+      } else {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+          if (left > p * kSpan) {
+            copy_async<16>(x_at(s, p), ahead + p * kSpan);
+            if constexpr ((MORE & kAdd) != 0)
+              copy_async<16>(x_at(s, p) + F::kRow / 16, other + p * kSpan);
+          }
+      }
     }
     copies_commit();  // one group a row, also when there is none
     ahead += step * a.ld_x;
@@ -311,9 +363,20 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
   int stage = 0, flip = 0;
   for (size_t first = (size_t)blockIdx.x * kRows; first < a.tokens; first += step, row += step) {
     const bool live = kRows == 1 || row < a.tokens;
+    // this row's elements, where they are not copied by the threads that use them
+    [[maybe_unused]] const T* here = ahead;
+    [[maybe_unused]] const T* there = other;
     if constexpr (kStages > 0) {
+      if constexpr (!VEC && G == 32) __syncwarp();  // all lanes are through with the stage
       copy_row(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
+      if constexpr (!VEC) {
+        sync_row<G>();
+        here = in_window(window(stage), static_cast<const T*>(a.x) + row * a.ld_x) + col;
+        if constexpr ((MORE & kAdd) != 0)
+          there = in_window(window(stage) + F::kRow,
+                            static_cast<const T*>(a.residual) + row * a.ld_residual) + col;
+      }
     }
     float2 v[kParts][P::kPairs];
     float2 sq = both(0.f);
@@ -321,18 +384,18 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
     for (int p = 0; p < kParts; ++p) {
       uint4 raw = make_uint4(0u, 0u, 0u, 0u);
       if (live && left > p * kSpan) {
-        if constexpr (kStages > 0)
+        if constexpr (VEC && kStages > 0)
           raw = *x_at(stage, p);
         else
-          raw = load_part<VEC>(ahead + p * kSpan, left - p * kSpan);
+          raw = load_part<VEC>(here + p * kSpan, left - p * kSpan);
       }
       widen(raw, v[p], T());
       if constexpr ((MORE & kAdd) != 0) {
         // the sum as it is written: the norm is taken of what the next layer reads
         if (live && left > p * kSpan) {
           float2 r[P::kPairs];
-          widen(kStages > 0 ? x_at(stage, p)[F::kRow / 16]
-                            : load_part<VEC>(other + p * kSpan, left - p * kSpan), r, T());
+          widen(VEC && kStages > 0 ? x_at(stage, p)[F::kRow / 16]
+                                   : load_part<VEC>(there + p * kSpan, left - p * kSpan), r, T());
 #pragma unroll
           for (int e = 0; e < P::kPairs; ++e) v[p][e] = add2(v[p][e], r[e]);
           store_part<VEC>(sum_out + p * kSpan, left - p * kSpan, v[p]);
@@ -444,13 +507,16 @@ struct NormBack {
   static constexpr int kThreads = kBlock<G>;
   static constexpr int kParts = NV * 8 / Part<T, VEC>::kE;
   static constexpr int kScaled = kThreads / Part<T, VEC>::kLanes;  // groups of one part
-  static constexpr int kRow = kThreads * kParts * 16;  // of dy, and of the sum's gradient
-  static constexpr int kStage = kRow + kThreads * kParts * Part<T, VEC>::kE +
-                                kParts * kScaled * 4 + (MORE & kAdd ? kRow : 0);
+  static constexpr int kOne = NV * 8 * G * (int)sizeof(T) + (VEC ? 0 : kWindow);  // a row
+  static constexpr int kRow = kThreads / G * kOne;  // of dy, and of the sum's gradient
+  static constexpr int kStage = kRow + kThreads * NV * 8 +
+                                (VEC ? kParts * kScaled : kThreads * NV * 8 / (int)kKeepGroup) * 4 +
+                                (MORE & kAdd ? kRow : 0);
   static constexpr bool kHoldWeight = kThreads * NV * 32 + 2 * kStage <= kSharedMost;
   static constexpr int kWeight = kHoldWeight ? kThreads * NV * 32 : 0;
   static constexpr int kFit = (kSharedMost - kWeight) / kStage;
-  static constexpr int kStages = VEC && kFit >= 2 ? (kFit < kBackStages ? kFit : kBackStages) : 0;
+  static constexpr int kStages = (VEC || (MORE & kAdd)) && kFit >= 2
+                                     ? (kFit < kBackStages ? kFit : kBackStages) : 0;
   static constexpr int kShared = kWeight + kStages * kStage;
   static constexpr int kPerSm = blocks_per_sm(kStages ? kBackThreads : kBackDirect, kThreads, kShared);
   // a block's rows of partial sums are added up where the weight was
@@ -460,8 +526,8 @@ struct NormBack {
 // Rows are dealt to the blocks in turn; a thread keeps the weight gradient of
 // its columns in registers over all of its rows, and each block writes one
 // row of partial sums, which norm_dweight_kernel adds in a fixed order.
-// Bandwidth bound: rows are copied ahead into shared memory (aligned rows,
-// VEC) while the current one is reduced.
+// Bandwidth bound: rows are copied ahead into shared memory (aligned rows, VEC;
+// with kAdd all) while the current one is reduced.
 template <typename T, int G, int NV, bool VEC, int MORE>
 __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPerSm)
     norm_backward_kernel(const NormGradArgs a) {
@@ -528,8 +594,34 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
     scales += step * groups;
     ahead_row += step;
   };
+  // rows that are not aligned: dy, the sum's gradient, bytes and scales of the
+  // group's row, each kind's rows one after the other
+  [[maybe_unused]] auto window = [&](int s, int input) {
+    return smem + B::kWeight + s * B::kStage + input * B::kRow + tid / G * B::kOne;
+  };
+  constexpr int kInputs = MORE & kAdd ? 2 : 1;
+  [[maybe_unused]] auto bytes_at = [&](int s) {
+    return reinterpret_cast<int8_t*>(smem + B::kWeight + s * B::kStage + kInputs * B::kRow +
+                                     tid / G * (NV * 8 * G));
+  };
+  [[maybe_unused]] auto scales_at = [&](int s) {
+    return reinterpret_cast<float*>(smem + B::kWeight + s * B::kStage + kInputs * B::kRow +
+                                    kThreads * NV * 8) + tid / G * (NV * 8 * G / (int)kKeepGroup);
+  };
   auto copy_row = [&](int s) {
-    if (ahead_row < a.tokens) {
+    if (!VEC && ahead_row < a.tokens) {
+      const T* base = static_cast<const T*>(a.dy);
+      copy_window<G>(window(s, 0), dy - col, dim, base, base + (a.tokens - 1) * a.ld_dy + dim, t);
+      if constexpr ((MORE & kAdd) != 0) {
+        base = static_cast<const T*>(a.dsum);
+        copy_window<G>(window(s, 1), dh - col, dim, base,
+                       base + (a.tokens - 1) * a.ld_dsum + dim, t);
+      }
+      for (int c = t; c < groups * (int)kKeepGroup / 16; c += G)
+        copy_async<16>(bytes_at(s) + 16 * c, kept - col + 16 * c);
+      for (int c = t; c < groups; c += G)
+        copy_async<4>(scales_at(s) + c, scales - col / (int)kKeepGroup + c);
+    } else if (ahead_row < a.tokens) {
 #pragma unroll
       for (int p = 0; p < kParts; ++p) {
         if (left > p * kSpan) {
@@ -562,10 +654,26 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
   int stage = 0, flip = 0;
   for (size_t first = (size_t)blockIdx.x * kRows; first < a.tokens; first += step, row += step) {
     const bool live = kRows == 1 || row < a.tokens;
+    // this row's elements, where they are not copied by the threads that use them
+    [[maybe_unused]] const T* dy_here = dy;
+    [[maybe_unused]] const T* dh_here = dh;
+    [[maybe_unused]] const int8_t* kept_here = kept;
+    [[maybe_unused]] const float* scales_here = scales;
     if constexpr (kStages > 0) {
+      if constexpr (!VEC && G == 32) __syncwarp();  // all lanes are through with the stage
       copy_row(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
-      __syncwarp();  // a group's scale is one lane's copy
+      if constexpr (VEC) {
+        __syncwarp();  // a group's scale is one lane's copy
+      } else {
+        sync_row<G>();
+        dy_here = in_window(window(stage, 0), static_cast<const T*>(a.dy) + row * a.ld_dy) + col;
+        if constexpr ((MORE & kAdd) != 0)
+          dh_here =
+              in_window(window(stage, 1), static_cast<const T*>(a.dsum) + row * a.ld_dsum) + col;
+        kept_here = bytes_at(stage) + col;
+        scales_here = scales_at(stage) + col / (int)kKeepGroup;
+      }
     }
     // kept over the reduction: dy w, and dy and the bytes as they came
     uint4 raw[kParts];
@@ -577,17 +685,17 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       if (live && left > p * kSpan) {
-        if constexpr (kStages > 0) {
+        if constexpr (VEC && kStages > 0) {
           raw[p] = *dy_at(stage, p);
           load_bytes<VEC>(reinterpret_cast<const int8_t*>(q_at(stage, p)), P::kE, q[p]);
           scale[p][0] = *scale_at(stage, p);
         } else {
-          raw[p] = load_part<VEC>(dy + p * kSpan, left - p * kSpan);
-          load_bytes<VEC>(kept + p * kSpan, left - p * kSpan, q[p]);
+          raw[p] = load_part<VEC>(dy_here + p * kSpan, left - p * kSpan);
+          load_bytes<VEC>(kept_here + p * kSpan, left - p * kSpan, q[p]);
 #pragma unroll
           for (int i = 0; i < P::kScales; ++i)
             scale[p][i] = left > p * kSpan + i * (int)kKeepGroup
-                              ? scales[p * (kSpan / (int)kKeepGroup) + i] : 0.f;
+                              ? scales_here[p * (kSpan / (int)kKeepGroup) + i] : 0.f;
         }
         float2 x[P::kPairs], d[P::kPairs], w[P::kPairs];
         weight(p, w);
@@ -627,8 +735,9 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
         }
         if constexpr ((MORE & kAdd) != 0) {
           float2 more[P::kPairs];
-          widen(kStages > 0 ? *dh_at(stage, p)
-                            : load_part<VEC>(dh + p * kSpan, left - p * kSpan), more, T());
+          widen(VEC && kStages > 0 ? *dh_at(stage, p)
+                                   : load_part<VEC>(dh_here + p * kSpan, left - p * kSpan),
+                more, T());
 #pragma unroll
           for (int e = 0; e < P::kPairs; ++e) out[e] = add2(out[e], more[e]);
         }

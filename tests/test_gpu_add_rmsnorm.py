@@ -293,3 +293,44 @@ def test_many_rows_and_a_captured_call():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [9, 257, 1001, 2047, 4095, 4096, 20001])
+def test_rows_anywhere(dtype, dim):
+    """Rows that are on no boundary, their neighbours NaN: the bits of rows that
+    stand alone, in blocks that take many of them."""
+    g = defs.gen(68)
+    tokens = 7 if dim > 5000 else 3000 if dim > 300 else 9000
+    clean = [defs.randn(g, tokens, dim, dtype=dtype) for _ in range(2)]
+    weight = 1.0 + defs.randn(g, dim, scale=0.2)
+
+    def place(t, offset, extra):
+        wide = torch.full((offset + tokens * (dim + extra),), float("nan"), dtype=dtype, device=DEV)
+        rows = wide[offset:].view(tokens, dim + extra)[:, :dim]
+        rows.copy_(t)
+        return rows
+
+    def run(offset, extra):
+        x, r = place(clean[0], offset, extra), place(clean[1], 1, 2 * extra + 1)
+        y, h, kept = rcc.add_rmsnorm_forward(x, r, weight, keep=True)
+        y8, _ = rcc.add_rmsnorm_forward(x, r, weight, out_dtype=E4M3)
+        dx, dw = rcc.add_rmsnorm_backward(x, r, kept, weight)
+        alone, kept2 = rcc.rmsnorm_forward(place(h, offset, extra), weight, keep=True)
+        assert torch.equal(alone, y) and torch.equal(kept2.data, kept.data)
+        return y, h, kept.data, y8.values.view(torch.uint8), y8.scales, dx, dw
+    want = run(1, 1)
+    assert torch.equal(want[1], (clean[0].float() + clean[1].float()).to(dtype))
+    assert torch.isfinite(want[5]).all() and torch.isfinite(want[6]).all()
+    for offset, extra in ((3, 0), (0, 3), (7, 6), (5, 8)):
+        assert all(torch.equal(a, b) for a, b in zip(run(offset, extra), want))
+    # in place, each row written once it has been read
+    x, r = place(clean[0], 1, 1), clean[1].clone()
+    y, h = rcc.add_rmsnorm_forward(x, r, weight, h=r)
+    assert h.data_ptr() == r.data_ptr() and torch.equal(h, want[1]) and torch.equal(y, want[0])
+    dh = want[1].clone()
+    dx, _ = rcc.add_rmsnorm_backward(place(clean[0], 1, 0), dh, rcc.Kept(tokens, dim, data=want[2]),
+                                     weight, dx=dh)
+    again, _ = rcc.add_rmsnorm_backward(place(clean[0], 3, 1), want[1],
+                                        rcc.Kept(tokens, dim, data=want[2]), weight)
+    assert dx.data_ptr() == dh.data_ptr() and torch.equal(dx, again)
