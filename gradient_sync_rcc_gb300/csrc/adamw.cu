@@ -206,10 +206,15 @@ __device__ __forceinline__ void add_range(const AdamWTensor& t, uint64_t begin, 
       add_vectors<false>(t.grad, t.wide, begin, vectors, s);
     from = begin + vectors * kUnit;
   }
-  for (uint64_t i = from + threadIdx.x; i < end; i += kThreads) {
-    const float g = grad_at(t, i);
-    s.seen |= __float_as_uint(g) & 0x7FFFFFFFu;
-    s.add(make_float2(g, 0.f));
+  for (uint64_t i = from + threadIdx.x; i < end; i += 8 * kThreads) {
+    float g[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = i + k * kThreads < end ? grad_at(t, i + k * kThreads) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      s.seen |= (__float_as_uint(g[k]) | __float_as_uint(g[k + 1])) & 0x7FFFFFFFu;
+      s.add(make_float2(g[k], g[k + 1]));
+    }
   }
 }
 
@@ -373,14 +378,17 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const 
 
 // ---- the update -----------------------------------------------------------------
 
-// Eight neighbours as they lie in memory, and their group's scales
+// Eight elements as they lie in memory, and the scales of the first and the last
+// four: neighbours, of one group; or (buffers on no boundary, the end of a tensor)
+// every 32nd of the warp's 256, so that a warp's accesses lie side by side and its
+// two groups are the first and the last four of all lanes.
 template <bool EIGHT, bool BF16>
 struct Unit {
   Raw<BF16> g;
   float p[kUnit];
   float m[EIGHT ? 1 : kUnit], v[EIGHT ? 1 : kUnit];
   uint2 m8, v8;
-  float ms, vs;
+  float ms[2], vs[2];
 };
 
 __device__ __forceinline__ void widen_e4m3(uint2 q, float2 (&v)[4]) {
@@ -415,29 +423,38 @@ __device__ __forceinline__ float round_e4m3(float y, uint32_t number) {
   return __fsub_rn(__uint_as_float(b), low);
 }
 
-// What eight values of a group are held as, and its scale s: the smallest power
-// of two with max <= 448 s.  448 is 1.75 2^8, so a fraction above 0.75 carries
-// into the exponent.  0 for next to nothing, NaN for a NaN.
-template <bool ROOT>
-__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&number)[kUnit],
-                                      float& scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = __float_as_uint(v[i].x), y = __float_as_uint(v[i].y);
-    top = ROOT ? max(max(top, x), y) : max(max(top, x << 1), y << 1);  // but their signs
-  }
-  // over the 16 threads of a group; a NaN's bits are the largest of all
-  top = __reduce_max_sync(threadIdx.x & 16 ? 0xFFFF0000u : 0x0000FFFFu, top);
-  if (!ROOT) top >>= 1;
+// The scale s of a group by the bits of its largest value: the smallest power of
+// two with max <= 448 s.  448 is 1.75 2^8, so a fraction above 0.75 carries into
+// the exponent.  0 for next to nothing, NaN for a NaN.  `inv`: 1 / s, or 0.
+__device__ __forceinline__ float scale_for(uint32_t top, float& inv) {
   const uint32_t s = ((min(top, 0x7F7FFFFFu) + 0x1FFFFFu) & 0x7F800000u) - (8u << 23);
   const bool some = top >= kNothingBits;
-  scale = some ? __uint_as_float(top > 0x7F800000u ? top : s) : 0.f;
-  const float inv = some ? __uint_as_float((254u << 23) - s) : 0.f;
+  inv = some ? __uint_as_float((254u << 23) - s) : 0.f;
+  return some ? __uint_as_float(top > 0x7F800000u ? top : s) : 0.f;
+}
+
+// What eight values are held as, and their scales
+template <bool ROOT, bool STRIDED>
+__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&number)[kUnit],
+                                      float (&scale)[2]) {
+  float inv[2];
+#pragma unroll
+  for (int half = 0; half < (STRIDED ? 2 : 1); ++half) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 2 * half; i < (STRIDED ? 2 * half + 2 : 4); ++i) {
+      const uint32_t x = __float_as_uint(v[i].x), y = __float_as_uint(v[i].y);
+      top = ROOT ? max(max(top, x), y) : max(max(top, x << 1), y << 1);  // but their signs
+    }
+    // over the threads of the group; a NaN's bits are the largest of all
+    const uint32_t lanes = STRIDED ? 0xFFFFFFFFu : threadIdx.x & 16 ? 0xFFFF0000u : 0x0000FFFFu;
+    top = __reduce_max_sync(lanes, top);
+    scale[half] = scale_for(ROOT ? top : top >> 1, inv[half]);
+  }
   float2 w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 y = mul2(v[i], both(inv));
+    const float2 y = mul2(v[i], both(inv[STRIDED ? i / 2 : 0]));
     w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), number[2 * i]);
     w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), number[2 * i + 1]);
     if (ROOT) {
@@ -452,91 +469,120 @@ __device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&num
   return narrow_e4m3(w);
 }
 
-// Up to eight elements from the i-th on; zeros past the tensor
+// Whether the warp's 256 elements from the i-th on are loaded in vectors
+__device__ __forceinline__ bool vectors(const AdamWTensor& t, uint64_t warp_first) {
+  return t.vec && warp_first + 32 * kUnit <= t.numel;
+}
+__device__ __forceinline__ uint64_t warp_first(uint64_t item_first) {
+  return item_first + threadIdx.x / 32 * 32 * kUnit;
+}
+// The first of a thread's neighbours, and the first of its strided elements
+__device__ __forceinline__ uint64_t neighbours(uint64_t warp) {
+  return warp + threadIdx.x % 32 * kUnit;
+}
+__device__ __forceinline__ uint64_t strided(uint64_t warp) { return warp + threadIdx.x % 32; }
+
 template <bool EIGHT, bool BF16>
-__device__ __forceinline__ void load_unit(const AdamWTensor& t, uint64_t i,
-                                          Unit<EIGHT, BF16>& u) {
+__device__ __forceinline__ void load_vectors(const AdamWTensor& t, uint64_t warp,
+                                             Unit<EIGHT, BF16>& u) {
+  const uint64_t i = neighbours(warp);
+  if constexpr (BF16) {
+    load_raw(t.grad, i, t.wide, u.g);
+  } else if (t.bf16) {
+    set_wide(u.g, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.grad) + i));
+  } else {
+    load_raw(t.grad, i, t.wide, u.g);
+  }
+  load_eight(t.param + i, t.wide, u.p);
   if constexpr (EIGHT) {
-    const bool live = i < t.numel;
-    u.ms = live ? t.m_scales[i / kGroup] : 0.f;
-    u.vs = live ? t.v_scales[i / kGroup] : 0.f;
+    u.m8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
+    u.v8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
+    u.ms[0] = t.m_scales[i / kGroup];
+    u.vs[0] = t.v_scales[i / kGroup];
+  } else {
+    load_eight(static_cast<const float*>(t.m) + i, t.wide, u.m);
+    load_eight(static_cast<const float*>(t.v) + i, t.wide, u.v);
   }
-  if (t.vec && i + kUnit <= t.numel) {
-    if constexpr (BF16) {
-      load_raw(t.grad, i, t.wide, u.g);
-    } else if (t.bf16) {
-      set_wide(u.g, *reinterpret_cast<const uint4*>(
-                        static_cast<const __nv_bfloat16*>(t.grad) + i));
-    } else {
-      load_raw(t.grad, i, t.wide, u.g);
-    }
-    load_eight(t.param + i, t.wide, u.p);
-    if constexpr (EIGHT) {
-      u.m8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
-      u.v8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
-    } else {
-      load_eight(static_cast<const float*>(t.m) + i, t.wide, u.m);
-      load_eight(static_cast<const float*>(t.v) + i, t.wide, u.v);
-    }
-    return;
-  }
+}
+
+// Elements past the tensor are zeros
+template <bool EIGHT, bool BF16>
+__device__ __forceinline__ void load_strided(const AdamWTensor& t, uint64_t warp,
+                                             Unit<EIGHT, BF16>& u) {
 #pragma unroll
   for (int e = 0; e < Raw<BF16>::kWords; ++e) u.g.w[e] = 0u;
   uint32_t q[2][2] = {};
 #pragma unroll
   for (int e = 0; e < kUnit; ++e) {
-    const bool live = i + e < t.numel;
+    const uint64_t i = strided(warp) + 32 * e;
+    const bool live = i < t.numel;
     if constexpr (BF16)
-      u.g.w[e / 2] |= (live ? static_cast<const uint16_t*>(t.grad)[i + e] : 0u) << (16 * (e % 2));
+      u.g.w[e / 2] |= (live ? static_cast<const uint16_t*>(t.grad)[i] : 0u) << (16 * (e % 2));
     else
-      u.g.w[e] = live ? __float_as_uint(grad_at(t, i + e)) : 0u;
-    u.p[e] = live ? t.param[i + e] : 0.f;
+      u.g.w[e] = live ? __float_as_uint(grad_at(t, i)) : 0u;
+    u.p[e] = live ? t.param[i] : 0.f;
     if constexpr (EIGHT) {
-      q[0][e / 4] |= (live ? static_cast<const uint8_t*>(t.m)[i + e] : 0u) << (8 * (e % 4));
-      q[1][e / 4] |= (live ? static_cast<const uint8_t*>(t.v)[i + e] : 0u) << (8 * (e % 4));
+      q[0][e / 4] |= (live ? static_cast<const uint8_t*>(t.m)[i] : 0u) << (8 * (e % 4));
+      q[1][e / 4] |= (live ? static_cast<const uint8_t*>(t.v)[i] : 0u) << (8 * (e % 4));
     } else {
-      u.m[e] = live ? static_cast<const float*>(t.m)[i + e] : 0.f;
-      u.v[e] = live ? static_cast<const float*>(t.v)[i + e] : 0.f;
+      u.m[e] = live ? static_cast<const float*>(t.m)[i] : 0.f;
+      u.v[e] = live ? static_cast<const float*>(t.v)[i] : 0.f;
     }
   }
   if constexpr (EIGHT) {
     u.m8 = make_uint2(q[0][0], q[0][1]);
     u.v8 = make_uint2(q[1][0], q[1][1]);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint64_t at = warp + half * kGroup;
+      u.ms[half] = at < t.numel ? t.m_scales[at / kGroup] : 0.f;
+      u.vs[half] = at < t.numel ? t.v_scales[at / kGroup] : 0.f;
+    }
   }
 }
 
 template <bool EIGHT, bool BF16>
-__device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i,
-                                           const Unit<EIGHT, BF16>& u) {
+__device__ __forceinline__ void store_vectors(const AdamWTensor& t, uint64_t warp,
+                                              const Unit<EIGHT, BF16>& u) {
+  const uint64_t i = neighbours(warp);
+  store_eight(t.param + i, t.wide, u.p);
+  if (t.copy) store8(t.copy + i, u.p);
   if constexpr (EIGHT) {
-    if (threadIdx.x % kLanes == 0 && i < t.numel) {
-      t.m_scales[i / kGroup] = u.ms;
-      t.v_scales[i / kGroup] = u.vs;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = u.m8;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = u.v8;
+    if (threadIdx.x % kLanes == 0) {
+      t.m_scales[i / kGroup] = u.ms[0];
+      t.v_scales[i / kGroup] = u.vs[0];
     }
+  } else {
+    store_eight(static_cast<float*>(t.m) + i, t.wide, u.m);
+    store_eight(static_cast<float*>(t.v) + i, t.wide, u.v);
   }
-  if (t.vec && i + kUnit <= t.numel) {
-    store_eight(t.param + i, t.wide, u.p);
-    if (t.copy) store8(t.copy + i, u.p);
-    if constexpr (EIGHT) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = u.m8;
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = u.v8;
-    } else {
-      store_eight(static_cast<float*>(t.m) + i, t.wide, u.m);
-      store_eight(static_cast<float*>(t.v) + i, t.wide, u.v);
-    }
-    return;
-  }
+}
+
+template <bool EIGHT, bool BF16>
+__device__ __forceinline__ void store_strided(const AdamWTensor& t, uint64_t warp,
+                                              const Unit<EIGHT, BF16>& u) {
 #pragma unroll
   for (int e = 0; e < kUnit; ++e) {
-    if (i + e >= t.numel) continue;
-    t.param[i + e] = u.p[e];
-    if (t.copy) from_f32(u.p[e], t.copy[i + e]);
+    const uint64_t i = strided(warp) + 32 * e;
+    if (i >= t.numel) continue;
+    t.param[i] = u.p[e];
+    if (t.copy) from_f32(u.p[e], t.copy[i]);
     if constexpr (EIGHT) {
-      static_cast<uint8_t*>(t.m)[i + e] = (uint8_t)((e < 4 ? u.m8.x : u.m8.y) >> (8 * (e % 4)));
-      static_cast<uint8_t*>(t.v)[i + e] = (uint8_t)((e < 4 ? u.v8.x : u.v8.y) >> (8 * (e % 4)));
+      static_cast<uint8_t*>(t.m)[i] = (uint8_t)((e < 4 ? u.m8.x : u.m8.y) >> (8 * (e % 4)));
+      static_cast<uint8_t*>(t.v)[i] = (uint8_t)((e < 4 ? u.v8.x : u.v8.y) >> (8 * (e % 4)));
     } else {
-      static_cast<float*>(t.m)[i + e] = u.m[e];
-      static_cast<float*>(t.v)[i + e] = u.v[e];
+      static_cast<float*>(t.m)[i] = u.m[e];
+      static_cast<float*>(t.v)[i] = u.v[e];
+    }
+  }
+  if constexpr (EIGHT) {
+    const int half = threadIdx.x % 32;  // lane 0 the first group's, lane 1 the second's
+    const uint64_t at = warp + half * kGroup;
+    if (half < 2 && at < t.numel) {
+      t.m_scales[at / kGroup] = half ? u.ms[1] : u.ms[0];
+      t.v_scales[at / kGroup] = half ? u.vs[1] : u.vs[0];
     }
   }
 }
@@ -544,7 +590,7 @@ __device__ __forceinline__ void store_unit(const AdamWTensor& t, uint64_t i,
 // fp32 states: every operation rounded, as rcc_grad_sync_adamw's update
 template <bool BF16>
 __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecision& d,
-                                            uint32_t, Unit<false, BF16>& u) {
+                                            Unit<false, BF16>& u) {
 #pragma unroll
   for (int e = 0; e < kUnit; ++e) {
     const float2 two = pair_of(u.g, e / 2);
@@ -571,9 +617,11 @@ __device__ __forceinline__ float inverse_of(float v) {
 
 // 8-bit states: two elements an operation, products fused into sums, root and
 // quotient to 2^-22: what is held keeps four bits of it.
-template <bool BF16>
+// `key`: of the rounding numbers of the block of kNumbered elements, `first`: the
+// thread's first element in it.
+template <bool STRIDED, bool BF16>
 __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecision& d,
-                                            uint32_t first, Unit<true, BF16>& u) {
+                                            uint32_t key, uint32_t first, Unit<true, BF16>& u) {
   float2 m[4], v[4];
   widen_e4m3(u.m8, m);
   widen_e4m3(u.v8, v);
@@ -581,8 +629,9 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 g = mul2(pair_of(u.g, i), both(d.factor));
-    m[i] = fma2(m[i], both(u.ms * a.b1), mul2(g, both(a.one_minus_b1)));
-    const float2 root = mul2(v[i], both(u.vs));
+    constexpr int kHalf = STRIDED ? 2 : 4;  // pairs of one scale
+    m[i] = fma2(m[i], both(u.ms[i / kHalf] * a.b1), mul2(g, both(a.one_minus_b1)));
+    const float2 root = mul2(v[i], both(u.vs[i / kHalf]));
     v[i] = fma2(mul2(root, root), both(a.b2), mul2(mul2(g, g), both(a.one_minus_b2)));
     v[i] = make_float2(root_of(v[i].x), root_of(v[i].y));
     const float2 denom = fma2(v[i], both(d.inv_root), both(a.eps));
@@ -591,23 +640,37 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
                           mul2(make_float2(u.p[2 * i], u.p[2 * i + 1]), both(a.decay)));
     u.p[2 * i] = p.x;
     u.p[2 * i + 1] = p.y;
-    const uint32_t h = mix(first + i);
-    number[2 * i] = h & 0xFFFFu;
-    number[2 * i + 1] = h >> 16;
+    if constexpr (STRIDED) {
+#pragma unroll
+      for (int e = 2 * i; e < 2 * i + 2; ++e) {
+        const uint32_t at = first + 32 * e, h = mix(key + at / 2);
+        number[e] = at % 2 ? h >> 16 : h & 0xFFFFu;
+      }
+    } else {
+      const uint32_t h = mix(key + first / 2 + i);
+      number[2 * i] = h & 0xFFFFu;
+      number[2 * i + 1] = h >> 16;
+    }
   }
-  u.m8 = hold<false>(m, number, u.ms);
-  u.v8 = hold<true>(v, number, u.vs);
+  u.m8 = hold<false, STRIDED>(m, number, u.ms);
+  u.v8 = hold<true, STRIDED>(v, number, u.vs);
 }
 
 // fp32 states: a thread's loads are bytes enough by themselves.
 template <bool BF16>
 __device__ __forceinline__ void update_item(const AdamWArgs& a, const AdamWDecision& d,
                                             const AdamWTensor& t, uint32_t chunk) {
-  const uint64_t i = (uint64_t)chunk * kAdamWItem + threadIdx.x * kUnit;
+  const uint64_t warp = warp_first((uint64_t)chunk * kAdamWItem);
   Unit<false, BF16> u;
-  load_unit(t, i, u);
-  update_unit(a, d, 0, u);
-  store_unit(t, i, u);
+  if (vectors(t, warp)) {
+    load_vectors(t, warp, u);
+    update_unit(a, d, u);
+    store_vectors(t, warp, u);
+  } else {
+    load_strided(t, warp, u);
+    update_unit(a, d, u);
+    store_strided(t, warp, u);
+  }
 }
 __global__ void __launch_bounds__(kThreads, kUpdatePerSm) adamw_update_kernel(const AdamWArgs a) {
   __shared__ AdamWTensor t;
@@ -721,8 +784,8 @@ __device__ __forceinline__ void take_unit(const unsigned char* stage, bool bf16,
   }
   u.m8 = reinterpret_cast<const uint2*>(stage + S::kM)[tid];
   u.v8 = reinterpret_cast<const uint2*>(stage + S::kV)[tid];
-  u.ms = reinterpret_cast<const float*>(stage + S::kMs)[tid / kLanes];
-  u.vs = reinterpret_cast<const float*>(stage + S::kVs)[tid / kLanes];
+  u.ms[0] = reinterpret_cast<const float*>(stage + S::kMs)[tid / kLanes];
+  u.vs[0] = reinterpret_cast<const float*>(stage + S::kVs)[tid / kLanes];
 }
 
 __device__ __forceinline__ void arrive(uint32_t bar) {
@@ -807,15 +870,22 @@ __global__ void __launch_bounds__(kEightThreads, kEightPerSm)
     }
     const unsigned char* stage = smem + s * S::kBytes;
     const Entry& e = *reinterpret_cast<const Entry*>(stage + S::kEntry);
-    const uint64_t first = (uint64_t)e.item.chunk * kAdamWItem, i = first + tid * kUnit;
+    const uint64_t first = (uint64_t)e.item.chunk * kAdamWItem, warp = warp_first(first);
+    const uint32_t key =
+        mix(mix(step_key + e.item.tensor * kGolden) ^ (uint32_t)(first / kNumbered));
     Unit<true, BF16> u;
-    if (whole_item(e.t, first))
-      take_unit<BF16>(stage, e.t.bf16, u);
-    else
-      load_unit(e.t, i, u);
-    const uint32_t key = mix(mix(step_key + e.item.tensor * kGolden) ^ (uint32_t)(i / kNumbered));
-    update_unit(a, d, key + (uint32_t)(i % kNumbered) / 2, u);
-    store_unit(e.t, i, u);
+    if (vectors(e.t, warp)) {
+      if (whole_item(e.t, first))
+        take_unit<BF16>(stage, e.t.bf16, u);
+      else
+        load_vectors(e.t, warp, u);
+      update_unit<false>(a, d, key, (uint32_t)(neighbours(warp) % kNumbered), u);
+      store_vectors(e.t, warp, u);
+    } else {
+      load_strided(e.t, warp, u);
+      update_unit<true>(a, d, key, (uint32_t)(strided(warp) % kNumbered), u);
+      store_strided(e.t, warp, u);
+    }
     __syncwarp();
     if (tid % 32 == 0) arrive(empty + 8 * s);
   }
