@@ -4,6 +4,8 @@
 // Device side: each kernel first waits for the grid ahead of it on the
 // stream to complete and flush its memory (griddepcontrol.wait), before any
 // global memory access, so stream order holds exactly as with a plain launch.
+// (AdamW over many tensors reads its tables before: a host copy wrote them, and no
+// kernel does.)
 // Then it lets the next grid on the stream be scheduled as soon as all of its
 // own CTAs have started (griddepcontrol.launch_dependents).  The next
 // kernel's CTAs take the SM slots that this kernel's last wave frees and start

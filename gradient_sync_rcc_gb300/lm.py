@@ -234,7 +234,7 @@ class AdamWPlan:
     The tensors' addresses are kept: a step reads the gradients where they were.
     The plan and the states it makes belong to `stream`; steps on another one have
     to wait for it.  One step after the other: a plan's steps, and graphs of them,
-    share its workspace."""
+    share its workspace; graphs need the plan (its workspace) to live."""
 
     def __init__(self, tensors, states=torch.float32, seed=0, step=0, betas=(0.9, 0.999),
                  stream=None):

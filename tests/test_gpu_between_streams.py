@@ -1,5 +1,7 @@
 """The `stream` argument of the residual norm, rotary positions and AdamW: calls on
 a stream that is not the current one, with outputs and workspaces left out."""
+import threading
+
 import pytest
 import torch
 
@@ -129,3 +131,65 @@ def test_a_plan_is_not_made_while_capturing():
         rcc.adamw_step(plan, rcc.adamw_cfg())
     graph.replay()
     assert rcc.adamw_report(plan).step == 1
+
+
+def test_calls_of_several_threads():
+    """Threads with streams and plans of their own, at once."""
+    g = defs.gen(124)
+    work = []
+    for i in range(4):
+        n = 50000 + 777 * i
+        work.append(dict(param=defs.randn(g, n), grad=defs.randn(g, n, dtype=BF16)))
+    step = Step(125)
+    cfg = rcc.adamw_cfg(max_grad_norm=1.0)
+
+    def run(i, param, stream, out):
+        plan = rcc.AdamWPlan([dict(param=param, grad=work[i]["grad"])], states=E4M3, seed=i,
+                             stream=stream)
+        for _ in range(20):
+            rcc.adamw_step(plan, cfg, stream=stream)
+            y, h = rcc.add_rmsnorm_forward(step.x, step.r, step.weight, stream=stream)
+        q, _ = rcc.rotary_forward(y.view(TOKENS, HEADS, -1), None, step.turns, stream=stream)
+        out[i] = (plan, y, h, q, rcc.adamw_report(plan, stream=stream).step)
+
+    want, got = {}, {}
+    alone = [w["param"].clone() for w in work]
+    together = [w["param"].clone() for w in work]
+    for i, p in enumerate(alone):
+        run(i, p, None, want)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i, p, torch.cuda.Stream(), got))
+               for i, p in enumerate(together)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(got) == 4
+    for i in range(4):
+        assert got[i][4] == want[i][4] == 20 and torch.equal(alone[i], together[i])
+        assert all(torch.equal(a, b) for a, b in zip(got[i][1:4], want[i][1:4]))
+
+
+def test_graphs_of_two_plans_in_turn():
+    g = defs.gen(126)
+    cfg = rcc.adamw_cfg(max_grad_norm=1.0)
+    params = [defs.randn(g, 9000), defs.randn(g, 300)]
+    grads = [defs.randn(g, p.numel()) for p in params]
+    plain = [p.clone() for p in params]
+    plans = [rcc.AdamWPlan([dict(param=p, grad=d)], states=E4M3) for p, d in zip(params, grads)]
+    others = [rcc.AdamWPlan([dict(param=p, grad=d)], states=E4M3) for p, d in zip(plain, grads)]
+    graphs = []
+    torch.cuda.synchronize()
+    for plan in plans:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rcc.adamw_step(plan, cfg)
+        graphs.append(graph)
+    for _ in range(5):
+        for graph, other in zip(graphs, others):
+            graph.replay()
+            rcc.adamw_step(other, cfg)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(params, plain))
+    assert [rcc.adamw_report(p).step for p in plans] == [5, 5]
