@@ -505,3 +505,35 @@ def test_refusals_on_the_gpu():
     del plan
     cfg = rcc.adamw_cfg()
     assert rcc.raw("rcc_adamw_step", handle, C.byref(cfg), 1.0, None) == rcc.ERR_MISSING_REGISTRATION
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("n", [100, 5000, 3000000])
+def test_what_the_kernels_just_ahead_wrote(eight, n):
+    """A step reads gradients, parameters and states that the work right ahead of it
+    on the stream wrote, skipped steps between: the bits of a plan that waits."""
+    g = defs.gen(92)
+    tensors = [make(g, n, BF16, eight, True), make(g, 77, BF16, eight, True)]
+    twin = clone(tensors)
+    plan, other = rcc.AdamWPlan(tensors, seed=1), rcc.AdamWPlan(twin, seed=1)
+    cfg = rcc.adamw_cfg(max_grad_norm=1.0)
+    draws = [[defs.randn(g, t["grad"].numel(), dtype=BF16) for t in tensors] for _ in range(5)]
+    draws[3][1][5] = float("nan")
+
+    def before(tensors, k):
+        for t, d in zip(tensors, draws[k % 5]):
+            t["grad"].copy_(d)
+            t["param"].mul_(0.999)
+            bits(t["exp_avg"]).copy_(bits(t["exp_avg"]).clone())
+    torch.cuda.synchronize()
+    for k in range(40):
+        before(tensors, k)
+        rcc.adamw_step(plan, cfg)
+    for k in range(40):
+        before(twin, k)
+        torch.cuda.synchronize()
+        rcc.adamw_step(other, cfg)
+        torch.cuda.synchronize()
+    assert rcc.adamw_report(plan).step == rcc.adamw_report(other).step == 32
+    for a, b in zip(tensors, twin):
+        assert all(torch.equal(bits(a[k]).view(torch.uint8), bits(b[k]).view(torch.uint8)) for k in a)
