@@ -300,7 +300,9 @@ __device__ __forceinline__ void decide(const AdamWArgs& a, const Powers& p, doub
   d.skip = bad > 0 || !(norm < INFINITY);
   const double coef = !d.skip && a.max_norm > 0.0 && norm > a.max_norm ? a.max_norm / norm : 1.0;
   d.coef = (float)coef;
-  d.factor = (float)((double)d.coef * a.inv_scale64);
+  const double factor = (double)d.coef * a.inv_scale64;
+  d.factor1 = (float)(factor * (1.0 - a.beta1));
+  d.factor2 = (float)(factor * a.root_one_minus_b2);
   d.step = (uint32_t)p.step;
   d.step_size = p.step_size;
   d.inv_root = p.inv_root;
@@ -458,10 +460,8 @@ __device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&num
     w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), number[2 * i]);
     w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), number[2 * i + 1]);
     if (ROOT) {
-      // the smallest step, but for zeros: times 2^126 all else is above it
-      const float2 f = mul2(y, both(0x1p126f));
-      w[i].x = fmaxf(w[i].x, fminf(f.x, 0x1p-9f));
-      w[i].y = fmaxf(w[i].y, fminf(f.y, 0x1p-9f));
+      if (y.x > 0.f) w[i].x = fmaxf(w[i].x, 0x1p-9f);
+      if (y.y > 0.f) w[i].y = fmaxf(w[i].y, 0x1p-9f);
     } else {
       w[i] = make_float2(copysignf(w[i].x, y.x), copysignf(w[i].y, y.y));
     }
@@ -628,11 +628,12 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
   uint32_t number[kUnit];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 g = mul2(pair_of(u.g, i), both(d.factor));
+    // (1 - b1) g and sqrt(1 - b2) g each in one product, sqrt(b2 v) in one
+    const float2 g = pair_of(u.g, i), h = mul2(g, both(d.factor2));
     constexpr int kHalf = STRIDED ? 2 : 4;  // pairs of one scale
-    m[i] = fma2(m[i], both(u.ms[i / kHalf] * a.b1), mul2(g, both(a.one_minus_b1)));
-    const float2 root = mul2(v[i], both(u.vs[i / kHalf]));
-    v[i] = fma2(mul2(root, root), both(a.b2), mul2(mul2(g, g), both(a.one_minus_b2)));
+    m[i] = fma2(m[i], both(u.ms[i / kHalf] * a.b1), mul2(g, both(d.factor1)));
+    const float2 root = mul2(v[i], both(u.vs[i / kHalf] * a.root_b2));
+    v[i] = fma2(root, root, mul2(h, h));
     v[i] = make_float2(root_of(v[i].x), root_of(v[i].y));
     const float2 denom = fma2(v[i], both(d.inv_root), both(a.eps));
     const float2 change = mul2(m[i], make_float2(inverse_of(denom.x), inverse_of(denom.y)));
@@ -643,13 +644,13 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
     if constexpr (STRIDED) {
 #pragma unroll
       for (int e = 2 * i; e < 2 * i + 2; ++e) {
-        const uint32_t at = first + 32 * e, h = mix(key + at / 2);
-        number[e] = at % 2 ? h >> 16 : h & 0xFFFFu;
+        const uint32_t at = first + 32 * e, two = mix(key + at / 2);
+        number[e] = at % 2 ? two >> 16 : two & 0xFFFFu;
       }
     } else {
-      const uint32_t h = mix(key + first / 2 + i);
-      number[2 * i] = h & 0xFFFFu;
-      number[2 * i + 1] = h >> 16;
+      const uint32_t two = mix(key + first / 2 + i);
+      number[2 * i] = two & 0xFFFFu;
+      number[2 * i + 1] = two >> 16;
     }
   }
   u.m8 = hold<false, STRIDED>(m, number, u.ms);

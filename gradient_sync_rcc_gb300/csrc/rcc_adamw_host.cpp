@@ -260,6 +260,8 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   a.lr = cfg->lr;
   a.beta1 = cfg->beta1;
   a.beta2 = cfg->beta2;
+  a.root_one_minus_b2 = std::sqrt(1.0 - cfg->beta2);
+  a.root_b2 = (float)std::sqrt(cfg->beta2);
   a.inv_scale = (float)(1.0 / scale);
   a.b1 = (float)cfg->beta1;
   a.one_minus_b1 = (float)(1.0 - cfg->beta1);
