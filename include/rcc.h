@@ -482,7 +482,8 @@ rcc_status rcc_rmsnorm_backward(const void* dy, rcc_dtype type, size_t ld_dy, co
 /* The norm with the residual's addition before it, and with its output in 8
  * bits:
  *   sum = x + residual, rounded once to `type`;  y = sum r weight with r =
- *   1 / sqrt(mean(sum^2) + eps): the same bits as rcc_rmsnorm_forward's of sum.
+ *   1 / sqrt(mean(sum^2) + eps): rcc_rmsnorm_forward's of sum, bit for bit where
+ *   x and residual lie on 16-byte boundaries if sum does.
  * y_scales NULL: y is of `type`.  Else y is e4m3 (1 sign, 4 exponent and 3
  * fraction bits, largest 448): for each group of 128 columns with a = max|y|,
  *   y = the nearest e4m3 value, ties to even, of y * (448 * (1 / a)),
@@ -553,8 +554,8 @@ typedef struct {
 } rcc_rotary_rows;
 
 /* Turns q and, unless NULL, k (a part of the same packed rows, for instance),
- * both of `type` and head_dim.  positions [tokens], NULL: 0, 1, ...; offset is
- * added to each.  A position below 0 is padding: its rows are only scaled.  The
+ * both of `type` and head_dim.  positions [tokens], NULL: 0, 1, ...; offset, in
+ * [0, 2^31), is added to each.  A position below 0 is padding: its rows are only scaled.  The
  * backward pass turns the other way: gradients of the outputs in, of the inputs
  * out.  tokens of any number; heads up to 65,536, head_dim up to 8,192. */
 rcc_status rcc_rotary_forward(const rcc_rotary_rows* q, const rcc_rotary_rows* k, rcc_dtype type,
