@@ -143,20 +143,22 @@ def add_rmsnorm_forward(x, residual, weight, eps=1e-6, out_dtype=None, keep=Fals
     y is of x's type; with out_dtype=torch.float8_e4m3fn, or a Scaled as `out`,
     it is a Scaled.  h may be x or residual itself.  A residual of None (8-bit
     y) adds nothing and gives an h of None."""
-    eight = out_dtype == torch.float8_e4m3fn or isinstance(out, Scaled)
-    if out_dtype not in (None, x.dtype, torch.float8_e4m3fn) or \
-            (out is not None and isinstance(out, Scaled) != eight):
-        raise ValueError("out_dtype must be x's type or torch.float8_e4m3fn, and out fit it")
-    values, scales = (out.values, out.scales) if isinstance(out, Scaled) else (out, None)
-    buffer, tokens, dim = (keep.data, keep.tokens, keep.dim) if isinstance(keep, Kept) else \
-        (True if keep else None, 0, 0)
+    eight, values, scales = False, None, None
+    if out_dtype is not None or out is not None:
+        eight = out_dtype == torch.float8_e4m3fn or isinstance(out, Scaled)
+        if out_dtype not in (None, x.dtype, torch.float8_e4m3fn) or \
+                (out is not None and isinstance(out, Scaled) != eight):
+            raise ValueError("out_dtype must be x's type or torch.float8_e4m3fn, and out fit it")
+        values, scales = (out.values, out.scales) if isinstance(out, Scaled) else (out, None)
+    if not keep:
+        y, scales, h, _ = _lm.add_rmsnorm_forward(x, residual, weight, eps, eight, None, 0, 0, h,
+                                                  values, scales, stream)
+        return (out or Scaled(y, scales)) if eight else y, h
+    buffer, tokens, dim = (True, 0, 0) if keep is True else (keep.data, keep.tokens, keep.dim)
     y, scales, h, data = _lm.add_rmsnorm_forward(x, residual, weight, eps, eight, buffer, tokens,
                                                  dim, h, values, scales, stream)
-    if eight:
-        y = out if isinstance(out, Scaled) else Scaled(y, scales)
-    if not keep:
-        return y, h
-    return y, h, Kept(x.shape[0], x.shape[1], data=data) if keep is True else keep
+    return (out or Scaled(y, scales)) if eight else y, h, \
+        Kept(x.shape[0], x.shape[1], data=data) if keep is True else keep
 
 
 def add_rmsnorm_backward(dy, dh, kept, weight, eps=1e-6, dx=None, dweight=None, accumulate=False,
