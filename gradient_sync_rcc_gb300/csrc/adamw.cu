@@ -383,7 +383,9 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const 
 // Eight elements as they lie in memory, and the scales of the first and the last
 // four: neighbours, of one group; or (buffers on no boundary, the end of a tensor)
 // every 32nd of the warp's 256, so that a warp's accesses lie side by side and its
-// two groups are the first and the last four of all lanes.
+// two groups are the first and the last four of all lanes.  100 M elements one
+// element off their boundaries, fp32 gradients: fp32 states 538 us a step (507 on
+// them; 1,362 as neighbours, element by element), 8-bit states 650 (325; 867).
 template <bool EIGHT, bool BF16>
 struct Unit {
   Raw<BF16> g;
@@ -793,7 +795,10 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <bool BF16>  // every gradient of the plan is; else they may be mixed
+// BF16: every gradient of the plan is; else they may be mixed, and are widened where
+// they are taken (1,024 tensors of 544 M elements, all bf16: 1,565 us a step, 1,576 by
+// the mixed form).
+template <bool BF16>
 __global__ void __launch_bounds__(kEightThreads, kEightPerSm)
     adamw_update_eight_kernel(const AdamWArgs a) {
   using S = Stage<BF16>;
