@@ -540,7 +540,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---- AdamW over many tensors -----------------------------------------------------
 
-// plan, cfg's address, scale, device, stream
+// plan, cfg's address, scale, device, stream: the stream's handle
 PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry("adamw_step", n, 5, [&] {
     auto plan = static_cast<rcc_adamw>(PyLong_AsVoidPtr(a[0]));
@@ -552,7 +552,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) throw python_error();
     const Stream stream(a[4], at::Device(at::kCUDA, (c10::DeviceIndex)device));
     call(rcc_.adamw_step, plan, cfg, scale, stream.handle());
-    return Py_NewRef(Py_None);
+    return PyLong_FromVoidPtr(stream.handle());
   });
 }
 

@@ -235,8 +235,10 @@ class AdamWPlan:
 
     The tensors' addresses are kept: a step reads the gradients where they were.
     The plan and the states it makes belong to `stream`; steps on another one have
-    to wait for it.  One step after the other: a plan's steps, and graphs of them,
-    share its workspace; graphs need the plan (its workspace) to live."""
+    to wait for it, and that one, if it is not torch's, has to live as long as the
+    plan.  A plan may be dropped while its steps run, but graphs need it to live.
+    One step after the other: a plan's steps, and graphs of them, share its
+    workspace."""
 
     def __init__(self, tensors, states=torch.float32, seed=0, step=0, betas=(0.9, 0.999),
                  stream=None):
@@ -253,7 +255,9 @@ class AdamWPlan:
             raise ValueError("the operators take tensors on a CUDA device")
         _lm.check_device(dev.index, torch.cuda.current_device())
         self.device = dev.index
+        given = {id(v) for t in tensors for v in t.values()}
         with _lm_stream(stream, dev):
+            self.streams = {torch.cuda.current_stream().cuda_stream}   # that its memory is known to
             self.tensors = [self._with_states(t, states) for t in tensors]
             arr = (_rcc.AdamWTensor * len(self.tensors))(*map(self._entry, self.tensors))
             need = _lib.rcc_adamw_workspace(arr, len(arr))
@@ -264,6 +268,8 @@ class AdamWPlan:
                 self.workspace.data_ptr(), need, torch.cuda.current_stream().cuda_stream,
                 C.byref(handle)))
         self.handle = handle.value
+        self._own = [self.workspace] + [v for t in self.tensors for v in t.values()
+                                        if id(v) not in given]
         # the last step's gradient norm: float64, on the device, written by each step
         self.grad_norm = self.workspace[8:16].view(torch.float64)[0]
 
@@ -316,20 +322,27 @@ class AdamWPlan:
             p["exp_avg"], p["exp_avg_sq"], p.get("exp_avg_scale"), p.get("exp_avg_sq_scale"),
             p.get("copy"))
 
+    def _used_on(self, stream):
+        """Memory that a step on another stream may still be using is not given out
+        again before that step is through."""
+        self.streams.add(stream)
+        for v in self._own:
+            v.record_stream(_stream_of(stream, self.workspace.device))
+
     def __del__(self):
         if self.handle is not None and _lib is not None:   # None: the interpreter ends
             _lib.rcc_adamw_destroy(self.handle)
             self.handle = None
 
 
+def _stream_of(handle, dev):
+    return torch.cuda.default_stream(dev) if handle in (0, 1) else \
+        torch.cuda.ExternalStream(handle, device=dev)
+
+
 def _lm_stream(stream, dev):
     """The given stream as the current one, as the compiled calls have it."""
-    if stream is None:
-        return torch.cuda.stream(None)
-    if isinstance(stream, int):
-        stream = torch.cuda.default_stream(dev) if stream in (0, 1) else \
-            torch.cuda.ExternalStream(stream, device=dev)
-    return torch.cuda.stream(stream)
+    return torch.cuda.stream(_stream_of(stream, dev) if isinstance(stream, int) else stream)
 
 
 def adamw_step(plan, cfg, scale=1.0, stream=None):
@@ -337,7 +350,9 @@ def adamw_step(plan, cfg, scale=1.0, stream=None):
     the loss scale `scale`.  cfg: adamw_cfg.  Nothing is read back."""
     if not isinstance(cfg, _rcc.AdamWCfg):
         raise ValueError("cfg must be one of adamw_cfg's")
-    _lm.adamw_step(plan.handle, C.addressof(cfg), scale, plan.device, stream)
+    used = _lm.adamw_step(plan.handle, C.addressof(cfg), scale, plan.device, stream)
+    if used not in plan.streams:
+        plan._used_on(used)
 
 
 def adamw_report(plan, stream=None):

@@ -193,3 +193,37 @@ def test_graphs_of_two_plans_in_turn():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(params, plain))
     assert [rcc.adamw_report(p).step for p in plans] == [5, 5]
+
+
+@pytest.mark.parametrize("states", [torch.float32, E4M3])
+@pytest.mark.parametrize("other", ["stream", "default", "handle"])
+def test_a_plan_is_dropped_while_a_step_runs_on_another_stream(states, other):
+    """Its workspace, and the states that it made, are not given out before the step
+    is through."""
+    n = 3 << 20   # blocks of their own in the allocator
+    g = defs.gen(127)
+    param, grad = defs.randn(g, n), defs.randn(g, n)
+    want = param.clone()
+    alone = rcc.AdamWPlan([dict(param=want, grad=grad)], states=states)
+    rcc.adamw_step(alone, rcc.adamw_cfg())
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    made_on, run_on = (one, torch.cuda.default_stream()) if other == "default" else \
+        (torch.cuda.default_stream(), two)
+    plan = rcc.AdamWPlan([dict(param=param, grad=grad)], states=states, stream=made_on)
+    held = [plan.workspace] + [plan.tensors[0][k] for k in ("exp_avg", "exp_avg_sq")]
+    places = [(v.data_ptr(), v.data_ptr() + v.nbytes, v.nbytes) for v in held]
+    del held
+    torch.cuda.synchronize()
+    with torch.cuda.stream(run_on):
+        torch.cuda._sleep(DELAY)
+    rcc.adamw_step(plan, rcc.adamw_cfg(),
+                   stream=run_on.cuda_stream if other == "handle" else run_on)
+    del plan
+    with torch.cuda.stream(made_on):
+        new = [torch.empty(size, dtype=torch.uint8, device=DEV) for _, _, size in places * 2]
+    assert not run_on.query()   # the step is still to come
+    for v in new:
+        assert all(v.data_ptr() + v.nbytes <= lo or v.data_ptr() >= hi for lo, hi, _ in places)
+    torch.cuda.synchronize()
+    assert torch.equal(param, want)
