@@ -3,8 +3,8 @@
 //   g = grad (1/scale) coef,  coef = max_grad_norm / |g| where that is less than 1
 //   m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2
 //   p = p (1 - lr wd) - lr/(1-b1^t) m / (sqrt(v) / sqrt(1-b2^t) + eps)
-// With fp32 states every operation is rounded, in the order of
-// rcc_grad_sync_adamw's, whose bits these are.
+// Every operation is rounded to fp32, in the order of rcc_grad_sync_adamw's, whose
+// bits these are with fp32 states.
 //
 // States in 8 bits: m and sqrt(v) (half the range of v, and what is divided by)
 // as e4m3 with one scale for 128 elements, the smallest power of two that holds
@@ -22,6 +22,7 @@
 // tensor), the update from its end, where the gradients are still in L2.
 #include "lm_common.cuh"
 #include "lm_internal.h"
+#include "rounded.cuh"
 
 namespace rcc {
 namespace lm {
@@ -300,9 +301,6 @@ __device__ __forceinline__ void decide(const AdamWArgs& a, const Powers& p, doub
   d.skip = bad > 0 || !(norm < INFINITY);
   const double coef = !d.skip && a.max_norm > 0.0 && norm > a.max_norm ? a.max_norm / norm : 1.0;
   d.coef = (float)coef;
-  const double factor = (double)d.coef * a.inv_scale64;
-  d.factor1 = (float)(factor * (1.0 - a.beta1));
-  d.factor2 = (float)(factor * a.root_one_minus_b2);
   d.step = (uint32_t)p.step;
   d.step_size = p.step_size;
   d.inv_root = p.inv_root;
@@ -419,11 +417,11 @@ __device__ __forceinline__ uint2 narrow_e4m3(const float2 (&v)[4]) {
 }
 
 // y >= 0 on the grid of e4m3, up with a chance of its distance over a step:
-// `number` of 2^16.  Below 2^-6 the grid is even, as it is from 2^-6 to 2^-5.
-// Over 448 is left to the conversion, which saturates.
+// `number` of 2^20, in steps of 16.  Below 2^-6 the grid is even, as it is from 2^-6
+// to 2^-5.  Over 448 is left to the conversion, which saturates.
 __device__ __forceinline__ float round_e4m3(float y, uint32_t number) {
   const float low = y < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t b = (__float_as_uint(__fadd_rn(y, low)) + (number << 4)) & 0xFFF00000u;
+  const uint32_t b = (__float_as_uint(__fadd_rn(y, low)) + number) & 0xFFF00000u;
   return __fsub_rn(__uint_as_float(b), low);
 }
 
@@ -437,30 +435,39 @@ __device__ __forceinline__ float scale_for(uint32_t top, float& inv) {
   return some ? __uint_as_float(top > 0x7F800000u ? top : s) : 0.f;
 }
 
-// What eight values are held as, and their scales
+// The bits of the largest of a thread's values (ROOT: none is negative), of each group
 template <bool ROOT, bool STRIDED>
-__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&number)[kUnit],
-                                      float (&scale)[2]) {
-  float inv[2];
+__device__ __forceinline__ void top_of(const float2 (&v)[4], uint32_t (&top)[2]) {
 #pragma unroll
   for (int half = 0; half < (STRIDED ? 2 : 1); ++half) {
-    uint32_t top = 0;
+    top[half] = 0;
 #pragma unroll
     for (int i = 2 * half; i < (STRIDED ? 2 * half + 2 : 4); ++i) {
       const uint32_t x = __float_as_uint(v[i].x), y = __float_as_uint(v[i].y);
-      top = ROOT ? max(max(top, x), y) : max(max(top, x << 1), y << 1);  // but their signs
+      top[half] = ROOT ? max(max(top[half], x), y) : max(max(top[half], x << 1), y << 1);
     }
+    if (!ROOT) top[half] >>= 1;
+  }
+}
+
+// What eight values are held as, and their scales.  `top`: of the thread's values.
+// `number`: of two elements each, 16 bits of them.
+template <bool ROOT, bool STRIDED>
+__device__ __forceinline__ uint2 hold(const float2 (&v)[4], const uint32_t (&top)[2],
+                                      const uint32_t (&number)[4], float (&scale)[2]) {
+  float inv[2];
+#pragma unroll
+  for (int half = 0; half < (STRIDED ? 2 : 1); ++half) {
     // over the threads of the group; a NaN's bits are the largest of all
     const uint32_t lanes = STRIDED ? 0xFFFFFFFFu : threadIdx.x & 16 ? 0xFFFF0000u : 0x0000FFFFu;
-    top = __reduce_max_sync(lanes, top);
-    scale[half] = scale_for(ROOT ? top : top >> 1, inv[half]);
+    scale[half] = scale_for(__reduce_max_sync(lanes, top[half]), inv[half]);
   }
   float2 w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = mul2(v[i], both(inv[STRIDED ? i / 2 : 0]));
-    w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), number[2 * i]);
-    w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), number[2 * i + 1]);
+    w[i].x = round_e4m3(ROOT ? y.x : fabsf(y.x), number[i] << 4 & 0xFFFF0u);
+    w[i].y = round_e4m3(ROOT ? y.y : fabsf(y.y), number[i] >> 12 & 0xFFFF0u);
     if (ROOT) {
       if (y.x > 0.f) w[i].x = fmaxf(w[i].x, 0x1p-9f);
       if (y.y > 0.f) w[i].y = fmaxf(w[i].y, 0x1p-9f);
@@ -606,57 +613,88 @@ __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecis
   }
 }
 
-__device__ __forceinline__ float root_of(float v) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float inverse_of(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
+// Whether denominators are in quotient2's range for all v <= kMost (sqrt(v) <= 2^15),
+// and the step size over 2^64 is exact
+__device__ __forceinline__ bool in_range(const AdamWArgs& a, const AdamWDecision& d) {
+  return a.eps >= 0x1p-30f && a.eps <= 1.f && d.inv_root <= 0x1p8f &&
+         (d.step_size >= 0x1p-62f || d.step_size == 0.f);
 }
 
-// 8-bit states: two elements an operation, products fused into sums, root and
-// quotient to 2^-22: what is held keeps four bits of it.
+// 8-bit states: what they stand for (value times scale; a root's square is v), then
+// the same operations, each rounded, two elements at a time.  So the bytes are the
+// definition's, step after step: a value that one last place moves across its
+// rounding number is held a whole step of the grid off, and its parameter goes
+// another way from there on.  (Products fused into sums and roots to 2^-22: 1,562 us
+// where this takes 1,754, 450 of 544 M values off after one step, and after twelve
+// parameters by 0.1 of their root mean square.)
 // `key`: of the rounding numbers of the block of kNumbered elements, `first`: the
-// thread's first element in it.
+// thread's first element in it.  `usual`: in_range.
 template <bool STRIDED, bool BF16>
 __device__ __forceinline__ void update_unit(const AdamWArgs& a, const AdamWDecision& d,
-                                            uint32_t key, uint32_t first, Unit<true, BF16>& u) {
+                                            uint32_t key, uint32_t first, bool usual,
+                                            Unit<true, BF16>& u) {
   float2 m[4], v[4];
   widen_e4m3(u.m8, m);
   widen_e4m3(u.v8, v);
-  uint32_t number[kUnit];
+  uint32_t most = 0;  // of v and |m|, their bits
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // (1 - b1) g and sqrt(1 - b2) g each in one product, sqrt(b2 v) in one
-    const float2 g = pair_of(u.g, i), h = mul2(g, both(d.factor2));
+    const float2 g = mul2(mul2(pair_of(u.g, i), both(a.inv_scale)), both(d.coef));
     constexpr int kHalf = STRIDED ? 2 : 4;  // pairs of one scale
-    m[i] = fma2(m[i], both(u.ms[i / kHalf] * a.b1), mul2(g, both(d.factor1)));
-    const float2 root = mul2(v[i], both(u.vs[i / kHalf] * a.root_b2));
-    v[i] = fma2(root, root, mul2(h, h));
-    v[i] = make_float2(root_of(v[i].x), root_of(v[i].y));
-    const float2 denom = fma2(v[i], both(d.inv_root), both(a.eps));
-    const float2 change = mul2(m[i], make_float2(inverse_of(denom.x), inverse_of(denom.y)));
-    const float2 p = fma2(change, both(-d.step_size),
-                          mul2(make_float2(u.p[2 * i], u.p[2 * i + 1]), both(a.decay)));
-    u.p[2 * i] = p.x;
-    u.p[2 * i + 1] = p.y;
-    if constexpr (STRIDED) {
+    m[i] = mul2(m[i], both(u.ms[i / kHalf]));
+    m[i] = sum2(mul2(m[i], both(a.b1)), mul2(g, both(a.one_minus_b1)), a.one);
+    const float2 root = mul2(v[i], both(u.vs[i / kHalf]));
+    v[i] = sum2(mul2(mul2(root, root), both(a.b2)), mul2(mul2(g, g), both(a.one_minus_b2)), a.one);
+    most = max(most, max(__float_as_uint(v[i].x), __float_as_uint(v[i].y)));
+  }
+  uint32_t top[2];
+  top_of<false, STRIDED>(m, top);
+  most = max(most, STRIDED ? max(top[0], top[1]) : top[0]);
+  if (usual && most <= __float_as_uint(kMost)) {  // a NaN's bits are more
 #pragma unroll
-      for (int e = 2 * i; e < 2 * i + 2; ++e) {
-        const uint32_t at = first + 32 * e, two = mix(key + at / 2);
-        number[e] = at % 2 ? two >> 16 : two & 0xFFFFu;
-      }
-    } else {
-      const uint32_t two = mix(key + first / 2 + i);
-      number[2 * i] = two & 0xFFFFu;
-      number[2 * i + 1] = two >> 16;
+    for (int i = 0; i < 4; ++i) {
+      v[i] = root2(v[i]);
+      const float2 denom = sum2(mul2(v[i], both(d.inv_root)), both(a.eps), a.one);
+      const float2 p = sum2(mul2(make_float2(u.p[2 * i], u.p[2 * i + 1]), both(a.decay)),
+                            mul2(quotient2(m[i], denom), both(d.step_size * -0x1p-64f)), a.one);
+      u.p[2 * i] = p.x;
+      u.p[2 * i + 1] = p.y;
+    }
+  } else {  // a loop: where it is not taken, it costs no registers
+    float mm[kUnit], vv[kUnit], pp[kUnit];
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e) {
+      mm[e] = e % 2 ? m[e / 2].y : m[e / 2].x;
+      vv[e] = e % 2 ? v[e / 2].y : v[e / 2].x;
+      pp[e] = u.p[e];
+    }
+#pragma unroll 1
+    for (int e = 0; e < kUnit; ++e) {
+      vv[e] = __fsqrt_rn(vv[e]);
+      const float denom = __fadd_rn(__fmul_rn(vv[e], d.inv_root), a.eps);
+      const float change = __fdiv_rn(mm[e], denom);
+      pp[e] = __fsub_rn(__fmul_rn(pp[e], a.decay), __fmul_rn(d.step_size, change));
+    }
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e) {
+      (e % 2 ? v[e / 2].y : v[e / 2].x) = vv[e];
+      u.p[e] = pp[e];
     }
   }
-  u.m8 = hold<false, STRIDED>(m, number, u.ms);
-  u.v8 = hold<true, STRIDED>(v, number, u.vs);
+  uint32_t number[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (STRIDED) {  // both elements are the first, or the second, of their two
+      const uint32_t at = first + 64 * i;
+      number[i] = __byte_perm(mix(key + at / 2), mix(key + at / 2 + 16),
+                              at % 2 ? 0x7632 : 0x5410);
+    } else {
+      number[i] = mix(key + first / 2 + i);
+    }
+  }
+  u.m8 = hold<false, STRIDED>(m, top, number, u.ms);
+  top_of<true, STRIDED>(v, top);
+  u.v8 = hold<true, STRIDED>(v, top, number, u.vs);
 }
 
 // fp32 states: a thread's loads are bytes enough by themselves.
@@ -868,6 +906,7 @@ __global__ void __launch_bounds__(kEightThreads, kEightPerSm)
   pdl_wait_then_release();
   const AdamWDecision d = *a.decision;
   if (d.skip) return;
+  const bool usual = in_range(a, d);
   const uint32_t step_key = mix(a.seed ^ mix(d.step));
   for (uint64_t n = 0; n < items; ++n, next()) {
     if (!bar_wait(full + 8 * s, parity)) {
@@ -885,11 +924,11 @@ __global__ void __launch_bounds__(kEightThreads, kEightPerSm)
         take_unit<BF16>(stage, e.t.bf16, u);
       else
         load_vectors(e.t, warp, u);
-      update_unit<false>(a, d, key, (uint32_t)(neighbours(warp) % kNumbered), u);
+      update_unit<false>(a, d, key, (uint32_t)(neighbours(warp) % kNumbered), usual, u);
       store_vectors(e.t, warp, u);
     } else {
       load_strided(e.t, warp, u);
-      update_unit<true>(a, d, key, (uint32_t)(strided(warp) % kNumbered), u);
+      update_unit<true>(a, d, key, (uint32_t)(strided(warp) % kNumbered), usual, u);
       store_strided(e.t, warp, u);
     }
     __syncwarp();

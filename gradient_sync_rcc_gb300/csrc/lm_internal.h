@@ -143,7 +143,6 @@ struct AdamWRow {             // a block's part of the norm
 struct AdamWDecision {
   uint32_t skip, step;        // step: steps taken before, its low bits
   float coef, step_size, inv_root;
-  float factor1, factor2;     // coef / scale times 1 - beta1, sqrt(1 - beta2)
 };
 struct AdamWArgs {
   const AdamWTensor* tensors;
@@ -156,8 +155,9 @@ struct AdamWArgs {
   int sms;                    // that the rows have room for
   bool all_bf16;              // every gradient
   uint32_t seed;
-  double inv_scale64, max_norm, lr, beta1, beta2, root_one_minus_b2;
-  float inv_scale, b1, one_minus_b1, b2, one_minus_b2, root_b2, eps, decay;
+  double inv_scale64, max_norm, lr, beta1, beta2;
+  float inv_scale, b1, one_minus_b1, b2, one_minus_b2, eps, decay;
+  float one;                  // 1, where the compiler must not see it
 };
 int adamw_sms();              // of the current device
 int adamw_rows(int sms);

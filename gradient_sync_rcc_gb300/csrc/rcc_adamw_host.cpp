@@ -260,8 +260,6 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   a.lr = cfg->lr;
   a.beta1 = cfg->beta1;
   a.beta2 = cfg->beta2;
-  a.root_one_minus_b2 = std::sqrt(1.0 - cfg->beta2);
-  a.root_b2 = (float)std::sqrt(cfg->beta2);
   a.inv_scale = (float)(1.0 / scale);
   a.b1 = (float)cfg->beta1;
   a.one_minus_b1 = (float)(1.0 - cfg->beta1);
@@ -269,6 +267,7 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
   a.one_minus_b2 = (float)(1.0 - cfg->beta2);
   a.eps = (float)cfg->eps;
   a.decay = (float)(1.0 - cfg->lr * cfg->weight_decay);
+  a.one = 1.f;
   uint64_t launches = 0;
   const cudaError_t e = launch_adamw(a, p.eight, reinterpret_cast<cudaStream_t>(stream), &launches);
   rcc::add_launches(launches);

@@ -652,10 +652,13 @@ rcc_status rcc_adamw_create(const rcc_adamw_tensor* tensors, int num_tensors, ui
  *   norm = |grad| / scale (good to 2^-40); a gradient or norm that is not finite:
  *   nothing changes but the status;
  *   t = step + 1, g = grad / scale * coef, coef = max_grad_norm / norm where 0 <
- *   max_grad_norm < norm, else 1, and then rcc_grad_sync_adamw's update in fp32.
- * With fp32 states that is fl32(fl32(grad * fl32(1 / scale)) * coef) and the same
- * bits as there; with 8-bit states the gradient has one factor, products are fused
- * into sums, and root and quotient are good to 2^-22.
+ *   max_grad_norm < norm, else 1, and then rcc_grad_sync_adamw's update in fp32,
+ * every operation rounded:
+ *   g = (grad * fl32(1 / scale)) * coef
+ *   m = fl32(b1) * m + fl32(1 - b1) * g,  v = fl32(b2) * v + fl32(1 - b2) * (g * g)
+ *   param = param * fl32(1 - lr wd)
+ *           - fl32(lr / (1 - b1^t)) * (m / (sqrt(v) * fl32(1 / sqrt(1 - b2^t)) + eps))
+ * With fp32 states these are the bits of that call.
  * Of cfg lr, beta1, beta2, eps, weight_decay and max_grad_norm count; replicas
  * must be 1 and flags 0; eps must be a normal fp32 number.
  *
@@ -664,8 +667,13 @@ rcc_status rcc_adamw_create(const rcc_adamw_tensor* tensors, int num_tensors, ui
  * group is then held as zeros); they are held as |x| / s on the grid of e4m3,
  * saturating at 448, the value above with the chance of the distance from the
  * one below in sixteen-bit steps, which keeps small changes of a moment on
- * average; a u > 0 is held as 2^-9 at least.  m / sqrt(v) of this step is taken
- * before they are rounded.  The sixteen bits are, for elements 2 j and 2 j + 1
+ * average; a u > 0 is held as 2^-9 at least.  A step begins with m = value * s and
+ * v = u * u of u = value * s, takes m / sqrt(v) as above, and then rounds: with y =
+ * |x| / s and l = 2^-6 where y is below that, else 0, the bits of y + l in fp32 plus
+ * the sixteen bits times 16, without their lowest twenty, less l.  So the states are
+ * the same bits wherever they are computed (parameters too, but that a quotient
+ * below 2^-126 is not rounded to the 2^-149 of such numbers before its product).
+ * The sixteen bits are, for elements 2 j and 2 j + 1
  * of a tensor's 4,096, c-th block, the lower and upper half of
  *   h(h(h(h(seed ^ h(step)) + tensor * 0x9E3779B9) ^ c) + j)
  * in 32 bits with step the steps taken before and h(x): x ^= x >> 16; x *=
