@@ -276,9 +276,10 @@ constexpr int blocks_per_sm(int all, int threads, int shared) {
 // Rows copied ahead into shared memory.  Aligned rows (VEC): a thread writes and
 // reads its own parts alone, so the copies need no barrier; a group's scale is one
 // lane's copy, for the lanes of its warp.  Others: in whole 16 bytes that reach
-// into the neighbouring rows, read back element by element behind a barrier
+// into the neighbouring rows, read back element by element behind a barrier, with
+// another one between the last of that and the next copies into the same stage
 // (16,384 x 4,095 bf16: 85 us instead of 102, with the residual 125 instead of 198,
-// backward with kAdd 122 instead of 211; the backward pass without it stays as it
+// backward with kAdd 120 instead of 211; the backward pass without it stays as it
 // was: its dweight would be summed in another order).
 constexpr int kWindow = 32;  // bytes that a row's copy may be longer than the row
 template <typename T, int G, int NV, bool VEC, int MORE>
@@ -522,6 +523,14 @@ struct NormBack {
                                      ? (kFit < kBackStages ? kFit : kBackStages) : 0;
   static constexpr int kShared = kWeight + kStages * kStage;
   static constexpr int kPerSm = blocks_per_sm(kStages ? kBackThreads : kBackDirect, kThreads, kShared);
+  // Rows that are not aligned: dsum is read from its stage in front of the row's
+  // reduction, whose barrier then stands between it and the next copies into that
+  // stage; or, where a thread has no registers to hold it in, behind the reduction,
+  // and a barrier of its own stands in front of the copies.  16,384 x 4,095 bf16 120 us
+  // against 124, 8,190 x 8,191 131 against 137; fp32 4,095 183 against 182, 8,191 165
+  // against 152; 4,095 x 16,383 bf16 198 against 184.
+  static constexpr bool kEarly = kStages > 0 && !VEC && (MORE & kAdd) != 0 &&
+                                 kThreads * (int)sizeof(T) <= 1024;
   // a block's rows of partial sums are added up where the weight was
   static constexpr bool kJoin = (MORE & kAdd) != 0 && kThreads > G && kHoldWeight;
 };
@@ -663,7 +672,9 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
     [[maybe_unused]] const int8_t* kept_here = kept;
     [[maybe_unused]] const float* scales_here = scales;
     if constexpr (kStages > 0) {
-      if constexpr (!VEC && G == 32) __syncwarp();  // all lanes are through with the stage
+      // Other threads' copies go into the stage that this one has read.  Of G > 32 the
+      // barrier of row_sum is between all that is read in front of it and them.
+      if constexpr (!VEC && (G == 32 || !B::kEarly)) sync_row<G>();
       copy_row(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
       if constexpr (VEC) {
@@ -680,6 +691,7 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
     }
     // kept over the reduction: dy w, and dy and the bytes as they came
     uint4 raw[kParts];
+    [[maybe_unused]] uint4 raw_dh[kParts];  // kEarly
     uint32_t q[kParts][P::kBytes8];
     float2 dw[kParts][P::kPairs];
     float scale[kParts][P::kScales];
@@ -695,6 +707,7 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
         } else {
           raw[p] = load_part<VEC>(dy_here + p * kSpan, left - p * kSpan);
           load_bytes<VEC>(kept_here + p * kSpan, left - p * kSpan, q[p]);
+          if constexpr (B::kEarly) raw_dh[p] = load_part<VEC>(dh_here + p * kSpan, left - p * kSpan);
 #pragma unroll
           for (int i = 0; i < P::kScales; ++i)
             scale[p][i] = left > p * kSpan + i * (int)kKeepGroup
@@ -738,9 +751,12 @@ __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPer
         }
         if constexpr ((MORE & kAdd) != 0) {
           float2 more[P::kPairs];
-          widen(VEC && kStages > 0 ? *dh_at(stage, p)
-                                   : load_part<VEC>(dh_here + p * kSpan, left - p * kSpan),
-                more, T());
+          if constexpr (B::kEarly)
+            widen(raw_dh[p], more, T());
+          else
+            widen(VEC && kStages > 0 ? *dh_at(stage, p)
+                                     : load_part<VEC>(dh_here + p * kSpan, left - p * kSpan),
+                  more, T());
 #pragma unroll
           for (int e = 0; e < P::kPairs; ++e) out[e] = add2(out[e], more[e]);
         }
