@@ -241,7 +241,8 @@ rcc_status rcc_adamw_step(rcc_adamw plan, const rcc_adamw_cfg* cfg, double scale
     return fail(bad, "eps must be > 0 and a normal fp32 number");
   if (!std::isfinite(cfg->weight_decay) || !std::isfinite(cfg->max_grad_norm))
     return fail(bad, "weight_decay and max_grad_norm must be finite");
-  if (!finite_pos(scale)) return fail(bad, "scale must be finite and > 0");
+  if (!finite_pos(scale) || !std::isnormal((float)(1.0 / scale)))
+    return fail(bad, "scale must be > 0, and 1 / scale a normal fp32 number");
   rcc_status st = check_device(p.device);
   if (st != RCC_OK) return st;
   AdamWArgs a = {};

@@ -660,7 +660,7 @@ rcc_status rcc_adamw_create(const rcc_adamw_tensor* tensors, int num_tensors, ui
  *           - fl32(lr / (1 - b1^t)) * (m / (sqrt(v) * fl32(1 / sqrt(1 - b2^t)) + eps))
  * With fp32 states these are the bits of that call.
  * Of cfg lr, beta1, beta2, eps, weight_decay and max_grad_norm count; replicas
- * must be 1 and flags 0; eps must be a normal fp32 number.
+ * must be 1 and flags 0; eps and 1 / scale must be normal fp32 numbers.
  *
  * 8-bit states: m and u = sqrt(v) of 128 neighbours share a scale, the smallest
  * power of two s with max <= 448 s (0 where the max is below 2^-100, and the
