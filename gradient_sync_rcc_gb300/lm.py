@@ -257,7 +257,8 @@ class AdamWPlan:
         self.device = dev.index
         given = {id(v) for t in tensors for v in t.values()}
         with _lm_stream(stream, dev):
-            self.streams = {torch.cuda.current_stream().cuda_stream}   # that its memory is known to
+            self.last = torch.cuda.current_stream().cuda_stream   # stream of the last step
+            self.streams = {self.last}                            # that its memory is known to
             self.tensors = [self._with_states(t, states) for t in tensors]
             arr = (_rcc.AdamWTensor * len(self.tensors))(*map(self._entry, self.tensors))
             need = _lib.rcc_adamw_workspace(arr, len(arr))
@@ -351,13 +352,17 @@ def adamw_step(plan, cfg, scale=1.0, stream=None):
     if not isinstance(cfg, _rcc.AdamWCfg):
         raise ValueError("cfg must be one of adamw_cfg's")
     used = _lm.adamw_step(plan.handle, C.addressof(cfg), scale, plan.device, stream)
+    plan.last = used
     if used not in plan.streams:
         plan._used_on(used)
 
 
 def adamw_report(plan, stream=None):
-    """What the plan's last step did, an AdamWStatus: waits for it."""
-    with _lm_stream(stream, plan.workspace.device):
+    """What the plan's last step did, an AdamWStatus: waits for it, on whichever
+    stream adamw_step ran it, and for what is on `stream` (replays of a graph)."""
+    dev = plan.workspace.device
+    with _lm_stream(stream, dev):
+        torch.cuda.current_stream(dev).wait_stream(_stream_of(plan.last, dev))
         return _rcc.AdamWStatus.from_buffer_copy(
             plan.workspace[:C.sizeof(_rcc.AdamWStatus)].cpu().numpy().tobytes())
 
