@@ -145,7 +145,7 @@ def add_rmsnorm_forward(x, residual, weight, eps=1e-6, out_dtype=None, keep=Fals
     y) adds nothing and gives an h of None."""
     eight, values, scales = False, None, None
     if out_dtype is not None or out is not None:
-        eight = out_dtype == torch.float8_e4m3fn or isinstance(out, Scaled)
+        eight = isinstance(out, Scaled) if out_dtype is None else out_dtype == torch.float8_e4m3fn
         if out_dtype not in (None, x.dtype, torch.float8_e4m3fn) or \
                 (out is not None and isinstance(out, Scaled) != eight):
             raise ValueError("out_dtype must be x's type or torch.float8_e4m3fn, and out fit it")
