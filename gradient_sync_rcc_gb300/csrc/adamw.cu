@@ -39,13 +39,14 @@ constexpr uint32_t kNothingBits = 27u << 23;  // 2^-100: a group below it is hel
 
 // Blocks that an SM holds, of each kernel, vectors of eight fp32 gradients that a
 // thread of the norm has under way (bf16: twice as many), stages of the 8-bit
-// update.  Measured on 544 M elements of 1,024 tensors: the norm of bf16 182 us
-// (6.0 TB/s); 208 with eight blocks of 32 registers, 184 with three.  The
-// 8-bit update with three blocks and two stages 1.39 ms (6.3 TB/s), three stages
-// 1.49, four blocks 1.47, two blocks (of three stages) 1.40; loaded by its threads
-// instead of copied ahead 1.58, with a block barrier for each stage 1.68.
+// update.  A step of 544 M elements of 1,024 tensors, bf16 gradients, in 8-bit
+// states: 1,748 us (102 M in one tensor, fp32 gradients: 369).  With three blocks of
+// the norm 16 us more, with eight of 32 registers 34.  Update: two stages 1,777 (376),
+// four 1,752 (403); two blocks of four stages 1,822 (386), four blocks of two 1,834
+// (380).  With fused arithmetic, 1,562: loaded by its threads instead of copied ahead
+// 190 us more, with a block barrier for each stage 290.
 constexpr int kNormPerSm = 4, kNormAhead = 2, kUpdatePerSm = 4;
-constexpr int kEightPerSm = 3, kStages = 2;
+constexpr int kEightPerSm = 3, kStages = 3;
 
 static_assert(kAdamWItem == kThreads * kUnit && kNumbered % kAdamWItem == 0 && kLanes == 16,
               "whole units and groups");
@@ -422,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm) adamw_norm_kernel(const 
 // four: neighbours, of one group; or (buffers on no boundary, the end of a tensor)
 // every 32nd of the warp's 256, so that a warp's accesses lie side by side and its
 // two groups are the first and the last four of all lanes.  100 M elements one
-// element off their boundaries, fp32 gradients: fp32 states 538 us a step (507 on
-// them; 1,362 as neighbours, element by element), 8-bit states 650 (325; 867).
+// element off their boundaries, fp32 gradients: fp32 states 558 us a step (506 on
+// them; 1,362 as neighbours, element by element), 8-bit states 677 (360).
 template <bool EIGHT, bool BF16>
 struct Unit {
   Raw<BF16> g;
@@ -665,7 +666,7 @@ __device__ __forceinline__ bool in_range(const AdamWArgs& a, const AdamWDecision
 // definition's, step after step: a value that one last place moves across its
 // rounding number is held a whole step of the grid off, and its parameter goes
 // another way from there on.  (Products fused into sums and roots to 2^-22: 1,562 us
-// where this takes 1,754, 450 of 544 M values off after one step, and after twelve
+// where this took 1,754, 450 of 544 M values off after one step, and after twelve
 // parameters by 0.1 of their root mean square.)
 // `key`: of the rounding numbers of the block of kNumbered elements, `first`: the
 // thread's first element in it.  `usual`: in_range.
@@ -874,7 +875,7 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 }
 
 // BF16: every gradient of the plan is; else they may be mixed, and are widened where
-// they are taken (1,024 tensors of 544 M elements, all bf16: 1,565 us a step, 1,576 by
+// they are taken (1,024 tensors of 544 M elements, all bf16: 1,748 us a step, 1,775 by
 // the mixed form).
 template <bool BF16>
 __global__ void __launch_bounds__(kEightThreads, kEightPerSm)
