@@ -505,7 +505,11 @@ __global__ void __launch_bounds__(kBlock<G>) norm_forward_kernel(const NormArgs 
 
 // What a block of the backward pass holds in shared memory: the weight, and
 // rows of dy, the 8-bit input and its scales copied ahead.  Where not even two
-// rows fit (fp32 rows of more than 16,384) nothing is copied ahead.
+// rows fit (fp32 rows of more than 16,384; with kAdd, two inputs, fp32 of more than
+// 8,192 and bf16 of more than 16,384) nothing is copied ahead and one block an SM
+// loads as it goes.  With kAdd (without), 67 M elements: fp32 of 8,192 columns 134 us
+// (98), of 12,288 217 (159), of 20,480 385 (241); bf16 of 8,192 74 (69), of 16,384
+// 120 (93), of 20,480 205 (181).
 template <typename T, int G, int NV, bool VEC, int MORE>
 struct NormBack {
   static constexpr int kThreads = kBlock<G>;
@@ -539,7 +543,7 @@ struct NormBack {
 // its columns in registers over all of its rows, and each block writes one
 // row of partial sums, which norm_dweight_kernel adds in a fixed order.
 // Bandwidth bound: rows are copied ahead into shared memory (aligned rows, VEC;
-// with kAdd all) while the current one is reduced.
+// with kAdd others too) while the current one is reduced, where two of them fit.
 template <typename T, int G, int NV, bool VEC, int MORE>
 __global__ void __launch_bounds__(kBlock<G>, NormBack<T, G, NV, VEC, MORE>::kPerSm)
     norm_backward_kernel(const NormGradArgs a) {

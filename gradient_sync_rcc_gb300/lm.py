@@ -208,7 +208,8 @@ def rotary_forward(q, k, turns, positions=None, offset=0, layout="half", scale=1
                    k_out=None, stream=None):
     """rcc_rotary_forward: q and k [tokens, heads, head_dim] (k may be None),
     turned by their tokens' positions: positions + offset, or 0, 1, ... + offset.
-    Returns (q, k) turned.  Any strides but the last; q_out may be q itself."""
+    Returns (q, k) turned.  Any strides that keep the heads apart (none of them 0), but
+    a head's elements lie side by side; q_out may be q itself."""
     return _lm.rotary(False, q, k, turns, positions, offset, _layout(layout), scale, q_out, k_out,
                       stream)
 
@@ -348,7 +349,8 @@ def _lm_stream(stream, dev):
 
 def adamw_step(plan, cfg, scale=1.0, stream=None):
     """rcc_adamw_step: one step over a plan's tensors, their gradients carrying
-    the loss scale `scale`.  cfg: adamw_cfg.  Nothing is read back."""
+    the loss scale `scale` (1 / scale a normal fp32 number).  cfg: adamw_cfg.
+    Nothing is read back."""
     if not isinstance(cfg, _rcc.AdamWCfg):
         raise ValueError("cfg must be one of adamw_cfg's")
     used = _lm.adamw_step(plan.handle, C.addressof(cfg), scale, plan.device, stream)
