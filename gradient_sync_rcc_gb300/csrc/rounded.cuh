@@ -28,15 +28,14 @@ __device__ __forceinline__ float inverse_of(float v) {
 // approximate inverse is put right by its remainder, which a fused operation gives
 // exactly (P. Markstein, IBM J. Res. Dev. 34, 1990).  The scaling keeps the remainders
 // of the smallest values out of the underflow.
-//   root2, 0 <= v <= kMost: the bits of __fsqrt_rn for every one of them, tried one by
-//   one.
-//   quotient2, 2^64 m / b for |m| <= kMost and 2^-30 <= b <= 2^24: r = 1 / b to the
-//   nearest (tried for every fraction of b), a quotient within one last place after
-//   the first remainder; Markstein's theorem has it that the second one makes it the
-//   nearest.
+//   root2, 0 <= v <= kMostSquare: the bits of __fsqrt_rn for every one of them, tried
+//   one by one.
+//   quotient2, 2^64 m / b for |m| <= kMost and kLeastBelow <= b <= 2^24: r = 1 / b to
+//   the nearest (tried for every b), a quotient within one last place after the first
+//   remainder; Markstein's theorem has it that the second one makes it the nearest.
 // An AdamW step of 544 M elements in 8-bit states: 1,754 us; 2,092 with __fsqrt_rn and
 // __fdiv_rn.
-constexpr float kMost = 0x1p30f;
+constexpr float kMostSquare = 0x1p30f, kMost = 0x1p10f, kLeastBelow = 0x1p-50f;
 __device__ __forceinline__ float2 root2(float2 v) {
   const float2 x = mul2(v, both(0x1p64f)), neg_x = mul2(v, both(-0x1p64f));
   const float2 y = make_float2(inverse_root_of(fmaxf(x.x, 0x1p-96f)),

@@ -74,12 +74,13 @@ def raw(v):
     return v.contiguous().view(torch.uint8)
 
 
-def follow(tensors, steps, limit, scale, seed=0x12345678, first=40):
+def follow(tensors, steps, limit, scale, seed=0x12345678, first=40, **more):
     """Steps of a plan and of the definition, side by side."""
     own = [dict(t) for t in adamw.clone(tensors)]
-    plan = rcc.AdamWPlan(tensors, seed=seed, step=first, betas=CFG["betas"])
-    powers = adamw.Powers(CFG["betas"], first)
-    cfg = rcc.adamw_cfg(max_grad_norm=limit, **CFG)
+    settings = CFG | more
+    plan = rcc.AdamWPlan(tensors, seed=seed, step=first, betas=settings["betas"])
+    powers = adamw.Powers(settings["betas"], first)
+    cfg = rcc.adamw_cfg(max_grad_norm=limit, **settings)
     for k in range(steps):
         rcc.adamw_step(plan, cfg, scale)
         r = rcc.adamw_report(plan)
@@ -88,7 +89,7 @@ def follow(tensors, steps, limit, scale, seed=0x12345678, first=40):
         now = powers.next()
         for i, t in enumerate(own):
             numbers = adamw.numbers_of(t["param"].numel(), i, seed, first + k)
-            step_of(t, adamw.groups(numbers).int(), CFG, scale, r.clip_coef, now)
+            step_of(t, adamw.groups(numbers).int(), settings, scale, r.clip_coef, now)
         for i, (got, want) in enumerate(zip(tensors, own)):
             for key, v in want.items():
                 wrong = raw(got[key]) != raw(v)
@@ -165,3 +166,17 @@ def test_bits_of_extreme_values():
     for i in range(40):
         t["grad"][128 * i:128 * (i + 1)] *= 2.0 ** (-140 + 6 * i)
     follow([t], 12, 0.0, 1.0)
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("more", [dict(eps=1e-15), dict(eps=1e-20), dict(eps=2.0), dict(lr=1e-25),
+                                  dict(lr=0.0), dict(betas=(0.0, 0.99999)), dict(betas=(0.9, 0.0)),
+                                  dict(weight_decay=0.0)])
+def test_bits_of_other_settings(offset, more):
+    """Denominators, step sizes and moments on both sides of the range that is taken two
+    at a time; first steps, where the corrections are largest."""
+    g = defs.gen(204)
+    tensors = [heavy(g, adamw.make(g, n, F32, True, True, offset=offset)) for n in (5000, 300, 4096)]
+    tensors[0]["grad"][1000:3000] *= 2.0 ** 12
+    tensors[0]["grad"][2000:4000:7] *= 2.0 ** 10
+    follow(tensors, 6, 0.0, 1.0, first=0, **more)

@@ -30,7 +30,7 @@ __device__ void count(unsigned long long* wrong, float got, float want) {
 }
 
 __global__ void roots(unsigned long long* wrong) {
-  const uint64_t most = __float_as_uint(kMost), step = 2ull * gridDim.x * blockDim.x;
+  const uint64_t most = __float_as_uint(kMostSquare), step = 2ull * gridDim.x * blockDim.x;
   for (uint64_t i = 2ull * (blockIdx.x * blockDim.x + threadIdx.x); i <= most; i += step) {
     const float2 v = make_float2(__uint_as_float((uint32_t)i), __uint_as_float((uint32_t)min(i + 1, most)));
     const float2 s = root2(v);
@@ -40,7 +40,7 @@ __global__ void roots(unsigned long long* wrong) {
 }
 __global__ void reciprocals(unsigned long long* wrong) {
   const uint32_t fraction = blockIdx.x * blockDim.x + threadIdx.x;   // of 2^23
-  for (int e = -30; e < 24; ++e) {
+  for (int e = -50; e < 24; ++e) {
     const float b = __uint_as_float((uint32_t)(127 + e) << 23 | fraction);
     const float2 q = quotient2(both(1.f), both(b));
     count(wrong, q.x * 0x1p-64f, __frcp_rn(b));
@@ -51,10 +51,11 @@ __global__ void quotients(unsigned long long* wrong, uint32_t seed, int each, fl
   for (int k = 0; k < each; ++k) {
     const uint32_t i = (blockIdx.x * blockDim.x + threadIdx.x) * each + k;
     const uint32_t h = stir(i ^ seed), l = stir(h + 0x9E3779B9u), b0 = stir(l ^ seed);
-    // |m| from 2^-90 to 2^30, every 16th zero; b from 2^-30 to 2^24
+    // |m| from 2^-76 to 2^10, every 16th zero; b from kLeastBelow = 2^-50 to 2^24: all
+    // quotients are normal numbers
     const float m = __uint_as_float((l & 0x80000000u) | (l & 0x7FFFFFu) |
-                                    (h % 16 ? (uint32_t)(37 + (h >> 4) % 120) << 23 : 0u));
-    const float b = __uint_as_float((uint32_t)(97 + (h >> 16) % 54) << 23 | (b0 & 0x7FFFFFu));
+                                    (h % 16 ? (uint32_t)(51 + (h >> 4) % 86) << 23 : 0u));
+    const float b = __uint_as_float((uint32_t)(77 + (h >> 16) % 74) << 23 | (b0 & 0x7FFFFFu));
     const float x = h % 16 ? m : copysignf(0.f, m);
     const float2 q = quotient2(make_float2(x, -x), both(b));
     count(wrong, q.x * 0x1p-64f, __fdiv_rn(x, b));
