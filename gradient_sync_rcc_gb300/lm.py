@@ -208,8 +208,8 @@ def rotary_forward(q, k, turns, positions=None, offset=0, layout="half", scale=1
                    k_out=None, stream=None):
     """rcc_rotary_forward: q and k [tokens, heads, head_dim] (k may be None),
     turned by their tokens' positions: positions + offset, or 0, 1, ... + offset.
-    Returns (q, k) turned.  Any strides that keep the heads apart (none of them 0), but
-    a head's elements lie side by side; q_out may be q itself."""
+    Returns (q, k) turned.  Any strides that keep the heads apart; a head's
+    elements lie side by side.  q_out may be q itself."""
     return _lm.rotary(False, q, k, turns, positions, offset, _layout(layout), scale, q_out, k_out,
                       stream)
 
